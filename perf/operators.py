@@ -106,7 +106,7 @@ def draw(rng):
                  gate=rng.choice(["none", "channel", "token"]))
         return c
     while True:
-        c = dict(op=op, T=_log(rng, 1, 4096), k=rng.randint(1, 8), d=_log(rng, 64, 8192, 8),
+        c = dict(op=op, T=_log(rng, 1, 4096), k=rng.randint(1, 8), d=_log(rng, 64, 8192, 64),
                  y=rng.choice(["bf16", "f32"]), out=rng.choice(["bf16", "f32"]))
         if c["T"] * c["k"] * c["d"] <= 1e8:
             return c
@@ -195,8 +195,8 @@ def prepare(case, seed):
                       dw_pre=new(s["w_pre"]), dgate=new(s["gate"]))
     else:
         T, k, d = c["T"], c["k"], c["d"]
-        _, _, inv = _route(g, T, k, max(64, k), True)
-        s |= dict(inv=inv, w=torch.softmax(normal(T, k, dt=torch.float32), 1),
+        _, _, inv = _route(g, T, k, 64, True)
+        s |= dict(shape=(d, 64, 64, k, 64, 0), inv=inv, w=torch.softmax(normal(T, k, dt=torch.float32), 1),
                   dout=normal(T, d, dt=DTYPES[c["out"]], scale=1e-2),
                   y=normal(T * k, d, dt=DTYPES[c["y"]]))
         s |= dict(dy=torch.empty_like(s["y"]), dw=torch.empty_like(s["w"]))
@@ -252,7 +252,7 @@ def _run_own(s, c):
                                 s["gate"], s["scale"], EPS, ws)
         return dict(dy=s["dy"], dres=s["dres"], dw_post=s["dw_post"], dw_pre=s["dw_pre"],
                     dgate=s["dgate"])
-    moe.moe_combine_grad(s["dout"], s["y"], s["inv"], s["w"], s["dy"], s["dw"])
+    moe.moe_combine_grad(s["shape"], s["dout"], s["y"], s["inv"], s["w"], s["dy"], s["dw"])
     return dict(dy=s["dy"], dw=s["dw"])
 
 
