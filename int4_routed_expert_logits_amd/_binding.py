@@ -32,7 +32,11 @@ EXPORTS = ("moe_expert_bytes", "moe_pack_experts", "moe_quantize", "moe_route_wo
            "moe_cache_create", "moe_cache_destroy", "moe_cache_pin",
            "moe_cache_plan", "moe_cache_stats", "moe_cache_last_fetch", "moe_cache_unplan_last",
            "moe_cache_workspace_bytes",
-           "moe_cache_layer_decode", "moe_status_str", "moe_measure_stream_read")
+           "moe_cache_layer_decode", "moe_status_str", "moe_measure_stream_read",
+           "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
+           "moe_grouped_mm_dw_workspace_bytes", "moe_blockscale_quantize", "moe_blockscale_mm",
+           "moe_swiglu", "moe_swiglu_quantize", "moe_swiglu_grad", "moe_combine_grad",
+           "moe_block_norm", "moe_block_norm_grad", "moe_block_norm_grad_workspace_bytes")
 
 
 class Shape(ctypes.Structure):
@@ -126,6 +130,26 @@ def load():
     lib.moe_quantize.argtypes = [c_int32, c_int32, c_void_p, c_int32, c_int32, c_void_p, c_void_p,
                                  c_void_p]
     lib.moe_quantize.restype = c_int32
+    i32, f32, sz = c_int32, ctypes.c_float, c_size_t
+    for name, args, res in (
+            ("moe_grouped_mm", [i32] * 4 + [vp, i32, vp, i32, vp, vp, vp, i32, vp], i32),
+            ("moe_grouped_mm_dx", [i32] * 4 + [vp, vp, vp, vp, i32, vp], i32),
+            ("moe_grouped_mm_dw_workspace_bytes", [i32] * 4, sz),
+            ("moe_grouped_mm_dw", [i32] * 4 + [vp, vp, i32, vp, i32, vp, vp, i32, vp, sz, vp], i32),
+            ("moe_blockscale_quantize", [i32] * 3 + [vp, i32, i32, vp, vp, vp], i32),
+            ("moe_blockscale_mm",
+             [i32] * 4 + [vp, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp], i32),
+            ("moe_swiglu", [i32, i32, vp, vp, i32, vp, vp], i32),
+            ("moe_swiglu_quantize", [i32, i32, vp, i32, vp, vp, vp, vp], i32),
+            ("moe_swiglu_grad", [i32, i32, vp, vp, vp, i32, vp, vp], i32),
+            ("moe_combine_grad", [sp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp], i32),
+            ("moe_block_norm", [i32, i32, vp, i32, vp, vp, i32, f32, vp, i32, vp, vp, f32, vp, i32,
+                                vp], i32),
+            ("moe_block_norm_grad_workspace_bytes", [i32, i32], sz),
+            ("moe_block_norm_grad", [i32, i32, vp, i32, vp, vp, i32, f32, vp, i32, vp, f32, vp, vp,
+                                     i32, vp, vp, vp, vp, vp, vp, sz, vp], i32)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, res
     lib.moe_status_str.argtypes = [c_int32]
     lib.moe_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -379,3 +403,253 @@ def moe_cache_layer_decode(cache: int, x, w_router, bias, shared, topk_idx, topk
         _ptr(topk_idx), _ptr(topk_w), _ptr(y), _ptr(y_shared), _ptr(out), _dtype(out),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream),
         _stream(copy_stream) if copy_stream is not None else _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# float and 8-bit expert weights, gradients, block norms
+# (include/moe_int4_block.h)
+#
+# These take whole tensors and check them first: each on the GPU of the first
+# one, without gaps, of the named type and shape (TypeError, ValueError); the
+# sizes' limits are the library's (MoeError).  A call runs on the tensors'
+# GPU, on `stream` or on that GPU's current stream.
+# ----------------------------------------------------------------------------
+
+def _take(fn: str, device, name: str, t, dtypes, shape):
+    """t's address, after checking it (None passes as NULL)."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise TypeError(f"{fn}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on the GPU of the first tensor ({device})")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not contiguous")
+    return t.data_ptr()
+
+
+def _dim(fn: str, name: str, t, n: int):
+    if t.dim() != n:
+        raise ValueError(f"{fn}: {name} has {t.dim()} dimensions, not {n}")
+    return t.shape
+
+
+def _workspace(fn: str, device, t):
+    """(address, bytes) of a workspace tensor of any type; (NULL, 0) for None."""
+    if t is None:
+        return None, 0
+    return _take(fn, device, "workspace", t, (t.dtype,), t.shape), t.numel() * t.element_size()
+
+
+def _run(fn: str, device, stream, *args):
+    """One C call with the tensors' GPU current, on `stream` or its current stream."""
+    import torch
+    call = getattr(load(), fn)
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(fn, call(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn, call(*args, stream))
+
+
+def _types():
+    import torch
+    return torch.bfloat16, torch.float32, (torch.bfloat16, torch.float32), torch.int32, (
+        torch.float8_e4m3fn, torch.uint8)
+
+
+def _rows_args(fn, device, P, rows):
+    import torch
+    return _take(fn, device, "rows", rows, (torch.int32,), (P,))
+
+
+def moe_grouped_mm(x, w, offsets, y, rows=None, rows_div: int = 1, stream=None):
+    """y[p] = w[e] x[rows[p] // rows_div] (x[p] without rows): x [X, K] bf16,
+    w [E, N, K] bf16, offsets [E + 1] and rows [P] int32, y [P, N] bf16/f32."""
+    fn, dev = "moe_grouped_mm", x.device
+    bf16, _, floats, i32, _ = _types()
+    E, N, K = _dim(fn, "w", w, 3)
+    P, X = _dim(fn, "y", y, 2)[0], _dim(fn, "x", x, 2)[0]
+    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "x", x, (bf16,), (X, K)), X,
+         _rows_args(fn, dev, P, rows), rows_div, _take(fn, dev, "w", w, (bf16,), (E, N, K)),
+         _take(fn, dev, "offsets", offsets, (i32,), (E + 1,)),
+         _take(fn, dev, "y", y, floats, (P, N)), _dtype(y))
+
+
+def moe_grouped_mm_dx(dy, w, offsets, dx, stream=None):
+    """dx[p] = w[e]^T dy[p]: dy [P, N] bf16, w [E, N, K] bf16, dx [P, K] bf16/f32."""
+    fn, dev = "moe_grouped_mm_dx", dy.device
+    bf16, _, floats, i32, _ = _types()
+    E, N, K = _dim(fn, "w", w, 3)
+    P = _dim(fn, "dx", dx, 2)[0]
+    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "dy", dy, (bf16,), (P, N)),
+         _take(fn, dev, "w", w, (bf16,), (E, N, K)),
+         _take(fn, dev, "offsets", offsets, (i32,), (E + 1,)),
+         _take(fn, dev, "dx", dx, floats, (P, K)), _dtype(dx))
+
+
+def moe_grouped_mm_dw_workspace_bytes(E: int, P: int, N: int, K: int) -> int:
+    return load().moe_grouped_mm_dw_workspace_bytes(E, P, N, K)
+
+
+def moe_grouped_mm_dw(dy, x, offsets, dw, workspace=None, rows=None, rows_div: int = 1,
+                      stream=None):
+    """dw[e] = sum over e's positions of dy[p] x[row(p)]^T: dy [P, N] and
+    x [X, K] bf16, dw [E, N, K] bf16/f32 (all of it written)."""
+    fn, dev = "moe_grouped_mm_dw", dy.device
+    bf16, _, floats, i32, _ = _types()
+    E, N, K = _dim(fn, "dw", dw, 3)
+    P, X = _dim(fn, "dy", dy, 2)[0], _dim(fn, "x", x, 2)[0]
+    ws, nws = _workspace(fn, dev, workspace)
+    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "dy", dy, (bf16,), (P, N)),
+         _take(fn, dev, "x", x, (bf16,), (X, K)), X, _rows_args(fn, dev, P, rows), rows_div,
+         _take(fn, dev, "offsets", offsets, (i32,), (E + 1,)),
+         _take(fn, dev, "dw", dw, floats, (E, N, K)), _dtype(dw), ws, nws)
+
+
+def moe_blockscale_quantize(x, block_rows: int, codes, scales, stream=None):
+    """x [R, K] or [n, R, K] bf16/f32 -> e4m3 codes of x's shape
+    (float8_e4m3fn or uint8) and float32 scales per 128 columns: [.., R, K/128]
+    for block_rows 1, [.., R/128, K/128] for 128 (rounded up)."""
+    fn, dev = "moe_blockscale_quantize", x.device
+    _, f32, floats, _, codes_t = _types()
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{fn}: x has {x.dim()} dimensions, not 2 or 3")
+    *lead, R, K = x.shape
+    sr = R if block_rows == 1 else -(-R // 128)
+    _run(fn, dev, stream, lead[0] if lead else 1, R, K, _take(fn, dev, "x", x, floats, x.shape),
+         _dtype(x), block_rows, _take(fn, dev, "codes", codes, codes_t, x.shape),
+         _take(fn, dev, "scales", scales, (f32,), (*lead, sr, -(-K // 128))))
+
+
+def moe_blockscale_mm(xq, xs, wq, ws, offsets, y, rows=None, rows_div: int = 1, stream=None):
+    """moe_grouped_mm over e4m3 codes: xq [X, K] with xs [X, K/128], wq
+    [E, N, K] with ws [E, N/128, K/128] (rounded up), y [P, N] bf16/f32."""
+    fn, dev = "moe_blockscale_mm", xq.device
+    _, f32, floats, i32, codes_t = _types()
+    E, N, K = _dim(fn, "wq", wq, 3)
+    P, X, kb = _dim(fn, "y", y, 2)[0], _dim(fn, "xq", xq, 2)[0], -(-K // 128)
+    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "xq", xq, codes_t, (X, K)),
+         _take(fn, dev, "xs", xs, (f32,), (X, kb)), X, _rows_args(fn, dev, P, rows), rows_div,
+         _take(fn, dev, "wq", wq, codes_t, (E, N, K)),
+         _take(fn, dev, "ws", ws, (f32,), (E, -(-N // 128), kb)),
+         _take(fn, dev, "offsets", offsets, (i32,), (E + 1,)),
+         _take(fn, dev, "y", y, floats, (P, N)), _dtype(y))
+
+
+def _n_rows(fn, dev, n_rows):
+    import torch
+    return _take(fn, dev, "n_rows", n_rows, (torch.int32,), (1,))
+
+
+def moe_swiglu(gu, h, n_rows=None, stream=None):
+    """h = silu(gu[:, :f]) * gu[:, f:]: gu [P, 2 f], h [P, f], both bf16 or both
+    f32; n_rows: device int32 [1], rows from it on are left as they were."""
+    fn, dev = "moe_swiglu", gu.device
+    P, f = _dim(fn, "h", h, 2)
+    _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, _types()[2], (P, 2 * f)),
+         _take(fn, dev, "h", h, (gu.dtype,), (P, f)), _dtype(gu), _n_rows(fn, dev, n_rows))
+
+
+def moe_swiglu_quantize(gu, codes, scales, n_rows=None, stream=None):
+    """moe_swiglu's result as e4m3 codes [P, f] and scales [P, f/128] (rounded up)."""
+    fn, dev = "moe_swiglu_quantize", gu.device
+    _, f32, floats, _, codes_t = _types()
+    P, f = _dim(fn, "codes", codes, 2)
+    _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, floats, (P, 2 * f)), _dtype(gu),
+         _take(fn, dev, "codes", codes, codes_t, (P, f)),
+         _take(fn, dev, "scales", scales, (f32,), (P, -(-f // 128))), _n_rows(fn, dev, n_rows))
+
+
+def moe_swiglu_grad(gu, dh, dgu, n_rows=None, stream=None):
+    """moe_swiglu's gradient: gu, dgu [P, 2 f], dh [P, f], one type; dgu may be gu."""
+    fn, dev = "moe_swiglu_grad", gu.device
+    P, f = _dim(fn, "dh", dh, 2)
+    _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, _types()[2], (P, 2 * f)),
+         _take(fn, dev, "dh", dh, (gu.dtype,), (P, f)),
+         _take(fn, dev, "dgu", dgu, (gu.dtype,), (P, 2 * f)), _dtype(gu), _n_rows(fn, dev, n_rows))
+
+
+def moe_combine_grad(shape, dout, y, inv_perm, topk_w, dy, dtopk_w, stream=None):
+    """moe_combine's gradient: dout [T, d], y and dy [T * k, d] (bf16/f32, one
+    type; dy may be y), inv_perm [T * k] int32, topk_w and dtopk_w [T, k] f32."""
+    fn, dev = "moe_combine_grad", dout.device
+    _, f32, floats, i32, _ = _types()
+    sh = _shape(shape)
+    T, n = _dim(fn, "dout", dout, 2)[0], dout.shape[0] * sh.top_k
+    _run(fn, dev, stream, ctypes.byref(sh), T,
+         _take(fn, dev, "dout", dout, floats, (T, sh.d)), _dtype(dout),
+         _take(fn, dev, "y", y, floats, (n, sh.d)), _dtype(y),
+         _take(fn, dev, "inv_perm", inv_perm, (i32,), (n,)),
+         _take(fn, dev, "topk_w", topk_w, (f32,), (T, sh.top_k)),
+         _take(fn, dev, "dy", dy, (y.dtype,), (n, sh.d)),
+         _take(fn, dev, "dtopk_w", dtopk_w, (f32,), (T, sh.top_k)))
+
+
+def _norm_args(fn, y, res, w_post, w_pre, gate, scale):
+    """The first arguments of the block norm calls and the sizes they check by."""
+    bf16, f32, floats, _, _ = _types()
+    first = y if y is not None else res
+    if first is None:
+        raise ValueError(f"{fn}: neither y nor res")
+    dev, (T, d) = first.device, _dim(fn, "y" if y is not None else "res", first, 2)
+    ydt = bf16 if y is None else y.dtype
+    rdt = ydt if res is None else res.dtype
+    g = 0 if gate is None else _dim(fn, "gate", gate, 2)[0]
+    head = (T, d, _take(fn, dev, "y", y, floats, (T, d)), MOE_BF16 if ydt == bf16 else MOE_F32,
+            _take(fn, dev, "w_post", w_post, (f32,), (d,)),
+            _take(fn, dev, "gate", gate, (ydt,), (g, d)), g, scale,
+            _take(fn, dev, "res", res, (rdt,) if rdt in floats else floats, (T, d)))
+    return dev, T, d, ydt, rdt, head, _take(fn, dev, "w_pre", w_pre, (f32,), (d,))
+
+
+def moe_block_norm(y, res, res_out, normed, w_post=None, w_pre=None, gate=None, scale=1.0,
+                   eps=1e-6, stream=None):
+    """r = res + scale * gate * norm(y) * w_post -> res_out, norm(r) * w_pre ->
+    normed: y, res, res_out, normed [T, d] bf16/f32 (res_out of res's type, or
+    y's without res), w_post, w_pre [d] f32, gate [1 or T, d] of y's type.  Any
+    of y, res, res_out, w_post, gate and (w_pre with normed) may be None."""
+    fn = "moe_block_norm"
+    _, _, floats, _, _ = _types()
+    dev, T, d, _, rdt, head, w2 = _norm_args(fn, y, res, w_post, w_pre, gate, scale)
+    if res is None and res_out is not None:
+        rdt = res_out.dtype
+    _run(fn, dev, stream, *head, _code(rdt), _take(fn, dev, "res_out", res_out, (rdt,), (T, d)),
+         w2, eps, _take(fn, dev, "normed", normed, floats, (T, d)),
+         MOE_F32 if normed is None else _dtype(normed))
+
+
+def _code(dtype) -> int:
+    import torch
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dtype}")
+    return MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+
+
+def moe_block_norm_grad_workspace_bytes(T: int, d: int) -> int:
+    return load().moe_block_norm_grad_workspace_bytes(T, d)
+
+
+def moe_block_norm_grad(y, res, dr, dn, dy, dres, dw_post, dw_pre, dgate, w_post=None, w_pre=None,
+                        gate=None, scale=1.0, eps=1e-6, workspace=None, stream=None):
+    """moe_block_norm's gradient at the same inputs, given dr (of res_out, of
+    its type; or None) and dn (of normed): dy, dres [T, d], dw_post, dw_pre [d],
+    dgate of gate's shape, each None where not wanted."""
+    fn = "moe_block_norm_grad"
+    _, f32, floats, _, _ = _types()
+    dev, T, d, ydt, rdt, head, w2 = _norm_args(fn, y, res, w_post, w_pre, gate, scale)
+    if res is None:
+        rdt = dr.dtype if dr is not None else dres.dtype if dres is not None else rdt
+    ws, nws = _workspace(fn, dev, workspace)
+    _run(fn, dev, stream, *head, _code(rdt), w2, eps, _take(fn, dev, "dr", dr, (rdt,), (T, d)),
+         _take(fn, dev, "dn", dn, floats, (T, d)), MOE_F32 if dn is None else _dtype(dn),
+         _take(fn, dev, "dy", dy, (ydt,), (T, d)), _take(fn, dev, "dres", dres, (rdt,), (T, d)),
+         _take(fn, dev, "dgate", dgate, (ydt,), (head[6], d)),
+         _take(fn, dev, "dw_post", dw_post, (f32,), (d,)),
+         _take(fn, dev, "dw_pre", dw_pre, (f32,), (d,)), ws, nws)

@@ -11,11 +11,15 @@
 
 namespace {
 
+using moe::aligned;
+using moe::hip_status;
+using moe::kWorkspaceAlign;
+using moe::round_up;
+
 constexpr int kMaxDim = 8192;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 constexpr int64_t kMaxSlots = int64_t(1) << 24;  // T * top_k
-constexpr size_t kWorkspaceAlign = 256;
 // moe_layer_decode: batches of at most this many tokens let every gate/up
 // workgroup derive the top-k and the grouping itself (a launch fewer); larger
 // ones group once.  Measured on the d=6144, f=2048 layer (HIP graphs): 1
@@ -23,10 +27,6 @@ constexpr size_t kWorkspaceAlign = 256;
 // 330 us against 240 us.
 constexpr int kLayerDecodePrologueMaxT = 1;
 constexpr int kMaxQuantK = 65536;
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-size_t round_up(size_t n) { return (n + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; }
 
 // group 64: int4 codes with a float16 scale per 64 elements; group 32:
 // MXFP4 (E2M1 codes with an E8M0 scale per 32 elements), which only the
@@ -59,15 +59,18 @@ moe_status check_tokens(const moe_shape* s, int32_t T) {
 // The workspace sizes are 0 for a token count the calls reject.
 bool shape_tokens_ok(const moe_shape* s, int32_t T) { return check_tokens(s, T) == MOE_OK; }
 
-moe_status hip_status(hipError_t e) {
-  if (e == hipSuccess) return MOE_OK;
-  if (e == hipErrorNotSupported) return MOE_ERR_UNSUPPORTED;
-  return MOE_ERR_HIP;
-}
-
 }  // namespace
 
 namespace moe {
+
+moe_status combine_check(const moe_shape* shape, int32_t T, moe_dtype y_dt, moe_dtype out_dt) {
+  moe_status st = check_shape(shape, true);
+  if (st != MOE_OK) return st;
+  if ((st = check_tokens(shape, T)) != MOE_OK) return st;
+  if ((y_dt != MOE_F32 && y_dt != MOE_BF16) || (out_dt != MOE_F32 && out_dt != MOE_BF16))
+    return MOE_ERR_DTYPE;
+  return MOE_OK;
+}
 
 // Every argument check of moe_layer_decode except the workspace's.
 moe_status layer_decode_check(const moe_shape* shape, int32_t T, const void* x, moe_dtype x_dt,
@@ -290,12 +293,8 @@ moe_status moe_expert_ffn(const moe_shape* shape, int32_t T, const void* x, moe_
 moe_status moe_combine(const moe_shape* shape, int32_t T, const void* y, const void* y_shared,
                        moe_dtype y_dt, const int32_t* inv_perm, const float* topk_w, void* out,
                        moe_dtype out_dt, void* stream) {
-  moe_status st = check_shape(shape, true);
-  if (st != MOE_OK) return st;
-  if ((st = check_tokens(shape, T)) != MOE_OK) return st;
-  if ((y_dt != MOE_F32 && y_dt != MOE_BF16) || (out_dt != MOE_F32 && out_dt != MOE_BF16))
-    return MOE_ERR_DTYPE;
-  if (T == 0) return MOE_OK;
+  const moe_status st = moe::combine_check(shape, T, y_dt, out_dt);
+  if (st != MOE_OK || T == 0) return st;
   if (!y || !inv_perm || !topk_w || !out) return MOE_ERR_NULL;
   if ((shape->f_shared != 0) != (y_shared != nullptr)) return MOE_ERR_NULL;
   if (!aligned(y, 16) || (y_shared && !aligned(y_shared, 16)) || !aligned(out, 16) ||

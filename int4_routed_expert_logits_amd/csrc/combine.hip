@@ -52,6 +52,23 @@ __device__ __forceinline__ void load_row8(const void* base, size_t i, float (&v)
   }
 }
 
+template <bool BF16>
+__device__ __forceinline__ void store_row8(void* base, size_t i, const float (&v)[8]) {
+  if constexpr (BF16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = static_cast<uint32_t>(f32_to_bf16(v[2 * j])) |
+             (static_cast<uint32_t>(f32_to_bf16(v[2 * j + 1])) << 16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    float* o = static_cast<float*>(base) + i;
+    *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // All k row indices and weights of a token are loaded before any y row, and
 // the y rows of 8 slots are in flight together; empty slots (inv_perm < 0)
 // leave the sum untouched.
@@ -116,7 +133,58 @@ __global__ __launch_bounds__(64) void combine_kernel(const void* __restrict__ y,
   }
 }
 
+// Gradient of the combine: one wavefront per routing slot s = t * k + j reads
+// dout[t] and the slot's row of y once,
+//   dy[inv_perm[s]] = topk_w[s] * dout[t],  dtopk_w[s] = <y[inv_perm[s]], dout[t]>
+// in float32, the dot product by lane and then over the lanes in a fixed
+// order.  A slot without a row (inv_perm outside [0, T k)) has dtopk_w 0 and no
+// row of dy to write.
+template <bool YBF16, bool OBF16>
+__global__ __launch_bounds__(256) void combine_grad_kernel(const void* dout, const void* y,
+                                                           const int32_t* inv_perm,
+                                                           const float* topk_w, void* dy,
+                                                           float* dtopk_w, int slots, int d,
+                                                           int k) {
+  constexpr int V = 8;
+  const int lane = threadIdx.x % kWave;
+  const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
+  if (s >= slots) return;
+  const int p = inv_perm[s];
+  float dot = 0.0f;
+  if (p >= 0 && p < slots) {
+    const float w = topk_w[s];
+    const size_t src = static_cast<size_t>(s / k) * d, dst = static_cast<size_t>(p) * d;
+    for (int c = lane * V; c < d; c += kWave * V) {
+      float o[V], v[V];
+      load_row8<OBF16>(dout, src + c, o);
+      load_row8<YBF16>(y, dst + c, v);
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        dot = fmaf(v[q], o[q], dot);
+        o[q] *= w;
+      }
+      store_row8<YBF16>(dy, dst + c, o);
+    }
+  }
+  dot = group_sum(dot, kWave);
+  if (lane == 0) dtopk_w[s] = dot;
+}
+
 }  // namespace
+
+hipError_t launch_combine_grad(int T, int d, int k, const void* dout, bool out_bf16,
+                               const void* y, bool y_bf16, const int32_t* inv_perm,
+                               const float* topk_w, void* dy, float* dtopk_w, hipStream_t stream) {
+  const int slots = T * k, per = 256 / kWave;
+  const dim3 block(256), grid((slots + per - 1) / per);
+  auto go = [&](auto kernel) {
+    return launch(kernel, grid, block, 0, stream, dout, y, inv_perm, topk_w, dy, dtopk_w, slots, d,
+                  k);
+  };
+  if (y_bf16)
+    return out_bf16 ? go(combine_grad_kernel<true, true>) : go(combine_grad_kernel<true, false>);
+  return out_bf16 ? go(combine_grad_kernel<false, true>) : go(combine_grad_kernel<false, false>);
+}
 
 hipError_t launch_combine(int T, int d, int k, const void* y, const void* y_shared, bool y_bf16,
                           const int32_t* inv_perm, const float* topk_w, void* out,

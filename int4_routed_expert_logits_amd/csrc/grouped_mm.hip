@@ -1,0 +1,491 @@
+// Matrix products over rows grouped by expert, on the bf16 matrix cores:
+//   rows     y[p]  = W_e x[row(p)]                 p in [offsets[e], offsets[e+1])
+//   input    dx[p] = W_e^T dy[p]
+//   weights  dW_e  = sum over the group's p of dy[p] x[row(p)]^T
+// and the first of them over e4m3 codes with a float32 scale per 128 columns
+// of a row and per 128 x 128 weights.
+//
+// All four are one loop: D[m][n] = sum_k R[m][k] F[n][k] over a 256-column
+// tile of one group, R being the operand whose index is the output's row and
+// F the one whose index is its column.  A stage of the loop is 128 bytes of
+// the contraction (64 bf16, 128 codes) of every row of R and F in LDS,
+// fetched by global_load_lds.  An operand that is contiguous along the
+// contraction is stored [row][128 bytes]; one that is contiguous along its
+// own index (W of `input`, both operands of `weights`) is stored
+// [64 of the contraction][its columns] and read with the transposing
+// ds_read_b64_tr_b16, so no operand is ever transposed in memory.
+// Chunks past an operand's end are fetched from a zero block, so no tail of
+// K, N or a group's rows needs a branch in the arithmetic, and both operands
+// are zero there (no 0 * inf).  F goes to the matrix instruction's A side:
+// a lane then holds four consecutive columns of one output row.
+#include <type_traits>
+
+#include "common.h"
+#include "launch.h"
+
+namespace moe {
+
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+
+constexpr int kThreads = 512;  // 8 wavefronts
+constexpr int kWaves = kThreads / kWave;
+constexpr int kStageBytes = 128;  // bytes of the contraction per stage and row
+constexpr int kBN = 256;          // output columns per tile
+constexpr int kBlock = 128;       // columns (and weight rows) per scale
+
+// What a fetch past an operand's end reads.
+__device__ const uint4 g_zero[8] = {};
+
+// kCodesF32: the codes multiplied as bf16, for float32 results.
+enum Kind { kRows, kInput, kWeights, kCodes, kCodesF32 };
+
+// LDS byte address of a pointer into a __shared__ array.
+__device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8*)p));
+}
+
+// One LDS DMA instruction: every lane's 16 (or 4) bytes at g go to LDS at
+// m0 + 16 (or 4) * lane.  Asm, as the compiler would wait for all of them
+// before each LDS read; the loop waits for a stage's fetches itself.  No
+// register outputs.
+__device__ __forceinline__ void dma16(const uint8_t* g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const uint8_t* g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds)
+               : "memory", "m0");
+}
+
+// This wavefront's fetches but the newest N done and its LDS reads back, then
+// every wavefront of the workgroup here.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
+}
+
+__device__ __forceinline__ const uint8_t* zero_block() {
+  return reinterpret_cast<const uint8_t*>(g_zero);
+}
+
+// n / div for 0 <= n < 2^24 and div <= 256; magic = ceil(2^32 / div), 0 for 1.
+__device__ __forceinline__ uint32_t row_div(uint32_t n, uint32_t magic) {
+  return magic ? __umulhi(n, magic) : n;
+}
+
+// Eight e4m3 codes as bf16, exactly.
+__device__ __forceinline__ bf16x8_t codes_to_bf16(uint32_t lo, uint32_t hi) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+struct Group {
+  int e, a, b;  // expert, its grouped positions
+  int t;        // this workgroup's tile of the group
+};
+
+// The group's bounds as the kernels take them: whatever offsets holds, they
+// lie in [0, P].
+__device__ __forceinline__ void group_bounds(const GroupedMm& g, int e, int& a, int& b) {
+  a = min(max(g.offsets[e], 0), g.P);
+  b = min(max(g.offsets[e + 1], a), g.P);
+}
+
+// Which group holds row tile `tile` (groups in ascending order, ceil(rows /
+// BM) tiles each): every thread takes two groups, a scan over the workgroup
+// gives their first tiles, and the owner tells the others.  e = -1 past the
+// last tile.
+template <int BM>
+__device__ Group find_group(const GroupedMm& g, int tile, int* sh) {
+  const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave;
+  int a[2] = {0, 0}, b[2] = {0, 0}, n[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (2 * t + i < g.E) {
+      group_bounds(g, 2 * t + i, a[i], b[i]);
+      n[i] = (b[i] - a[i] + BM - 1) / BM;
+    }
+  int inc = n[0] + n[1];
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int v = __shfl_up(inc, off, kWave);
+    if (lane >= off) inc += v;
+  }
+  if (t == 0) sh[kWaves] = -1;
+  if (lane == kWave - 1) sh[wv] = inc;
+  __syncthreads();
+  int first = inc - n[0] - n[1];
+  for (int w = 0; w < wv; ++w) first += sh[w];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (tile >= first && tile < first + n[i]) {
+      sh[kWaves] = 2 * t + i;
+      sh[kWaves + 1] = a[i];
+      sh[kWaves + 2] = b[i];
+      sh[kWaves + 3] = tile - first;
+    }
+    first += n[i];
+  }
+  __syncthreads();
+  Group r{sh[kWaves], sh[kWaves + 1], sh[kWaves + 2], sh[kWaves + 3]};
+  __syncthreads();
+  return r;
+}
+
+// Row of x (or of the codes) at grouped position p; -1 where it has none.
+__device__ __forceinline__ int64_t source_row(const GroupedMm& g, int p) {
+  if (!g.rows) return p;
+  const uint32_t s = static_cast<uint32_t>(g.rows[p]);
+  return s < g.row_limit ? static_cast<int64_t>(row_div(s, g.div_magic)) : -1;
+}
+
+// WM x WN wavefronts, each with RF x FF fragments of 16 x 16 outputs.
+template <int KIND, int WM_, int WN_, int RF_, int FF_, int NST_>
+struct Cfg {
+  static constexpr int K = KIND, WM = WM_, WN = WN_, RF = RF_, FF = FF_, NST = NST_;
+  static constexpr int BM = WM * RF * 16;
+  static constexpr bool RT = KIND == kWeights;                     // R contiguous along m
+  static constexpr bool FT = KIND == kInput || KIND == kWeights;   // F contiguous along n
+  static constexpr bool F8 = KIND == kCodes || KIND == kCodesF32;
+  static constexpr int RBytes = BM * kStageBytes, FBytes = kBN * kStageBytes;
+  static constexpr int SBytes = F8 ? kThreads * 4 : 0;  // a stage's row scales
+  static constexpr int Stage = RBytes + FBytes + SBytes;
+  static constexpr int RI = BM >= 64 ? BM / 64 : 1;  // R fetches per wavefront and stage
+  static constexpr int FI = 4;
+  static constexpr int Fetches = RI + FI + (F8 ? 1 : 0);
+  static_assert(WM * WN == kWaves && WN * FF * 16 == kBN, "tile");
+  static_assert(Stage * NST <= 160 * 1024 - 256, "LDS");
+};
+
+// Swizzle of the [row][128 bytes] layout: chunk c of row r is stored at
+// c ^ ((r >> 1) & 7), so the 16 rows a fragment read touches at once lie in
+// different banks.  The DMA writes LDS in lane order; the lanes pick their
+// sources accordingly.
+__device__ __forceinline__ int kc_slot(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+// ... of the [64][columns] layout: 32-byte segment s of row r is stored at
+// s ^ f(r), f from the three bits in which the eight rows that a transposing
+// read of half a wavefront touches differ.
+__device__ __forceinline__ int mn_swz(int row) { return (row & 3) | (((row >> 3) & 1) << 2); }
+
+// This lane's fetches of one operand, contiguous along the contraction.
+template <int NI>
+struct SrcK {
+  const uint8_t* p[NI];
+  int step[NI];   // bytes per stage: 128, or 0 for the zero block
+  int chunk[NI];  // byte offset of its chunk in a stage
+};
+template <int NI>
+__device__ __forceinline__ void issue_k(const SrcK<NI>& s, int stage, int red_bytes, uint32_t lds,
+                                        int first, int n_instr) {
+#pragma unroll
+  for (int j = 0; j < NI; ++j) {
+    const bool in = stage * kStageBytes + s.chunk[j] < red_bytes;
+    const uint8_t* p = in ? s.p[j] + static_cast<int64_t>(stage) * s.step[j] : zero_block();
+    dma16(p, lds + ((first + j) % n_instr) * 1024);
+  }
+}
+
+// One operand fragment: 16 rows x 64 contraction bytes (half `kk` of a
+// stage), 16 bytes per lane.
+__device__ __forceinline__ u32x4_t frag_k(const uint8_t* st, int row0, int kk, int lane) {
+  const int row = row0 + (lane & 15);
+  return *reinterpret_cast<const u32x4_t*>(st + row * kStageBytes +
+                                           (kc_slot(row, kk * 4 + (lane >> 4)) << 4));
+}
+// ... of the [64][width] layout: 16 columns x 32 of the contraction.  Two
+// transposing reads; in each, 16 lanes name four rows of 16 columns and get
+// four rows of their own column.
+template <int WIDTH>
+__device__ __forceinline__ u32x4_t frag_mn(const uint8_t* st, int col0, int kk, int lane) {
+  const int i = lane & 15, grp = lane >> 4;
+  const int row = kk * 32 + grp * 8 + (i >> 2);
+  const uint8_t* p = st + row * (WIDTH * 2) + (((col0 >> 4) ^ mn_swz(row)) << 5) + (i & 3) * 8;
+  const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * WIDTH * 2));
+  return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Output tile [m0, mend) x [n0, n0 + 256) of a group whose contraction is
+// [0, red) (kWeights: positions [ga, gb)).
+template <class C>
+__device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend, int n0, int ga,
+                     int gb) {
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int wv = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int wm = wv % C::WM, wn = wv / C::WM;
+  const int elem = C::F8 ? 1 : 2;
+  const int64_t wsz = static_cast<int64_t>(g.N) * g.K * elem;
+  const int red = C::K == kWeights ? gb - ga : C::K == kInput ? g.N : g.K;
+  const int red_bytes = C::RT ? 0 : red * elem;
+  const int stages = C::RT ? (red + 63) / 64 : (red_bytes + kStageBytes - 1) / kStageBytes;
+  const uint32_t lds0 = lds_addr(smem);
+
+  // ---- sources
+  SrcK<C::RI> rk;  // R along the contraction
+  SrcK<C::FI> fk;
+  const uint8_t* sp = zero_block();  // this lane's row scale
+  int sstep = 0;
+  if constexpr (!C::RT) {
+#pragma unroll
+    for (int j = 0; j < C::RI; ++j) {
+      const int row = ((wv * C::RI + j) * 8 + (lane >> 3)) % C::BM;
+      rk.chunk[j] = kc_slot(row, lane & 7) << 4;
+      int64_t src = -1;
+      if (m0 + row < mend)
+        src = C::K == kInput ? m0 + row : source_row(g, m0 + row);
+      rk.p[j] = src >= 0 ? g.r + src * red_bytes + rk.chunk[j] : zero_block();
+      rk.step[j] = src >= 0 ? kStageBytes : 0;
+    }
+    if constexpr (C::F8) {
+      const int row = t % C::BM;
+      const int64_t src = m0 + row < mend ? source_row(g, m0 + row) : -1;
+      if (src >= 0) {
+        sp = reinterpret_cast<const uint8_t*>(g.r_scale + src * stages);
+        sstep = 4;
+      }
+    }
+  }
+  if constexpr (!C::FT) {
+#pragma unroll
+    for (int j = 0; j < C::FI; ++j) {
+      const int row = (wv * C::FI + j) * 8 + (lane >> 3);
+      fk.chunk[j] = kc_slot(row, lane & 7) << 4;
+      const bool in = n0 + row < g.N;
+      fk.p[j] = in ? g.f + e * wsz + static_cast<int64_t>(n0 + row) * red_bytes + fk.chunk[j]
+                   : zero_block();
+      fk.step[j] = in ? kStageBytes : 0;
+    }
+  }
+  // an operand contiguous along its own index: chunk (lane) of row (instr)
+  auto issue_mn = [&](auto is_r, int stage, uint32_t lds) {
+    constexpr bool R = decltype(is_r)::value;
+    constexpr int W = R ? C::BM : kBN, NI = R ? C::RI : C::FI;
+    constexpr int LPR = W / 8;             // lanes per row of W columns
+    constexpr int RPI = kWave / LPR;       // rows per instruction
+    static_assert(LPR <= kWave && W >= 128, "row");  // the swizzle moves 8 segments
+    const int64_t ld = static_cast<int64_t>(R ? g.N : g.K) * 2;
+    const int width = R ? g.N : g.K, c0 = R ? m0 : n0;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int row = (wv * NI + j) * RPI + lane / LPR;
+      const int sw = lane % LPR;
+      const int col = c0 + ((((sw >> 1) ^ mn_swz(row)) << 1) | (sw & 1)) * 8;
+      const int k = stage * 64 + row;
+      const uint8_t* p = zero_block();
+      if (k < red && col < width) {
+        if constexpr (C::K == kInput) {
+          p = g.f + e * wsz + k * ld + col * 2;
+        } else {
+          const int64_t src = R ? ga + k : source_row(g, ga + k);
+          if (src >= 0) p = (R ? g.r : g.f) + src * ld + col * 2;
+        }
+      }
+      dma16(p, lds + (wv * NI + j) * 1024);
+    }
+  };
+  auto issue = [&](int stage, int buf) {
+    const uint32_t lds = lds0 + buf * C::Stage;
+    if constexpr (C::RT)
+      issue_mn(std::true_type{}, stage, lds);
+    else
+      issue_k<C::RI>(rk, stage, red_bytes, lds, wv * C::RI, C::BM / 8);
+    if constexpr (C::FT)
+      issue_mn(std::false_type{}, stage, lds + C::RBytes);
+    else
+      issue_k<C::FI>(fk, stage, red_bytes, lds + C::RBytes, wv * C::FI, kBN / 8);
+    if constexpr (C::F8)
+      dma4(stage < stages ? sp + stage * sstep : zero_block(),
+           lds + C::RBytes + C::FBytes + wv * 256);
+  };
+
+  f32x4_t acc[C::RF][C::FF];
+#pragma unroll
+  for (int i = 0; i < C::RF; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FF; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int mw = wm * C::RF * 16, nw = wn * C::FF * 16;
+  const float* fsc = nullptr;
+  if constexpr (C::F8)
+    fsc = g.f_scale + (static_cast<int64_t>(e) * ((g.N + kBlock - 1) / kBlock) +
+                       min(n0 + nw, g.N - 1) / kBlock) * stages;
+
+  auto math = [&](int stage, const uint8_t* st) {
+    const uint8_t *sr = st, *sf = st + C::RBytes;
+    if constexpr (C::K == kCodesF32) {
+      const float ws = fsc[stage];
+      const float* rs = reinterpret_cast<const float*>(sf + C::FBytes);
+      bf16x8_t fa[C::FF][4];  // 16 codes of each half of the stage
+#pragma unroll
+      for (int j = 0; j < C::FF; ++j)
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          const u32x4_t v = frag_k(sf, nw + j * 16, kk, lane);
+          fa[j][2 * kk] = codes_to_bf16(v[0], v[1]);
+          fa[j][2 * kk + 1] = codes_to_bf16(v[2], v[3]);
+        }
+#pragma unroll
+      for (int i = 0; i < C::RF; ++i) {
+        bf16x8_t rb[4];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          const u32x4_t v = frag_k(sr, mw + i * 16, kk, lane);
+          rb[2 * kk] = codes_to_bf16(v[0], v[1]);
+          rb[2 * kk + 1] = codes_to_bf16(v[2], v[3]);
+        }
+        const float s = rs[mw + i * 16 + (lane & 15)] * ws;
+#pragma unroll
+        for (int j = 0; j < C::FF; ++j) {
+          f32x4_t p{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[j][h], rb[h], p, 0, 0, 0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, p[q], acc[i][j][q]);
+        }
+      }
+    } else if constexpr (C::F8) {
+      const float ws = fsc[stage];
+      const float* rs = reinterpret_cast<const float*>(sf + C::FBytes);
+      i32x8_t fa[C::FF];
+#pragma unroll
+      for (int j = 0; j < C::FF; ++j) {
+        const u32x4_t lo = frag_k(sf, nw + j * 16, 0, lane), hi = frag_k(sf, nw + j * 16, 1, lane);
+        fa[j] = __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+#pragma unroll
+      for (int i = 0; i < C::RF; ++i) {
+        const u32x4_t lo = frag_k(sr, mw + i * 16, 0, lane), hi = frag_k(sr, mw + i * 16, 1, lane);
+        const i32x8_t rb =
+            __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        const float s = rs[mw + i * 16 + (lane & 15)] * ws;
+#pragma unroll
+        for (int j = 0; j < C::FF; ++j) {
+          const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              fa[j], rb, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, p[q], acc[i][j][q]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        bf16x8_t fa[C::FF];
+#pragma unroll
+        for (int j = 0; j < C::FF; ++j) {
+          if constexpr (C::FT)
+            fa[j] = __builtin_bit_cast(bf16x8_t, frag_mn<kBN>(sf, nw + j * 16, kk, lane));
+          else
+            fa[j] = __builtin_bit_cast(bf16x8_t, frag_k(sf, nw + j * 16, kk, lane));
+        }
+#pragma unroll
+        for (int i = 0; i < C::RF; ++i) {
+          bf16x8_t rb;
+          if constexpr (C::RT)
+            rb = __builtin_bit_cast(bf16x8_t, frag_mn<C::BM>(sr, mw + i * 16, kk, lane));
+          else
+            rb = __builtin_bit_cast(bf16x8_t, frag_k(sr, mw + i * 16, kk, lane));
+#pragma unroll
+          for (int j = 0; j < C::FF; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[j], rb, acc[i][j], 0, 0, 0);
+        }
+      }
+    }
+  };
+
+  // ---- the loop: NST - 1 stages in flight; one meeting per stage, after
+  // which the buffer of the stage before is free
+#pragma unroll
+  for (int s = 0; s < C::NST - 1; ++s) issue(s, s);
+  int buf = 0;
+  for (int s = 0; s < stages; ++s) {
+    wait_and_meet<(C::NST - 2) * C::Fetches>();
+    issue(s + C::NST - 1, buf == 0 ? C::NST - 1 : buf - 1);
+    math(s, smem + buf * C::Stage);
+    buf = buf == C::NST - 1 ? 0 : buf + 1;
+  }
+  wait_and_meet<0>();  // no fetch into LDS outlives the tile
+
+  // ---- store: lane holds columns n .. n + 3 of row m
+  const int cols = C::FT ? g.K : g.N;
+#pragma unroll
+  for (int i = 0; i < C::RF; ++i) {
+    const int m = m0 + mw + i * 16 + (lane & 15);
+    if (m >= mend) continue;
+    const int64_t row = C::K == kWeights ? static_cast<int64_t>(e) * g.N + m : m;
+#pragma unroll
+    for (int j = 0; j < C::FF; ++j) {
+      const int n = n0 + nw + j * 16 + (lane >> 4) * 4;
+      if (n >= cols) continue;
+      const f32x4_t v = acc[i][j];
+      if (g.out_f32) {
+        *reinterpret_cast<f32x4_t*>(static_cast<float*>(g.out) + row * cols + n) = v;
+      } else {
+        uint2 w;
+        w.x = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
+        w.y = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + row * cols + n) = w;
+      }
+    }
+  }
+}
+
+template <class C>
+__global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
+  __shared__ __align__(1024) uint8_t smem[C::Stage * C::NST];
+  __shared__ int sh[kWaves + 4];
+  const int cols = C::FT ? g.K : g.N;
+  const int nt = (cols + kBN - 1) / kBN;
+  if constexpr (C::K == kWeights) {
+    const int mt = (g.N + C::BM - 1) / C::BM;
+    const int e = blockIdx.x / (mt * nt), r = blockIdx.x % (mt * nt);
+    int a, b;
+    group_bounds(g, e, a, b);
+    tile<C>(g, smem, e, (r / nt) * C::BM, g.N, (r % nt) * kBN, a, b);
+  } else {
+    const Group gr = find_group<C::BM>(g, blockIdx.x / nt, sh);
+    if (gr.e < 0) return;
+    tile<C>(g, smem, gr.e, gr.a + gr.t * C::BM, gr.b, (blockIdx.x % nt) * kBN, gr.a, gr.b);
+  }
+}
+
+template <int KIND>
+using Simple = Cfg<KIND, 2, 4, 4, 4, 2>;  // 128 x 256
+
+}  // namespace
+
+size_t grouped_dw_workspace(int, int, int, int) { return 0; }
+
+hipError_t launch_grouped_mm(const GroupedMm& g, GroupedKind kind, hipStream_t stream) {
+  const int cols = kind == kGroupedInput || kind == kGroupedWeights ? g.K : g.N;
+  const int64_t nt = (cols + kBN - 1) / kBN;
+  constexpr int BM = 128;
+  int64_t mt;
+  if (kind == kGroupedWeights)
+    mt = static_cast<int64_t>(g.E) * ((g.N + BM - 1) / BM);
+  else  // the most row tiles any grouping of P rows can have
+    mt = g.P / BM + (g.E < g.P ? g.E : g.P);
+  const dim3 grid(static_cast<uint32_t>(mt * nt)), block(kThreads);
+  switch (kind) {
+    case kGroupedRows: return launch(grouped_tiles<Simple<kRows>>, grid, block, 0, stream, g);
+    case kGroupedInput: return launch(grouped_tiles<Simple<kInput>>, grid, block, 0, stream, g);
+    case kGroupedWeights: return launch(grouped_tiles<Simple<kWeights>>, grid, block, 0, stream, g);
+    case kGroupedCodes:
+      return g.out_f32 ? launch(grouped_tiles<Simple<kCodesF32>>, grid, block, 0, stream, g)
+                       : launch(grouped_tiles<Simple<kCodes>>, grid, block, 0, stream, g);
+  }
+  return hipErrorNotSupported;
+}
+
+}  // namespace moe

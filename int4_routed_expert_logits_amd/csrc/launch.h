@@ -118,4 +118,53 @@ hipError_t launch_combine(int T, int d, int k, const void* y, const void* y_shar
                           const int32_t* inv_perm, const float* topk_w, void* out,
                           bool out_bf16, hipStream_t stream);
 
+// grouped_mm.hip: products over rows grouped by expert.
+struct GroupedMm {
+  const uint8_t* r;  // operand indexed by the output's row: x or its codes, dy
+  const uint8_t* f;  // ... by the output's column: w or its codes, x
+  const float *r_scale, *f_scale;  // kGroupedCodes: per (row, 128 columns), per 128 x 128
+  const int32_t* offsets;          // [E + 1]
+  const int32_t* rows;             // [P] source rows of x times div, or NULL
+  uint32_t row_limit, div_magic;   // rows entries below row_limit are valid
+  void* out;
+  void* workspace;
+  int E, P, N, K;
+  bool out_f32;
+};
+size_t grouped_dw_workspace(int E, int P, int N, int K);
+enum GroupedKind { kGroupedRows, kGroupedInput, kGroupedWeights, kGroupedCodes };
+hipError_t launch_grouped_mm(const GroupedMm& g, GroupedKind kind, hipStream_t stream);
+
+// blockscale.hip: e4m3 codes with a float32 scale per 128 columns (or per 128
+// x 128), and SwiGLU over grouped rows (scales: h holds codes).
+hipError_t launch_blockscale_quantize(int n_mats, int R, int K, const void* x, bool f32,
+                                      bool square, uint8_t* codes, float* scales,
+                                      hipStream_t stream);
+hipError_t launch_swiglu(int P, int f, const void* gu, bool f32, void* h, float* scales,
+                         const int32_t* n_rows, hipStream_t stream);
+hipError_t launch_swiglu_grad(int P, int f, const void* gu, const void* dh, bool f32, void* dgu,
+                              const int32_t* n_rows, hipStream_t stream);
+
+// block_norm.hip: the norms and the residual around a block, and the gradient.
+struct BlockNorm {
+  int T, d, gate_rows;
+  float scale, eps;
+  bool y_bf16, res_bf16, normed_bf16;
+  const void *y, *res, *gate;
+  const float *w_post, *w_pre;
+  void *res_out, *normed;                 // forward
+  const void *dr, *dn;                    // gradient: of res_out, of normed
+  void *dy, *dres, *dgate;
+  float *dw_post, *dw_pre, *part;         // part: [norm_grad_parts][2][d]
+  bool columns;                           // a sum over the rows is asked for
+};
+int norm_grad_parts(int T);
+hipError_t launch_block_norm(const BlockNorm& g, hipStream_t stream);
+hipError_t launch_block_norm_grad(const BlockNorm& g, hipStream_t stream);
+
+// combine.hip: gradient of launch_combine.
+hipError_t launch_combine_grad(int T, int d, int k, const void* dout, bool out_bf16,
+                               const void* y, bool y_bf16, const int32_t* inv_perm,
+                               const float* topk_w, void* dy, float* dtopk_w, hipStream_t stream);
+
 }  // namespace moe
