@@ -179,21 +179,25 @@ __device__ __forceinline__ int kc_slot(int row, int chunk) { return chunk ^ ((ro
 // read of half a wavefront touches differ.
 __device__ __forceinline__ int mn_swz(int row) { return (row & 3) | (((row >> 3) & 1) << 2); }
 
-// This lane's fetches of one operand, contiguous along the contraction.
+// This lane's fetches of one operand: at stage s its chunk j comes from
+// p[j] + s * step where s * unit + off[j] < limit (the chunk lies before the
+// contraction's end), else from the zero block.  unit: contraction bytes of a
+// stage (operand contiguous along the contraction) or rows (the other kind).
+constexpr int kNever = 1 << 30;  // off of a chunk that no stage has
 template <int NI>
-struct SrcK {
+struct Src {
   const uint8_t* p[NI];
-  int step[NI];   // bytes per stage: 128, or 0 for the zero block
-  int chunk[NI];  // byte offset of its chunk in a stage
+  int off[NI];
+  int step;
 };
-template <int NI>
-__device__ __forceinline__ void issue_k(const SrcK<NI>& s, int stage, int red_bytes, uint32_t lds,
-                                        int first, int n_instr) {
+template <int NI, int UNIT>
+__device__ __forceinline__ void fetch(const Src<NI>& s, int stage, int limit, uint32_t lds,
+                                      int first, int n_instr) {
 #pragma unroll
   for (int j = 0; j < NI; ++j) {
-    const bool in = stage * kStageBytes + s.chunk[j] < red_bytes;
-    const uint8_t* p = in ? s.p[j] + static_cast<int64_t>(stage) * s.step[j] : zero_block();
-    dma16(p, lds + ((first + j) % n_instr) * 1024);
+    const uint8_t* p = s.p[j] + static_cast<int64_t>(stage) * s.step;
+    dma16(stage * UNIT + s.off[j] < limit ? p : zero_block(),
+          lds + ((first + j) % n_instr) * 1024);
   }
 }
 
@@ -233,20 +237,45 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   const uint32_t lds0 = lds_addr(smem);
 
   // ---- sources
-  SrcK<C::RI> rk;  // R along the contraction
-  SrcK<C::FI> fk;
+  constexpr int kUnitK = kStageBytes, kUnitMN = 64;
+  Src<C::RI> rs;
+  Src<C::FI> fs;
   const uint8_t* sp = zero_block();  // this lane's row scale
   int sstep = 0;
-  if constexpr (!C::RT) {
+  // an operand contiguous along its own index, W columns from c0 of `width`:
+  // chunk and row of fetch j
+  auto mn_row = [&](auto w, auto ni, int j) {
+    constexpr int LPR = decltype(w)::value / 8;  // lanes per row
+    return (wv * decltype(ni)::value + j) * (kWave / LPR) + lane / LPR;
+  };
+  auto mn_col = [&](auto w, int row) {
+    constexpr int LPR = decltype(w)::value / 8;
+    static_assert(LPR >= 16 && LPR <= kWave, "the swizzle moves 8 segments");
+    const int c = lane % LPR;
+    return ((((c >> 1) ^ mn_swz(row)) << 1) | (c & 1)) * 8;
+  };
+  using WR = std::integral_constant<int, C::RT ? C::BM : 128>;
+  using WF = std::integral_constant<int, kBN>;
+  using NR = std::integral_constant<int, C::RI>;
+  using NF = std::integral_constant<int, C::FI>;
+  if constexpr (C::RT) {
+    rs.step = 64 * g.N * 2;
+#pragma unroll
+    for (int j = 0; j < C::RI; ++j) {
+      const int row = mn_row(WR{}, NR{}, j), col = m0 + mn_col(WR{}, row);
+      rs.off[j] = col < g.N ? row : kNever;
+      rs.p[j] = g.r + (static_cast<int64_t>(ga + row) * g.N + col) * 2;
+    }
+  } else {
+    rs.step = kStageBytes;
 #pragma unroll
     for (int j = 0; j < C::RI; ++j) {
       const int row = ((wv * C::RI + j) * 8 + (lane >> 3)) % C::BM;
-      rk.chunk[j] = kc_slot(row, lane & 7) << 4;
+      const int chunk = kc_slot(row, lane & 7) << 4;
       int64_t src = -1;
-      if (m0 + row < mend)
-        src = C::K == kInput ? m0 + row : source_row(g, m0 + row);
-      rk.p[j] = src >= 0 ? g.r + src * red_bytes + rk.chunk[j] : zero_block();
-      rk.step[j] = src >= 0 ? kStageBytes : 0;
+      if (m0 + row < mend) src = C::K == kInput ? m0 + row : source_row(g, m0 + row);
+      rs.off[j] = src >= 0 ? chunk : kNever;
+      rs.p[j] = g.r + src * red_bytes + chunk;
     }
     if constexpr (C::F8) {
       const int row = t % C::BM;
@@ -257,58 +286,62 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       }
     }
   }
-  if constexpr (!C::FT) {
+  int next_row[C::FI];  // gathered F: rows entries of the stage after the next
+  const bool gather = C::K == kWeights && g.rows;
+  auto load_rows = [&](int stage) {
+#pragma unroll
+    for (int j = 0; j < C::FI; ++j) {
+      const int k = stage * 64 + mn_row(WF{}, NF{}, j);
+      next_row[j] = k < red ? g.rows[ga + k] : -1;
+    }
+  };
+  if constexpr (C::FT) {
+    fs.step = 64 * g.K * 2;
+#pragma unroll
+    for (int j = 0; j < C::FI; ++j) {
+      const int row = mn_row(WF{}, NF{}, j), col = n0 + mn_col(WF{}, row);
+      fs.off[j] = col < g.K ? row : kNever;
+      if (gather)
+        fs.p[j] = g.f + static_cast<int64_t>(col) * 2;
+      else
+        fs.p[j] = g.f + (C::K == kInput ? e * wsz : 0) +
+                  (static_cast<int64_t>(C::K == kInput ? row : ga + row) * g.K + col) * 2;
+    }
+  } else {
+    fs.step = kStageBytes;
 #pragma unroll
     for (int j = 0; j < C::FI; ++j) {
       const int row = (wv * C::FI + j) * 8 + (lane >> 3);
-      fk.chunk[j] = kc_slot(row, lane & 7) << 4;
-      const bool in = n0 + row < g.N;
-      fk.p[j] = in ? g.f + e * wsz + static_cast<int64_t>(n0 + row) * red_bytes + fk.chunk[j]
-                   : zero_block();
-      fk.step[j] = in ? kStageBytes : 0;
+      const int chunk = kc_slot(row, lane & 7) << 4;
+      fs.off[j] = n0 + row < g.N ? chunk : kNever;
+      fs.p[j] = g.f + e * wsz + static_cast<int64_t>(n0 + row) * red_bytes + chunk;
     }
   }
-  // an operand contiguous along its own index: chunk (lane) of row (instr)
-  auto issue_mn = [&](auto is_r, int stage, uint32_t lds) {
-    constexpr bool R = decltype(is_r)::value;
-    constexpr int W = R ? C::BM : kBN, NI = R ? C::RI : C::FI;
-    constexpr int LPR = W / 8;             // lanes per row of W columns
-    constexpr int RPI = kWave / LPR;       // rows per instruction
-    static_assert(LPR <= kWave && W >= 128, "row");  // the swizzle moves 8 segments
-    const int64_t ld = static_cast<int64_t>(R ? g.N : g.K) * 2;
-    const int width = R ? g.N : g.K, c0 = R ? m0 : n0;
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int row = (wv * NI + j) * RPI + lane / LPR;
-      const int sw = lane % LPR;
-      const int col = c0 + ((((sw >> 1) ^ mn_swz(row)) << 1) | (sw & 1)) * 8;
-      const int k = stage * 64 + row;
-      const uint8_t* p = zero_block();
-      if (k < red && col < width) {
-        if constexpr (C::K == kInput) {
-          p = g.f + e * wsz + k * ld + col * 2;
-        } else {
-          const int64_t src = R ? ga + k : source_row(g, ga + k);
-          if (src >= 0) p = (R ? g.r : g.f) + src * ld + col * 2;
-        }
-      }
-      dma16(p, lds + (wv * NI + j) * 1024);
-    }
-  };
   auto issue = [&](int stage, int buf) {
     const uint32_t lds = lds0 + buf * C::Stage;
     if constexpr (C::RT)
-      issue_mn(std::true_type{}, stage, lds);
+      fetch<C::RI, kUnitMN>(rs, stage, red, lds, wv * C::RI, 64);
     else
-      issue_k<C::RI>(rk, stage, red_bytes, lds, wv * C::RI, C::BM / 8);
-    if constexpr (C::FT)
-      issue_mn(std::false_type{}, stage, lds + C::RBytes);
-    else
-      issue_k<C::FI>(fk, stage, red_bytes, lds + C::RBytes, wv * C::FI, kBN / 8);
+      fetch<C::RI, kUnitK>(rs, stage, red_bytes, lds, wv * C::RI, C::BM / 8);
+    if constexpr (!C::FT) {
+      fetch<C::FI, kUnitK>(fs, stage, red_bytes, lds + C::RBytes, wv * C::FI, kBN / 8);
+    } else if (!gather) {
+      fetch<C::FI, kUnitMN>(fs, stage, red, lds + C::RBytes, wv * C::FI, 64);
+    } else {
+#pragma unroll
+      for (int j = 0; j < C::FI; ++j) {
+        const uint32_t r = static_cast<uint32_t>(next_row[j]);
+        const uint8_t* p = fs.p[j] + static_cast<int64_t>(row_div(r, g.div_magic)) * g.K * 2;
+        dma16(fs.off[j] != kNever && r < g.row_limit ? p : zero_block(),
+              lds + C::RBytes + (wv * C::FI + j) * 1024);
+      }
+      load_rows(stage + 1);
+    }
     if constexpr (C::F8)
       dma4(stage < stages ? sp + stage * sstep : zero_block(),
            lds + C::RBytes + C::FBytes + wv * 256);
   };
+  if (gather) load_rows(0);
 
   f32x4_t acc[C::RF][C::FF];
 #pragma unroll
@@ -325,7 +358,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     const uint8_t *sr = st, *sf = st + C::RBytes;
     if constexpr (C::K == kCodesF32) {
       const float ws = fsc[stage];
-      const float* rs = reinterpret_cast<const float*>(sf + C::FBytes);
+      const float* rsc = reinterpret_cast<const float*>(sf + C::FBytes);
       bf16x8_t fa[C::FF][4];  // 16 codes of each half of the stage
 #pragma unroll
       for (int j = 0; j < C::FF; ++j)
@@ -344,7 +377,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
           rb[2 * kk] = codes_to_bf16(v[0], v[1]);
           rb[2 * kk + 1] = codes_to_bf16(v[2], v[3]);
         }
-        const float s = rs[mw + i * 16 + (lane & 15)] * ws;
+        const float s = rsc[mw + i * 16 + (lane & 15)] * ws;
 #pragma unroll
         for (int j = 0; j < C::FF; ++j) {
           f32x4_t p{0.0f, 0.0f, 0.0f, 0.0f};
@@ -357,7 +390,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       }
     } else if constexpr (C::F8) {
       const float ws = fsc[stage];
-      const float* rs = reinterpret_cast<const float*>(sf + C::FBytes);
+      const float* rsc = reinterpret_cast<const float*>(sf + C::FBytes);
       i32x8_t fa[C::FF];
 #pragma unroll
       for (int j = 0; j < C::FF; ++j) {
@@ -369,7 +402,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
         const u32x4_t lo = frag_k(sr, mw + i * 16, 0, lane), hi = frag_k(sr, mw + i * 16, 1, lane);
         const i32x8_t rb =
             __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        const float s = rs[mw + i * 16 + (lane & 15)] * ws;
+        const float s = rsc[mw + i * 16 + (lane & 15)] * ws;
 #pragma unroll
         for (int j = 0; j < C::FF; ++j) {
           const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
@@ -441,27 +474,71 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   }
 }
 
-template <class C>
-__global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
-  __shared__ __align__(1024) uint8_t smem[C::Stage * C::NST];
-  __shared__ int sh[kWaves + 4];
-  const int cols = C::FT ? g.K : g.N;
-  const int nt = (cols + kBN - 1) / kBN;
-  if constexpr (C::K == kWeights) {
-    const int mt = (g.N + C::BM - 1) / C::BM;
-    const int e = blockIdx.x / (mt * nt), r = blockIdx.x % (mt * nt);
-    int a, b;
-    group_bounds(g, e, a, b);
-    tile<C>(g, smem, e, (r / nt) * C::BM, g.N, (r % nt) * kBN, a, b);
-  } else {
-    const Group gr = find_group<C::BM>(g, blockIdx.x / nt, sh);
-    if (gr.e < 0) return;
-    tile<C>(g, smem, gr.e, gr.a + gr.t * C::BM, gr.b, (blockIdx.x % nt) * kBN, gr.a, gr.b);
-  }
+// Workgroup -> tile: runs of kRun consecutive tiles go to one XCD (workgroups
+// are dealt to the 8 XCDs in turn), so the tiles that share a group's rows and
+// weights share an L2.
+constexpr int kXcds = 8, kRun = 4;
+__device__ __forceinline__ int64_t my_tile() {
+  const int xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
+  return (static_cast<int64_t>(i / kRun) * kXcds + xcd) * kRun + i % kRun;
+}
+uint32_t tile_grid(int64_t tiles) {
+  constexpr int64_t step = kXcds * kRun;
+  return static_cast<uint32_t>((tiles + step - 1) / step * step);
 }
 
+// Row tiles are 256 high; a group's last one takes the smallest height that
+// holds its rows.
+constexpr int kBM = 256;
 template <int KIND>
-using Simple = Cfg<KIND, 2, 4, 4, 4, 2>;  // 128 x 256
+using T256 = Cfg<KIND, 2, 4, 8, 4, 2>;
+template <int KIND>
+using T128 = Cfg<KIND, 2, 4, 4, 4, 3>;
+template <int KIND>
+using T64 = Cfg<KIND, 1, 8, 4, 2, 3>;
+template <int KIND>
+using T32 = Cfg<KIND, 1, 8, 2, 2, 4>;
+
+constexpr int cmax(int a, int b) { return a > b ? a : b; }
+template <class C>
+constexpr int lds_of() { return C::Stage * C::NST; }
+
+template <int KIND>
+__global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
+  constexpr int kLds = KIND == kWeights
+                           ? cmax(lds_of<T256<KIND>>(), lds_of<T128<KIND>>())
+                           : cmax(cmax(lds_of<T256<KIND>>(), lds_of<T128<KIND>>()),
+                                  cmax(lds_of<T64<KIND>>(), lds_of<T32<KIND>>()));
+  __shared__ __align__(1024) uint8_t smem[kLds];
+  const int cols = KIND == kInput || KIND == kWeights ? g.K : g.N;
+  const int nt = (cols + kBN - 1) / kBN;
+  const int64_t id = my_tile();
+  if constexpr (KIND == kWeights) {
+    const int mt = (g.N + kBM - 1) / kBM;
+    const int e = static_cast<int>(id / (mt * nt)), r = static_cast<int>(id % (mt * nt));
+    if (e >= g.E) return;
+    int a, b;
+    group_bounds(g, e, a, b);
+    const int m0 = (r / nt) * kBM, n0 = (r % nt) * kBN;
+    if (g.N - m0 > 128)
+      tile<T256<KIND>>(g, smem, e, m0, g.N, n0, a, b);
+    else
+      tile<T128<KIND>>(g, smem, e, m0, g.N, n0, a, b);
+  } else {
+    const Group gr = find_group<kBM>(g, static_cast<int>(id / nt), reinterpret_cast<int*>(smem));
+    if (gr.e < 0) return;
+    const int m0 = gr.a + gr.t * kBM, n0 = static_cast<int>(id % nt) * kBN;
+    const int rows = gr.b - m0;
+    if (rows > 128)
+      tile<T256<KIND>>(g, smem, gr.e, m0, min(gr.b, m0 + kBM), n0, gr.a, gr.b);
+    else if (rows > 64)
+      tile<T128<KIND>>(g, smem, gr.e, m0, gr.b, n0, gr.a, gr.b);
+    else if (rows > 32)
+      tile<T64<KIND>>(g, smem, gr.e, m0, gr.b, n0, gr.a, gr.b);
+    else
+      tile<T32<KIND>>(g, smem, gr.e, m0, gr.b, n0, gr.a, gr.b);
+  }
+}
 
 }  // namespace
 
@@ -470,20 +547,19 @@ size_t grouped_dw_workspace(int, int, int, int) { return 0; }
 hipError_t launch_grouped_mm(const GroupedMm& g, GroupedKind kind, hipStream_t stream) {
   const int cols = kind == kGroupedInput || kind == kGroupedWeights ? g.K : g.N;
   const int64_t nt = (cols + kBN - 1) / kBN;
-  constexpr int BM = 128;
   int64_t mt;
   if (kind == kGroupedWeights)
-    mt = static_cast<int64_t>(g.E) * ((g.N + BM - 1) / BM);
+    mt = static_cast<int64_t>(g.E) * ((g.N + kBM - 1) / kBM);
   else  // the most row tiles any grouping of P rows can have
-    mt = g.P / BM + (g.E < g.P ? g.E : g.P);
-  const dim3 grid(static_cast<uint32_t>(mt * nt)), block(kThreads);
+    mt = g.P / kBM + (g.E < g.P ? g.E : g.P);
+  const dim3 grid(tile_grid(mt * nt)), block(kThreads);
   switch (kind) {
-    case kGroupedRows: return launch(grouped_tiles<Simple<kRows>>, grid, block, 0, stream, g);
-    case kGroupedInput: return launch(grouped_tiles<Simple<kInput>>, grid, block, 0, stream, g);
-    case kGroupedWeights: return launch(grouped_tiles<Simple<kWeights>>, grid, block, 0, stream, g);
+    case kGroupedRows: return launch(grouped_tiles<kRows>, grid, block, 0, stream, g);
+    case kGroupedInput: return launch(grouped_tiles<kInput>, grid, block, 0, stream, g);
+    case kGroupedWeights: return launch(grouped_tiles<kWeights>, grid, block, 0, stream, g);
     case kGroupedCodes:
-      return g.out_f32 ? launch(grouped_tiles<Simple<kCodesF32>>, grid, block, 0, stream, g)
-                       : launch(grouped_tiles<Simple<kCodes>>, grid, block, 0, stream, g);
+      return g.out_f32 ? launch(grouped_tiles<kCodesF32>, grid, block, 0, stream, g)
+                       : launch(grouped_tiles<kCodes>, grid, block, 0, stream, g);
   }
   return hipErrorNotSupported;
 }
