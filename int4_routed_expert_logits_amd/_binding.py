@@ -415,83 +415,98 @@ def moe_cache_layer_decode(cache: int, x, w_router, bias, shared, topk_idx, topk
 # GPU, on `stream` or on that GPU's current stream.
 # ----------------------------------------------------------------------------
 
-def _take(fn: str, device, name: str, t, dtypes, shape):
+# set by _types(), which every call below makes first
+_T = _raw_stream = _current_device = None
+
+
+def _types():
+    """(bf16, f32, either, int32, e4m3 code) as tuples of torch types."""
+    global _T, _raw_stream, _current_device
+    if _T is None:
+        import torch
+        # the handle itself: building a torch Stream takes longer than a launch
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _current_device = torch.cuda.current_device
+        _T = ((torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32), (torch.int32,),
+              (torch.float8_e4m3fn, torch.uint8))
+    return _T
+
+
+def _take(fn: str, dev: int, name: str, t, dtypes, shape):
     """t's address, after checking it (None passes as NULL)."""
     if t is None:
         return None
     if t.dtype not in dtypes:
         raise TypeError(f"{fn}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{fn}: {name} is on {t.device}, not on the GPU of the first tensor ({device})")
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on the first tensor's GPU ({dev})")
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} is not contiguous")
     return t.data_ptr()
 
 
 def _dim(fn: str, name: str, t, n: int):
-    if t.dim() != n:
-        raise ValueError(f"{fn}: {name} has {t.dim()} dimensions, not {n}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{fn}: {name} has {len(shape)} dimensions, not {n}")
+    return shape
 
 
-def _workspace(fn: str, device, t):
+def _workspace(fn: str, dev: int, t):
     """(address, bytes) of a workspace tensor of any type; (NULL, 0) for None."""
     if t is None:
         return None, 0
-    return _take(fn, device, "workspace", t, (t.dtype,), t.shape), t.numel() * t.element_size()
+    return _take(fn, dev, "workspace", t, (t.dtype,), t.shape), t.numel() * t.element_size()
 
 
-def _run(fn: str, device, stream, *args):
-    """One C call with the tensors' GPU current, on `stream` or its current stream."""
-    import torch
-    call = getattr(load(), fn)
+def _run(fn: str, dev: int, stream, *args):
+    """One C call with GPU dev current, on `stream` or dev's current stream."""
+    if dev < 0:
+        raise ValueError(f"{fn}: the tensors are not on the GPU")
+    call = getattr(_lib or load(), fn)
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = _raw_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(fn, call(*args, stream))
+    if _current_device() == dev:
+        status = call(*args, stream)
     else:
-        with torch.cuda.device(device):
-            _check(fn, call(*args, stream))
+        import torch
+        with torch.cuda.device(dev):
+            status = call(*args, stream)
+    if status != MOE_OK:
+        raise MoeError(fn, status)
 
 
-def _types():
-    import torch
-    return torch.bfloat16, torch.float32, (torch.bfloat16, torch.float32), torch.int32, (
-        torch.float8_e4m3fn, torch.uint8)
-
-
-def _rows_args(fn, device, P, rows):
-    import torch
-    return _take(fn, device, "rows", rows, (torch.int32,), (P,))
+def _rows_args(fn, dev, P, rows):
+    return None if rows is None else _take(fn, dev, "rows", rows, _types()[3], (P,))
 
 
 def moe_grouped_mm(x, w, offsets, y, rows=None, rows_div: int = 1, stream=None):
     """y[p] = w[e] x[rows[p] // rows_div] (x[p] without rows): x [X, K] bf16,
     w [E, N, K] bf16, offsets [E + 1] and rows [P] int32, y [P, N] bf16/f32."""
-    fn, dev = "moe_grouped_mm", x.device
+    fn, dev = "moe_grouped_mm", x.get_device()
     bf16, _, floats, i32, _ = _types()
     E, N, K = _dim(fn, "w", w, 3)
     P, X = _dim(fn, "y", y, 2)[0], _dim(fn, "x", x, 2)[0]
-    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "x", x, (bf16,), (X, K)), X,
-         _rows_args(fn, dev, P, rows), rows_div, _take(fn, dev, "w", w, (bf16,), (E, N, K)),
-         _take(fn, dev, "offsets", offsets, (i32,), (E + 1,)),
-         _take(fn, dev, "y", y, floats, (P, N)), _dtype(y))
+    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "x", x, bf16, (X, K)), X,
+         _rows_args(fn, dev, P, rows), rows_div, _take(fn, dev, "w", w, bf16, (E, N, K)),
+         _take(fn, dev, "offsets", offsets, i32, (E + 1,)),
+         _take(fn, dev, "y", y, floats, (P, N)), _code(y.dtype))
 
 
 def moe_grouped_mm_dx(dy, w, offsets, dx, stream=None):
     """dx[p] = w[e]^T dy[p]: dy [P, N] bf16, w [E, N, K] bf16, dx [P, K] bf16/f32."""
-    fn, dev = "moe_grouped_mm_dx", dy.device
+    fn, dev = "moe_grouped_mm_dx", dy.get_device()
     bf16, _, floats, i32, _ = _types()
     E, N, K = _dim(fn, "w", w, 3)
     P = _dim(fn, "dx", dx, 2)[0]
-    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "dy", dy, (bf16,), (P, N)),
-         _take(fn, dev, "w", w, (bf16,), (E, N, K)),
-         _take(fn, dev, "offsets", offsets, (i32,), (E + 1,)),
-         _take(fn, dev, "dx", dx, floats, (P, K)), _dtype(dx))
+    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "dy", dy, bf16, (P, N)),
+         _take(fn, dev, "w", w, bf16, (E, N, K)),
+         _take(fn, dev, "offsets", offsets, i32, (E + 1,)),
+         _take(fn, dev, "dx", dx, floats, (P, K)), _code(dx.dtype))
 
 
 def moe_grouped_mm_dw_workspace_bytes(E: int, P: int, N: int, K: int) -> int:
@@ -502,94 +517,93 @@ def moe_grouped_mm_dw(dy, x, offsets, dw, workspace=None, rows=None, rows_div: i
                       stream=None):
     """dw[e] = sum over e's positions of dy[p] x[row(p)]^T: dy [P, N] and
     x [X, K] bf16, dw [E, N, K] bf16/f32 (all of it written)."""
-    fn, dev = "moe_grouped_mm_dw", dy.device
+    fn, dev = "moe_grouped_mm_dw", dy.get_device()
     bf16, _, floats, i32, _ = _types()
     E, N, K = _dim(fn, "dw", dw, 3)
     P, X = _dim(fn, "dy", dy, 2)[0], _dim(fn, "x", x, 2)[0]
     ws, nws = _workspace(fn, dev, workspace)
-    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "dy", dy, (bf16,), (P, N)),
-         _take(fn, dev, "x", x, (bf16,), (X, K)), X, _rows_args(fn, dev, P, rows), rows_div,
-         _take(fn, dev, "offsets", offsets, (i32,), (E + 1,)),
-         _take(fn, dev, "dw", dw, floats, (E, N, K)), _dtype(dw), ws, nws)
+    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "dy", dy, bf16, (P, N)),
+         _take(fn, dev, "x", x, bf16, (X, K)), X, _rows_args(fn, dev, P, rows), rows_div,
+         _take(fn, dev, "offsets", offsets, i32, (E + 1,)),
+         _take(fn, dev, "dw", dw, floats, (E, N, K)), _code(dw.dtype), ws, nws)
 
 
 def moe_blockscale_quantize(x, block_rows: int, codes, scales, stream=None):
     """x [R, K] or [n, R, K] bf16/f32 -> e4m3 codes of x's shape
     (float8_e4m3fn or uint8) and float32 scales per 128 columns: [.., R, K/128]
     for block_rows 1, [.., R/128, K/128] for 128 (rounded up)."""
-    fn, dev = "moe_blockscale_quantize", x.device
+    fn, dev = "moe_blockscale_quantize", x.get_device()
     _, f32, floats, _, codes_t = _types()
     if x.dim() not in (2, 3):
         raise ValueError(f"{fn}: x has {x.dim()} dimensions, not 2 or 3")
     *lead, R, K = x.shape
     sr = R if block_rows == 1 else -(-R // 128)
     _run(fn, dev, stream, lead[0] if lead else 1, R, K, _take(fn, dev, "x", x, floats, x.shape),
-         _dtype(x), block_rows, _take(fn, dev, "codes", codes, codes_t, x.shape),
-         _take(fn, dev, "scales", scales, (f32,), (*lead, sr, -(-K // 128))))
+         _code(x.dtype), block_rows, _take(fn, dev, "codes", codes, codes_t, x.shape),
+         _take(fn, dev, "scales", scales, f32, (*lead, sr, -(-K // 128))))
 
 
 def moe_blockscale_mm(xq, xs, wq, ws, offsets, y, rows=None, rows_div: int = 1, stream=None):
     """moe_grouped_mm over e4m3 codes: xq [X, K] with xs [X, K/128], wq
     [E, N, K] with ws [E, N/128, K/128] (rounded up), y [P, N] bf16/f32."""
-    fn, dev = "moe_blockscale_mm", xq.device
+    fn, dev = "moe_blockscale_mm", xq.get_device()
     _, f32, floats, i32, codes_t = _types()
     E, N, K = _dim(fn, "wq", wq, 3)
     P, X, kb = _dim(fn, "y", y, 2)[0], _dim(fn, "xq", xq, 2)[0], -(-K // 128)
     _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "xq", xq, codes_t, (X, K)),
-         _take(fn, dev, "xs", xs, (f32,), (X, kb)), X, _rows_args(fn, dev, P, rows), rows_div,
+         _take(fn, dev, "xs", xs, f32, (X, kb)), X, _rows_args(fn, dev, P, rows), rows_div,
          _take(fn, dev, "wq", wq, codes_t, (E, N, K)),
-         _take(fn, dev, "ws", ws, (f32,), (E, -(-N // 128), kb)),
-         _take(fn, dev, "offsets", offsets, (i32,), (E + 1,)),
-         _take(fn, dev, "y", y, floats, (P, N)), _dtype(y))
+         _take(fn, dev, "ws", ws, f32, (E, -(-N // 128), kb)),
+         _take(fn, dev, "offsets", offsets, i32, (E + 1,)),
+         _take(fn, dev, "y", y, floats, (P, N)), _code(y.dtype))
 
 
 def _n_rows(fn, dev, n_rows):
-    import torch
-    return _take(fn, dev, "n_rows", n_rows, (torch.int32,), (1,))
+    return None if n_rows is None else _take(fn, dev, "n_rows", n_rows, _types()[3], (1,))
 
 
 def moe_swiglu(gu, h, n_rows=None, stream=None):
     """h = silu(gu[:, :f]) * gu[:, f:]: gu [P, 2 f], h [P, f], both bf16 or both
     f32; n_rows: device int32 [1], rows from it on are left as they were."""
-    fn, dev = "moe_swiglu", gu.device
+    fn, dev = "moe_swiglu", gu.get_device()
     P, f = _dim(fn, "h", h, 2)
     _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, _types()[2], (P, 2 * f)),
-         _take(fn, dev, "h", h, (gu.dtype,), (P, f)), _dtype(gu), _n_rows(fn, dev, n_rows))
+         _take(fn, dev, "h", h, (gu.dtype,), (P, f)), _code(gu.dtype), _n_rows(fn, dev, n_rows))
 
 
 def moe_swiglu_quantize(gu, codes, scales, n_rows=None, stream=None):
     """moe_swiglu's result as e4m3 codes [P, f] and scales [P, f/128] (rounded up)."""
-    fn, dev = "moe_swiglu_quantize", gu.device
+    fn, dev = "moe_swiglu_quantize", gu.get_device()
     _, f32, floats, _, codes_t = _types()
     P, f = _dim(fn, "codes", codes, 2)
-    _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, floats, (P, 2 * f)), _dtype(gu),
+    _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, floats, (P, 2 * f)), _code(gu.dtype),
          _take(fn, dev, "codes", codes, codes_t, (P, f)),
-         _take(fn, dev, "scales", scales, (f32,), (P, -(-f // 128))), _n_rows(fn, dev, n_rows))
+         _take(fn, dev, "scales", scales, f32, (P, -(-f // 128))), _n_rows(fn, dev, n_rows))
 
 
 def moe_swiglu_grad(gu, dh, dgu, n_rows=None, stream=None):
     """moe_swiglu's gradient: gu, dgu [P, 2 f], dh [P, f], one type; dgu may be gu."""
-    fn, dev = "moe_swiglu_grad", gu.device
+    fn, dev = "moe_swiglu_grad", gu.get_device()
     P, f = _dim(fn, "dh", dh, 2)
     _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, _types()[2], (P, 2 * f)),
          _take(fn, dev, "dh", dh, (gu.dtype,), (P, f)),
-         _take(fn, dev, "dgu", dgu, (gu.dtype,), (P, 2 * f)), _dtype(gu), _n_rows(fn, dev, n_rows))
+         _take(fn, dev, "dgu", dgu, (gu.dtype,), (P, 2 * f)), _code(gu.dtype), _n_rows(fn, dev, n_rows))
 
 
 def moe_combine_grad(shape, dout, y, inv_perm, topk_w, dy, dtopk_w, stream=None):
     """moe_combine's gradient: dout [T, d], y and dy [T * k, d] (bf16/f32, one
     type; dy may be y), inv_perm [T * k] int32, topk_w and dtopk_w [T, k] f32."""
-    fn, dev = "moe_combine_grad", dout.device
+    fn, dev = "moe_combine_grad", dout.get_device()
     _, f32, floats, i32, _ = _types()
     sh = _shape(shape)
     T, n = _dim(fn, "dout", dout, 2)[0], dout.shape[0] * sh.top_k
     _run(fn, dev, stream, ctypes.byref(sh), T,
-         _take(fn, dev, "dout", dout, floats, (T, sh.d)), _dtype(dout),
-         _take(fn, dev, "y", y, floats, (n, sh.d)), _dtype(y),
-         _take(fn, dev, "inv_perm", inv_perm, (i32,), (n,)),
-         _take(fn, dev, "topk_w", topk_w, (f32,), (T, sh.top_k)),
+         _take(fn, dev, "dout", dout, floats, (T, sh.d)), _code(dout.dtype),
+         _take(fn, dev, "y", y, floats, (n, sh.d)), _code(y.dtype),
+         _take(fn, dev, "inv_perm", inv_perm, i32, (n,)),
+         _take(fn, dev, "topk_w", topk_w, f32, (T, sh.top_k)),
          _take(fn, dev, "dy", dy, (y.dtype,), (n, sh.d)),
-         _take(fn, dev, "dtopk_w", dtopk_w, (f32,), (T, sh.top_k)))
+         _take(fn, dev, "dtopk_w", dtopk_w, f32, (T, sh.top_k)))
 
 
 def _norm_args(fn, y, res, w_post, w_pre, gate, scale):
@@ -598,15 +612,16 @@ def _norm_args(fn, y, res, w_post, w_pre, gate, scale):
     first = y if y is not None else res
     if first is None:
         raise ValueError(f"{fn}: neither y nor res")
-    dev, (T, d) = first.device, _dim(fn, "y" if y is not None else "res", first, 2)
-    ydt = bf16 if y is None else y.dtype
+    name = "y" if y is not None else "res"
+    dev, (T, d) = first.get_device(), _dim(fn, name, first, 2)
+    ydt = bf16[0] if y is None else y.dtype
     rdt = ydt if res is None else res.dtype
     g = 0 if gate is None else _dim(fn, "gate", gate, 2)[0]
-    head = (T, d, _take(fn, dev, "y", y, floats, (T, d)), MOE_BF16 if ydt == bf16 else MOE_F32,
-            _take(fn, dev, "w_post", w_post, (f32,), (d,)),
+    head = (T, d, _take(fn, dev, "y", y, floats, (T, d)), _code(ydt),
+            _take(fn, dev, "w_post", w_post, f32, (d,)),
             _take(fn, dev, "gate", gate, (ydt,), (g, d)), g, scale,
             _take(fn, dev, "res", res, (rdt,) if rdt in floats else floats, (T, d)))
-    return dev, T, d, ydt, rdt, head, _take(fn, dev, "w_pre", w_pre, (f32,), (d,))
+    return dev, T, d, ydt, rdt, head, _take(fn, dev, "w_pre", w_pre, f32, (d,))
 
 
 def moe_block_norm(y, res, res_out, normed, w_post=None, w_pre=None, gate=None, scale=1.0,
@@ -622,14 +637,14 @@ def moe_block_norm(y, res, res_out, normed, w_post=None, w_pre=None, gate=None, 
         rdt = res_out.dtype
     _run(fn, dev, stream, *head, _code(rdt), _take(fn, dev, "res_out", res_out, (rdt,), (T, d)),
          w2, eps, _take(fn, dev, "normed", normed, floats, (T, d)),
-         MOE_F32 if normed is None else _dtype(normed))
+         MOE_F32 if normed is None else _code(normed.dtype))
 
 
 def _code(dtype) -> int:
-    import torch
-    if dtype not in (torch.bfloat16, torch.float32):
+    bf16, f32, *_ = _types()
+    if dtype not in bf16 + f32:
         raise TypeError(f"unsupported dtype {dtype}")
-    return MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+    return MOE_BF16 if dtype in bf16 else MOE_F32
 
 
 def moe_block_norm_grad_workspace_bytes(T: int, d: int) -> int:
@@ -648,8 +663,8 @@ def moe_block_norm_grad(y, res, dr, dn, dy, dres, dw_post, dw_pre, dgate, w_post
         rdt = dr.dtype if dr is not None else dres.dtype if dres is not None else rdt
     ws, nws = _workspace(fn, dev, workspace)
     _run(fn, dev, stream, *head, _code(rdt), w2, eps, _take(fn, dev, "dr", dr, (rdt,), (T, d)),
-         _take(fn, dev, "dn", dn, floats, (T, d)), MOE_F32 if dn is None else _dtype(dn),
+         _take(fn, dev, "dn", dn, floats, (T, d)), MOE_F32 if dn is None else _code(dn.dtype),
          _take(fn, dev, "dy", dy, (ydt,), (T, d)), _take(fn, dev, "dres", dres, (rdt,), (T, d)),
          _take(fn, dev, "dgate", dgate, (ydt,), (head[6], d)),
-         _take(fn, dev, "dw_post", dw_post, (f32,), (d,)),
-         _take(fn, dev, "dw_pre", dw_pre, (f32,), (d,)), ws, nws)
+         _take(fn, dev, "dw_post", dw_post, f32, (d,)),
+         _take(fn, dev, "dw_pre", dw_pre, f32, (d,)), ws, nws)

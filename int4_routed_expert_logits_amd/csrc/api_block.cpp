@@ -295,7 +295,7 @@ moe_status moe_block_norm(int32_t T, int32_t d, const void* y, moe_dtype y_dt,
 
 size_t moe_block_norm_grad_workspace_bytes(int32_t T, int32_t d) {
   if (T < 0 || d <= 0 || d % 8 != 0 || d > kMaxNorm || T > kMaxPositions) return 0;
-  return moe::round_up(static_cast<size_t>(moe::norm_grad_parts(T)) * 2 * d * sizeof(float));
+  return moe::round_up(static_cast<size_t>(moe::norm_grad_parts(T, d)) * 2 * d * sizeof(float));
 }
 
 moe_status moe_block_norm_grad(int32_t T, int32_t d, const void* y, moe_dtype y_dt,

@@ -110,89 +110,155 @@ __global__ __launch_bounds__(1024) void norm_rows(BlockNorm g) {
   }
 }
 
+// Sums of five values over the workgroup, in a fixed order; sh: 5 x kMaxWaves
+// floats not used since the last barrier.
+__device__ __forceinline__ void block_sum5(float (&v)[5], float (*sh)[kMaxWaves]) {
+#pragma unroll
+  for (int i = 0; i < 5; ++i) v[i] = group_sum(v[i], kWave);
+  const int waves = blockDim.x / kWave;
+  if (waves == 1) return;
+  if (threadIdx.x % kWave == 0) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) sh[i][threadIdx.x / kWave] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 5; ++i) v[i] = 0.0f;
+  for (int w = 0; w < waves; ++w)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] += sh[i][w];
+}
+
+// 8 values of a row as they lie in memory.
+struct Raw {
+  uint4 lo, hi;  // hi: the second half of 8 float32
+};
+template <bool ALL_BF16>
+__device__ __forceinline__ Raw raw8(const void* p, bool bf16, int64_t i) {
+  Raw r{};
+  if (ALL_BF16 || bf16) {
+    r.lo = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+  } else {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+    r.lo = q[0];
+    r.hi = q[1];
+  }
+  return r;
+}
+template <bool ALL_BF16>
+__device__ __forceinline__ void values(const Raw& r, bool bf16, float (&v)[kV]) {
+  const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+  if (ALL_BF16 || bf16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) v[j] = __uint_as_float(w[j]);
+  }
+}
+
 // One workgroup takes rows blockIdx.x, + gridDim.x, ...; the columns' sums
-//   s1 = sum_t [gate_t] dr ∘ yh     (dw_post, dgate of a broadcast gate)
-//   s2 = sum_t dn ∘ r b             (dw_pre)
+//   s1 = sum_t [gate_t] t ∘ yh      (dw_post, dgate of a broadcast gate)
+//   s2 = sum_t dn ∘ rh              (dw_pre)
 // stay in its registers and go to part[workgroup][2][d].  The gradient:
 //   t  = dr + b (v - rh mean(v rh)),  v = w_pre dn, rh = r b     -> dres
 //   dp = scale gate t;  dgate = scale t w_post yh
-//   dy = a (v - yh mean(v yh)),       v = w_post dp
-__global__ __launch_bounds__(1024) void norm_grad_rows(BlockNorm g) {
-  __shared__ float sh[4][kMaxWaves];
+//   dy = a (q' - yh mean(q' yh)),     q' = w_post dp
+// mean(q' yh) is linear in t, so with q = scale gate w_post yh it follows from
+// the sums of q dr, q v and q r: after a, one round of five sums (with r^2 and
+// v r) gives every scalar of the row, and a row costs two meetings of the
+// workgroup.  With all-bf16 rows the next row is fetched before this row's
+// sums (a row of float32 would not fit the registers twice).
+// THREADS, the most of a launch, sets the registers a thread may hold (256, 168,
+// 128): the widest rows have the fewest.  PER_TOKEN: a gate of T rows.
+template <int THREADS, bool ALL_BF16, bool PER_TOKEN>
+__global__ __launch_bounds__(THREADS) void norm_grad_rows(BlockNorm g) {
+  __shared__ float sh[2][6][kMaxWaves];  // by the row's parity
   const int c = threadIdx.x * kV;
   const bool in = c < g.d;
-  float w1[kV], w2[kV], g1[kV], s1[kV] = {}, s2[kV] = {};
+  float w1[kV], w2[kV], gt[kV], s1[kV] = {}, s2[kV] = {};
   ones(w1);
   ones(w2);
-  ones(g1);
+  ones(gt);
   if (in) {
     if (g.w_post) load8(g.w_post, false, c, w1);
     if (g.w_pre) load8(g.w_pre, false, c, w2);
-    if (g.gate && g.gate_rows == 1) load8(g.gate, g.y_bf16, c, g1);
+    if (!PER_TOKEN && g.gate) load8(g.gate, g.y_bf16, c, gt);
   }
   const float inv_d = 1.0f / static_cast<float>(g.d);
-  const bool per_token = g.gate && g.gate_rows != 1;
-  for (int64_t row = blockIdx.x; row < g.T; row += gridDim.x) {
+  Raw ry{}, rr{}, rt{}, rn{}, rg{};
+  auto read = [&](int64_t row) {
     const int64_t at = row * g.d + c;
-    float y[kV] = {}, r[kV] = {}, t[kV] = {}, dn[kV] = {}, gt[kV];
-#pragma unroll
-    for (int j = 0; j < kV; ++j) gt[j] = g1[j];
-    if (in) {
-      if (g.y) load8(g.y, g.y_bf16, at, y);
-      if (g.res) load8(g.res, g.res_bf16, at, r);
-      if (per_token) load8(g.gate, g.y_bf16, at, gt);
-      if (g.dr) load8(g.dr, g.res_bf16, at, t);
-      if (g.w_pre) load8(g.dn, g.normed_bf16, at, dn);
-    }
+    if (!in || row >= g.T) return;
+    if (g.y) ry = raw8<ALL_BF16>(g.y, g.y_bf16, at);
+    if (g.res) rr = raw8<ALL_BF16>(g.res, g.res_bf16, at);
+    if (g.dr) rt = raw8<ALL_BF16>(g.dr, g.res_bf16, at);
+    if (g.w_pre) rn = raw8<ALL_BF16>(g.dn, g.normed_bf16, at);
+    if (PER_TOKEN) rg = raw8<ALL_BF16>(g.gate, g.y_bf16, at);
+  };
+  read(blockIdx.x);
+  int odd = 0;
+  for (int64_t row = blockIdx.x; row < g.T; row += gridDim.x, odd ^= 1) {
+    const int64_t at = row * g.d + c;
+    float y[kV], r[kV], t[kV], dn[kV];
+    values<ALL_BF16>(ry, g.y_bf16, y);
+    values<ALL_BF16>(rr, g.res_bf16, r);
+    values<ALL_BF16>(rt, g.res_bf16, t);
+    values<ALL_BF16>(rn, g.normed_bf16, dn);
+    if (PER_TOKEN) values<ALL_BF16>(rg, g.y_bf16, gt);
+    if (ALL_BF16) read(row + gridDim.x);
     float a = 1.0f;
     if (g.y && g.w_post) {
-      a = inv_rms(block_sum(sum_sq(y), sh[0]), g.d, g.eps);
+      a = inv_rms(block_sum(sum_sq(y), sh[odd][5]), g.d, g.eps);
 #pragma unroll
       for (int j = 0; j < kV; ++j) y[j] *= a;  // yh
     }
-    if (g.y) {
+    float sum[5] = {};  // r^2, v r, q dr, q v, q r
 #pragma unroll
-      for (int j = 0; j < kV; ++j) r[j] = fmaf(g.scale * gt[j], w1[j] * y[j], r[j]);
+    for (int j = 0; j < kV; ++j) {
+      const float q = g.scale * gt[j] * (w1[j] * y[j]);
+      const float v = w2[j] * dn[j];
+      if (g.y) r[j] += q;
+      sum[0] = fmaf(r[j], r[j], sum[0]);
+      sum[1] = fmaf(v, r[j], sum[1]);
+      sum[2] = fmaf(q, t[j], sum[2]);
+      sum[3] = fmaf(q, v, sum[3]);
+      sum[4] = fmaf(q, r[j], sum[4]);
     }
+    block_sum5(sum, sh[odd]);
+    float mean_qt = sum[2];
     if (g.w_pre) {
-      const float b = inv_rms(block_sum(in ? sum_sq(r) : 0.0f, sh[1]), g.d, g.eps);
-      float dot = 0.0f;
+      const float b = inv_rms(sum[0], g.d, g.eps);
+      const float m = b * b * sum[1] * inv_d;  // mean(v rh) b, so t = dr + b (v - m r)
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        r[j] *= b;  // rh
-        s2[j] = fmaf(dn[j], r[j], s2[j]);
-        dn[j] *= w2[j];
-        dot = fmaf(dn[j], r[j], dot);
+        s2[j] = fmaf(dn[j], r[j] * b, s2[j]);
+        t[j] = fmaf(b, fmaf(-m, r[j], w2[j] * dn[j]), t[j]);
       }
-      const float mean = block_sum(in ? dot : 0.0f, sh[2]) * inv_d;
-#pragma unroll
-      for (int j = 0; j < kV; ++j) t[j] = fmaf(b, fmaf(-mean, r[j], dn[j]), t[j]);
+      mean_qt = fmaf(b, fmaf(-m, sum[4], sum[3]), mean_qt);
     }
+    mean_qt *= inv_d;  // mean(q' yh)
     if (in && g.dres) store8(g.dres, g.res_bf16, at, t);
     if (g.y) {
-      if (per_token) {
+      if (PER_TOKEN && in && g.dgate) {
         float dg[kV];
 #pragma unroll
         for (int j = 0; j < kV; ++j) dg[j] = g.scale * t[j] * (w1[j] * y[j]);
-        if (in && g.dgate) store8(g.dgate, g.y_bf16, at, dg);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) t[j] *= gt[j];
+        store8(g.dgate, g.y_bf16, at, dg);
       }
-      float dot = 0.0f, dp[kV];
+      float dp[kV];
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        s1[j] = fmaf(t[j], y[j], s1[j]);
-        dp[j] = g.scale * (per_token ? t[j] : t[j] * gt[j]) * w1[j];
-        dot = fmaf(dp[j], y[j], dot);
-      }
-      if (g.w_post) {
-        const float mean = block_sum(in ? dot : 0.0f, sh[3]) * inv_d;
-#pragma unroll
-        for (int j = 0; j < kV; ++j) dp[j] = a * fmaf(-mean, y[j], dp[j]);
+        s1[j] = fmaf(PER_TOKEN ? t[j] * gt[j] : t[j], y[j], s1[j]);
+        dp[j] = g.scale * (t[j] * gt[j]) * w1[j];
+        if (g.w_post) dp[j] = a * fmaf(-mean_qt, y[j], dp[j]);
       }
       if (in && g.dy) store8(g.dy, g.y_bf16, at, dp);
     }
-    __syncthreads();  // the sums' scratch is free for the next row
+    if (!ALL_BF16) read(row + gridDim.x);
   }
   if (in && g.part) {
     const int64_t o = static_cast<int64_t>(blockIdx.x) * 2 * g.d + c;
@@ -243,16 +309,37 @@ dim3 row_block(int d) { return dim3((d / kV + kWave - 1) / kWave * kWave); }
 
 }  // namespace
 
-int norm_grad_parts(int T) { return T < 512 ? T : 512; }
+// Workgroups of the gradient: one per CU, more where a row takes less than 16
+// wavefronts' share of it, and no more than rows.
+int norm_grad_parts(int T, int d) {
+  const int waves = (d / kV + kWave - 1) / kWave;
+  const int parts = 256 * (waves > 8 ? 1 : waves > 4 ? 2 : 4);
+  return T < parts ? T : parts;
+}
+
+template <int THREADS>
+hipError_t launch_norm_grad_rows(const BlockNorm& g, int parts, hipStream_t stream) {
+  const bool all_bf16 = g.y_bf16 && g.res_bf16 && g.normed_bf16;
+  const bool per_token = g.gate && g.gate_rows != 1;
+  auto go = [&](auto kernel) { return launch(kernel, dim3(parts), row_block(g.d), 0, stream, g); };
+  if (all_bf16)
+    return per_token ? go(norm_grad_rows<THREADS, true, true>)
+                     : go(norm_grad_rows<THREADS, true, false>);
+  return per_token ? go(norm_grad_rows<THREADS, false, true>)
+                   : go(norm_grad_rows<THREADS, false, false>);
+}
 
 hipError_t launch_block_norm(const BlockNorm& g, hipStream_t stream) {
   return launch(norm_rows, dim3(g.T), row_block(g.d), 0, stream, g);
 }
 
 hipError_t launch_block_norm_grad(const BlockNorm& g, hipStream_t stream) {
-  const int parts = norm_grad_parts(g.T);
+  const int parts = norm_grad_parts(g.T, g.d);
   if (parts > 0) {
-    const hipError_t e = launch(norm_grad_rows, dim3(parts), row_block(g.d), 0, stream, g);
+    const uint32_t threads = row_block(g.d).x;
+    const hipError_t e = threads <= 512   ? launch_norm_grad_rows<512>(g, parts, stream)
+                         : threads <= 768 ? launch_norm_grad_rows<768>(g, parts, stream)
+                                          : launch_norm_grad_rows<1024>(g, parts, stream);
     if (e != hipSuccess || !g.columns) return e;
   }
   return launch(norm_grad_columns, dim3((g.d + kWave - 1) / kWave), dim3(1024), 0, stream, g,

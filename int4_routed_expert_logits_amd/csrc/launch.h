@@ -158,7 +158,7 @@ struct BlockNorm {
   float *dw_post, *dw_pre, *part;         // part: [norm_grad_parts][2][d]
   bool columns;                           // a sum over the rows is asked for
 };
-int norm_grad_parts(int T);
+int norm_grad_parts(int T, int d);
 hipError_t launch_block_norm(const BlockNorm& g, hipStream_t stream);
 hipError_t launch_block_norm_grad(const BlockNorm& g, hipStream_t stream);
 
