@@ -35,10 +35,10 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+typedef const __attribute__((address_space(4))) int32_t const_i32;  // by scalar loads
 
 constexpr int kThreads = 512;  // 8 wavefronts
 constexpr int kWaves = kThreads / kWave;
-constexpr int kStageBytes = 128;  // bytes of the contraction per stage and row
 constexpr int kBN = 256;          // output columns per tile
 constexpr int kBlock = 128;       // columns (and weight rows) per scale
 
@@ -46,7 +46,8 @@ constexpr int kBlock = 128;       // columns (and weight rows) per scale
 __device__ const uint4 g_zero[8] = {};
 
 // kCodesF32: the codes multiplied as bf16, for float32 results.
-enum Kind { kRows, kInput, kWeights, kCodes, kCodesF32 };
+// kWeightsBy: kWeights with x gathered through rows.
+enum Kind { kRows, kInput, kWeights, kWeightsBy, kCodes, kCodesF32 };
 
 // LDS byte address of a pointer into a __shared__ array.
 __device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) {
@@ -72,6 +73,16 @@ template <int N>
 __device__ __forceinline__ void wait_and_meet() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
+}
+
+// This wavefront's LDS reads back, then a meeting; nothing is scheduled across.
+__device__ __forceinline__ void reads_and_meet() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+template <int N>
+__device__ __forceinline__ void wait_fetches() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
 }
 
 __device__ __forceinline__ const uint8_t* zero_block() {
@@ -152,18 +163,24 @@ __device__ __forceinline__ int64_t source_row(const GroupedMm& g, int p) {
 }
 
 // WM x WN wavefronts, each with RF x FF fragments of 16 x 16 outputs.
-template <int KIND, int WM_, int WN_, int RF_, int FF_, int NST_>
+template <int KIND, int WM_, int WN_, int RF_, int FF_, int NST_, int SB_ = 128, bool PP_ = false>
 struct Cfg {
   static constexpr int K = KIND, WM = WM_, WN = WN_, RF = RF_, FF = FF_, NST = NST_;
+  static constexpr bool PP = PP_;      // the two halves of the workgroup in turn
+  static constexpr int SB = SB_;       // bytes of the contraction per stage and row
+  static constexpr int SR = SB / 2;    // the same as bf16 elements
+  static constexpr int KK = SB / 64;   // matrix instructions' halves of a stage
+  static constexpr int CPR = SB / 16;  // 16-byte chunks of it
   static constexpr int BM = WM * RF * 16;
-  static constexpr bool RT = KIND == kWeights;                     // R contiguous along m
-  static constexpr bool FT = KIND == kInput || KIND == kWeights;   // F contiguous along n
+  static constexpr bool DW = KIND == kWeights || KIND == kWeightsBy;
+  static constexpr bool RT = DW;                    // R contiguous along m
+  static constexpr bool FT = DW || KIND == kInput;  // F contiguous along n
   static constexpr bool F8 = KIND == kCodes || KIND == kCodesF32;
-  static constexpr int RBytes = BM * kStageBytes, FBytes = kBN * kStageBytes;
+  static constexpr int RBytes = BM * SB, FBytes = kBN * SB;
   static constexpr int SBytes = F8 ? kThreads * 4 : 0;  // a stage's row scales
   static constexpr int Stage = RBytes + FBytes + SBytes;
-  static constexpr int RI = BM >= 64 ? BM / 64 : 1;  // R fetches per wavefront and stage
-  static constexpr int FI = 4;
+  static constexpr int RI = RBytes >= 8192 ? RBytes / 8192 : 1;  // fetches per wavefront, stage
+  static constexpr int FI = FBytes / 8192;
   static constexpr int Fetches = RI + FI + (F8 ? 1 : 0);
   static_assert(WM * WN == kWaves && WN * FF * 16 == kBN, "tile");
   static_assert(Stage * NST <= 160 * 1024 - 256, "LDS");
@@ -173,7 +190,11 @@ struct Cfg {
 // c ^ ((r >> 1) & 7), so the 16 rows a fragment read touches at once lie in
 // different banks.  The DMA writes LDS in lane order; the lanes pick their
 // sources accordingly.
-__device__ __forceinline__ int kc_slot(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+// With 64-byte rows four rows share the banks: c ^ ((r >> 2) & 3).
+template <int SB>
+__device__ __forceinline__ int kc_slot(int row, int chunk) {
+  return SB == 128 ? chunk ^ ((row >> 1) & 7) : chunk ^ ((row >> 2) & 3);
+}
 // ... of the [64][columns] layout: 32-byte segment s of row r is stored at
 // s ^ f(r), f from the three bits in which the eight rows that a transposing
 // read of half a wavefront touches differ.
@@ -201,12 +222,13 @@ __device__ __forceinline__ void fetch(const Src<NI>& s, int stage, int limit, ui
   }
 }
 
-// One operand fragment: 16 rows x 64 contraction bytes (half `kk` of a
+// One operand fragment: 16 rows x 64 contraction bytes (part `kk` of a
 // stage), 16 bytes per lane.
+template <int SB>
 __device__ __forceinline__ u32x4_t frag_k(const uint8_t* st, int row0, int kk, int lane) {
   const int row = row0 + (lane & 15);
-  return *reinterpret_cast<const u32x4_t*>(st + row * kStageBytes +
-                                           (kc_slot(row, kk * 4 + (lane >> 4)) << 4));
+  return *reinterpret_cast<const u32x4_t*>(st + row * SB +
+                                           (kc_slot<SB>(row, kk * 4 + (lane >> 4)) << 4));
 }
 // ... of the [64][width] layout: 16 columns x 32 of the contraction.  Two
 // transposing reads; in each, 16 lanes name four rows of 16 columns and get
@@ -231,13 +253,13 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   const int wm = wv % C::WM, wn = wv / C::WM;
   const int elem = C::F8 ? 1 : 2;
   const int64_t wsz = static_cast<int64_t>(g.N) * g.K * elem;
-  const int red = C::K == kWeights ? gb - ga : C::K == kInput ? g.N : g.K;
+  const int red = C::DW ? gb - ga : C::K == kInput ? g.N : g.K;
   const int red_bytes = C::RT ? 0 : red * elem;
-  const int stages = C::RT ? (red + 63) / 64 : (red_bytes + kStageBytes - 1) / kStageBytes;
+  const int stages = C::RT ? (red + C::SR - 1) / C::SR : (red_bytes + C::SB - 1) / C::SB;
   const uint32_t lds0 = lds_addr(smem);
 
   // ---- sources
-  constexpr int kUnitK = kStageBytes, kUnitMN = 64;
+  constexpr int kUnitK = C::SB, kUnitMN = C::SR;
   Src<C::RI> rs;
   Src<C::FI> fs;
   const uint8_t* sp = zero_block();  // this lane's row scale
@@ -259,7 +281,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   using NR = std::integral_constant<int, C::RI>;
   using NF = std::integral_constant<int, C::FI>;
   if constexpr (C::RT) {
-    rs.step = 64 * g.N * 2;
+    rs.step = C::SR * g.N * 2;
 #pragma unroll
     for (int j = 0; j < C::RI; ++j) {
       const int row = mn_row(WR{}, NR{}, j), col = m0 + mn_col(WR{}, row);
@@ -267,11 +289,11 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       rs.p[j] = g.r + (static_cast<int64_t>(ga + row) * g.N + col) * 2;
     }
   } else {
-    rs.step = kStageBytes;
+    rs.step = C::SB;
 #pragma unroll
     for (int j = 0; j < C::RI; ++j) {
-      const int row = ((wv * C::RI + j) * 8 + (lane >> 3)) % C::BM;
-      const int chunk = kc_slot(row, lane & 7) << 4;
+      const int row = ((wv * C::RI + j) * (kWave / C::CPR) + lane / C::CPR) % C::BM;
+      const int chunk = kc_slot<C::SB>(row, lane % C::CPR) << 4;
       int64_t src = -1;
       if (m0 + row < mend) src = C::K == kInput ? m0 + row : source_row(g, m0 + row);
       rs.off[j] = src >= 0 ? chunk : kNever;
@@ -286,33 +308,35 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       }
     }
   }
-  int next_row[C::FI];  // gathered F: rows entries of the stage after the next
-  const bool gather = C::K == kWeights && g.rows;
+  // gathered F: the next stage's entries of rows, this wavefront's consecutive
+  // ones, by scalar loads (a vector load's wait would drain the fetches)
+  constexpr int kWaveRows = C::K == kWeightsBy ? C::FBytes / (kBN * 2) / kWaves : 1;
+  uint32_t next_row[kWaveRows];
   auto load_rows = [&](int stage) {
 #pragma unroll
-    for (int j = 0; j < C::FI; ++j) {
-      const int k = stage * 64 + mn_row(WF{}, NF{}, j);
-      next_row[j] = k < red ? g.rows[ga + k] : -1;
+    for (int j = 0; j < kWaveRows; ++j) {
+      const int k = stage * C::SR + wv * kWaveRows + j;
+      next_row[j] = k < red ? static_cast<uint32_t>(((const_i32*)g.rows)[ga + k]) : ~0u;
     }
   };
   if constexpr (C::FT) {
-    fs.step = 64 * g.K * 2;
+    fs.step = C::SR * g.K * 2;
 #pragma unroll
     for (int j = 0; j < C::FI; ++j) {
       const int row = mn_row(WF{}, NF{}, j), col = n0 + mn_col(WF{}, row);
       fs.off[j] = col < g.K ? row : kNever;
-      if (gather)
+      if (C::K == kWeightsBy)
         fs.p[j] = g.f + static_cast<int64_t>(col) * 2;
       else
         fs.p[j] = g.f + (C::K == kInput ? e * wsz : 0) +
                   (static_cast<int64_t>(C::K == kInput ? row : ga + row) * g.K + col) * 2;
     }
   } else {
-    fs.step = kStageBytes;
+    fs.step = C::SB;
 #pragma unroll
     for (int j = 0; j < C::FI; ++j) {
-      const int row = (wv * C::FI + j) * 8 + (lane >> 3);
-      const int chunk = kc_slot(row, lane & 7) << 4;
+      const int row = (wv * C::FI + j) * (kWave / C::CPR) + lane / C::CPR;
+      const int chunk = kc_slot<C::SB>(row, lane % C::CPR) << 4;
       fs.off[j] = n0 + row < g.N ? chunk : kNever;
       fs.p[j] = g.f + e * wsz + static_cast<int64_t>(n0 + row) * red_bytes + chunk;
     }
@@ -320,19 +344,22 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   auto issue = [&](int stage, int buf) {
     const uint32_t lds = lds0 + buf * C::Stage;
     if constexpr (C::RT)
-      fetch<C::RI, kUnitMN>(rs, stage, red, lds, wv * C::RI, 64);
+      fetch<C::RI, kUnitMN>(rs, stage, red, lds, wv * C::RI, C::RBytes / 1024);
     else
-      fetch<C::RI, kUnitK>(rs, stage, red_bytes, lds, wv * C::RI, C::BM / 8);
+      fetch<C::RI, kUnitK>(rs, stage, red_bytes, lds, wv * C::RI, C::RBytes / 1024);
     if constexpr (!C::FT) {
-      fetch<C::FI, kUnitK>(fs, stage, red_bytes, lds + C::RBytes, wv * C::FI, kBN / 8);
-    } else if (!gather) {
-      fetch<C::FI, kUnitMN>(fs, stage, red, lds + C::RBytes, wv * C::FI, 64);
+      fetch<C::FI, kUnitK>(fs, stage, red_bytes, lds + C::RBytes, wv * C::FI, C::FBytes / 1024);
+    } else if constexpr (C::K != kWeightsBy) {
+      fetch<C::FI, kUnitMN>(fs, stage, red, lds + C::RBytes, wv * C::FI, C::FBytes / 1024);
     } else {
 #pragma unroll
-      for (int j = 0; j < C::FI; ++j) {
-        const uint32_t r = static_cast<uint32_t>(next_row[j]);
-        const uint8_t* p = fs.p[j] + static_cast<int64_t>(row_div(r, g.div_magic)) * g.K * 2;
-        dma16(fs.off[j] != kNever && r < g.row_limit ? p : zero_block(),
+      for (int j = 0; j < C::FI; ++j) {  // two rows per fetch, half a wavefront each
+        static_assert(kWaveRows == 2 * C::FI, "rows per fetch");
+        const uint32_t r0 = next_row[2 * j], r1 = next_row[2 * j + 1];
+        const int64_t b0 = r0 < g.row_limit ? static_cast<int64_t>(row_div(r0, g.div_magic)) : -1;
+        const int64_t b1 = r1 < g.row_limit ? static_cast<int64_t>(row_div(r1, g.div_magic)) : -1;
+        const int64_t src = lane < kWave / 2 ? b0 : b1;
+        dma16(fs.off[j] != kNever && src >= 0 ? fs.p[j] + src * g.K * 2 : zero_block(),
               lds + C::RBytes + (wv * C::FI + j) * 1024);
       }
       load_rows(stage + 1);
@@ -341,7 +368,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       dma4(stage < stages ? sp + stage * sstep : zero_block(),
            lds + C::RBytes + C::FBytes + wv * 256);
   };
-  if (gather) load_rows(0);
+  if constexpr (C::K == kWeightsBy) load_rows(0);
 
   f32x4_t acc[C::RF][C::FF];
 #pragma unroll
@@ -364,7 +391,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       for (int j = 0; j < C::FF; ++j)
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-          const u32x4_t v = frag_k(sf, nw + j * 16, kk, lane);
+          const u32x4_t v = frag_k<C::SB>(sf, nw + j * 16, kk, lane);
           fa[j][2 * kk] = codes_to_bf16(v[0], v[1]);
           fa[j][2 * kk + 1] = codes_to_bf16(v[2], v[3]);
         }
@@ -373,7 +400,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
         bf16x8_t rb[4];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-          const u32x4_t v = frag_k(sr, mw + i * 16, kk, lane);
+          const u32x4_t v = frag_k<C::SB>(sr, mw + i * 16, kk, lane);
           rb[2 * kk] = codes_to_bf16(v[0], v[1]);
           rb[2 * kk + 1] = codes_to_bf16(v[2], v[3]);
         }
@@ -394,12 +421,12 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       i32x8_t fa[C::FF];
 #pragma unroll
       for (int j = 0; j < C::FF; ++j) {
-        const u32x4_t lo = frag_k(sf, nw + j * 16, 0, lane), hi = frag_k(sf, nw + j * 16, 1, lane);
+        const u32x4_t lo = frag_k<C::SB>(sf, nw + j * 16, 0, lane), hi = frag_k<C::SB>(sf, nw + j * 16, 1, lane);
         fa[j] = __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
       }
 #pragma unroll
       for (int i = 0; i < C::RF; ++i) {
-        const u32x4_t lo = frag_k(sr, mw + i * 16, 0, lane), hi = frag_k(sr, mw + i * 16, 1, lane);
+        const u32x4_t lo = frag_k<C::SB>(sr, mw + i * 16, 0, lane), hi = frag_k<C::SB>(sr, mw + i * 16, 1, lane);
         const i32x8_t rb =
             __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         const float s = rsc[mw + i * 16 + (lane & 15)] * ws;
@@ -413,14 +440,14 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       }
     } else {
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int kk = 0; kk < C::KK; ++kk) {
         bf16x8_t fa[C::FF];
 #pragma unroll
         for (int j = 0; j < C::FF; ++j) {
           if constexpr (C::FT)
             fa[j] = __builtin_bit_cast(bf16x8_t, frag_mn<kBN>(sf, nw + j * 16, kk, lane));
           else
-            fa[j] = __builtin_bit_cast(bf16x8_t, frag_k(sf, nw + j * 16, kk, lane));
+            fa[j] = __builtin_bit_cast(bf16x8_t, frag_k<C::SB>(sf, nw + j * 16, kk, lane));
         }
 #pragma unroll
         for (int i = 0; i < C::RF; ++i) {
@@ -428,7 +455,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
           if constexpr (C::RT)
             rb = __builtin_bit_cast(bf16x8_t, frag_mn<C::BM>(sr, mw + i * 16, kk, lane));
           else
-            rb = __builtin_bit_cast(bf16x8_t, frag_k(sr, mw + i * 16, kk, lane));
+            rb = __builtin_bit_cast(bf16x8_t, frag_k<C::SB>(sr, mw + i * 16, kk, lane));
 #pragma unroll
           for (int j = 0; j < C::FF; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[j], rb, acc[i][j], 0, 0, 0);
@@ -437,18 +464,60 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     }
   };
 
-  // ---- the loop: NST - 1 stages in flight; one meeting per stage, after
-  // which the buffer of the stage before is free
+  if constexpr (C::PP) {
+    // ---- the loop of the two halves in turn: wavefronts 0..3 and 4..7 (one of
+    // each on every SIMD) run half a stage apart, so that while one half's
+    // matrix instructions run, the other reads its operands from LDS.  Three
+    // stages are in flight; a stage's buffer is fetched into after its last
+    // reader has its data.
+    static_assert(C::KK == 1 && !C::F8 && C::NST == 4, "buffers");
+    issue(0, 0);
+    issue(1, 1);
+    issue(2, 2);
+    wait_and_meet<2 * C::Fetches>();  // stage 0 is here
+    if (wv >= kWaves / 2) asm volatile("s_barrier" ::: "memory");
+    for (int s = 0; s < stages; ++s) {
+      const uint8_t* st = smem + (s & 3) * C::Stage;
+      bf16x8_t fa[C::FF], rb[C::RF];
 #pragma unroll
-  for (int s = 0; s < C::NST - 1; ++s) issue(s, s);
-  int buf = 0;
-  for (int s = 0; s < stages; ++s) {
-    wait_and_meet<(C::NST - 2) * C::Fetches>();
-    issue(s + C::NST - 1, buf == 0 ? C::NST - 1 : buf - 1);
-    math(s, smem + buf * C::Stage);
-    buf = buf == C::NST - 1 ? 0 : buf + 1;
+      for (int j = 0; j < C::FF; ++j)
+        fa[j] = __builtin_bit_cast(
+            bf16x8_t, C::FT ? frag_mn<kBN>(st + C::RBytes, nw + j * 16, 0, lane)
+                            : frag_k<C::SB>(st + C::RBytes, nw + j * 16, 0, lane));
+#pragma unroll
+      for (int i = 0; i < C::RF; ++i)
+        rb[i] = __builtin_bit_cast(bf16x8_t, C::RT ? frag_mn<C::BM>(st, mw + i * 16, 0, lane)
+                                                   : frag_k<C::SB>(st, mw + i * 16, 0, lane));
+      issue(s + 3, (s + 3) & 3);
+      wait_fetches<2 * C::Fetches>();  // this wavefront's part of stage s + 1
+      reads_and_meet();
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int i = 0; i < C::RF; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FF; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[j], rb[i], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (wv < kWaves / 2) asm volatile("s_barrier" ::: "memory");
+    wait_and_meet<0>();  // no fetch into LDS outlives the tile
+  } else {
+    // ---- the loop: NST - 1 stages in flight; one meeting per stage, after
+    // which the buffer of the stage before is free
+#pragma unroll
+    for (int s = 0; s < C::NST - 1; ++s) issue(s, s);
+    int buf = 0;
+    for (int s = 0; s < stages; ++s) {
+      wait_and_meet<(C::NST - 2) * C::Fetches>();
+      issue(s + C::NST - 1, buf == 0 ? C::NST - 1 : buf - 1);
+      math(s, smem + buf * C::Stage);
+      buf = buf == C::NST - 1 ? 0 : buf + 1;
+    }
+    wait_and_meet<0>();  // no fetch into LDS outlives the tile
   }
-  wait_and_meet<0>();  // no fetch into LDS outlives the tile
 
   // ---- store: lane holds columns n .. n + 3 of row m
   const int cols = C::FT ? g.K : g.N;
@@ -456,7 +525,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   for (int i = 0; i < C::RF; ++i) {
     const int m = m0 + mw + i * 16 + (lane & 15);
     if (m >= mend) continue;
-    const int64_t row = C::K == kWeights ? static_cast<int64_t>(e) * g.N + m : m;
+    const int64_t row = C::DW ? static_cast<int64_t>(e) * g.N + m : m;
 #pragma unroll
     for (int j = 0; j < C::FF; ++j) {
       const int n = n0 + nw + j * 16 + (lane >> 4) * 4;
@@ -491,7 +560,8 @@ uint32_t tile_grid(int64_t tiles) {
 // holds its rows.
 constexpr int kBM = 256;
 template <int KIND>
-using T256 = Cfg<KIND, 2, 4, 8, 4, 2>;
+using T256 = std::conditional_t<(KIND <= kWeightsBy), Cfg<KIND, 2, 4, 8, 4, 4, 64, true>,
+                                Cfg<KIND, 2, 4, 8, 4, 2>>;
 template <int KIND>
 using T128 = Cfg<KIND, 2, 4, 4, 4, 3>;
 template <int KIND>
@@ -505,15 +575,16 @@ constexpr int lds_of() { return C::Stage * C::NST; }
 
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
-  constexpr int kLds = KIND == kWeights
+  constexpr bool kDw = KIND == kWeights || KIND == kWeightsBy;
+  constexpr int kLds = kDw
                            ? cmax(lds_of<T256<KIND>>(), lds_of<T128<KIND>>())
                            : cmax(cmax(lds_of<T256<KIND>>(), lds_of<T128<KIND>>()),
                                   cmax(lds_of<T64<KIND>>(), lds_of<T32<KIND>>()));
   __shared__ __align__(1024) uint8_t smem[kLds];
-  const int cols = KIND == kInput || KIND == kWeights ? g.K : g.N;
+  const int cols = kDw || KIND == kInput ? g.K : g.N;
   const int nt = (cols + kBN - 1) / kBN;
   const int64_t id = my_tile();
-  if constexpr (KIND == kWeights) {
+  if constexpr (kDw) {
     const int mt = (g.N + kBM - 1) / kBM;
     const int e = static_cast<int>(id / (mt * nt)), r = static_cast<int>(id % (mt * nt));
     if (e >= g.E) return;
@@ -540,11 +611,169 @@ __global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// A few rows (few_rows): bound by reading the weights once.  A
+// workgroup takes 16 columns of one group; its four wavefronts take turns
+// along K (256 bytes of a weight row each), load their weights straight into
+// the matrix instruction's A registers -- 16 rows x 64 bytes a load, eight
+// loads in flight -- and the group's rows of x into its B registers, 16 at a
+// time, and join their sums through LDS in a fixed order.  There is nothing
+// to share through LDS, so the loads need no barrier, and with no more than
+// 64 registers a CU holds 32 wavefronts.  e4m3 codes are widened to bf16
+// (exact) whatever y's type is: at these sizes that costs nothing.
+// ---------------------------------------------------------------------------
+
+// Against the tiles, us per call (one N = 4096, K = 6144 bf16 expert; 64 of
+// N = K = 2048; 256 of 4096 x 6144, codes): 68 rows 50 / 60, 16 rows 15 / 45;
+// 256 rows 105 / 130; 512 rows 1013 / 1138, 2048 rows 1400 / 1318.  Past about
+// 3 rows a group (64 in one) a group's second pass over its weights costs more
+// than the tiles' staging.
+bool few_rows(const GroupedMm& g) { return g.P <= 64 + 3 * g.E; }
+
+constexpr int kSkinnyThreads = 256;
+constexpr int kSkinnyWaves = kSkinnyThreads / kWave;
+
+// Expert of the slot-th group that holds rows (each wavefront for itself).
+__device__ __forceinline__ int find_slot(const GroupedMm& g, int slot, int lane) {
+  for (int e0 = 0; e0 < g.E; e0 += kWave) {
+    const int e = e0 + lane;
+    int a = 0, b = 0;
+    if (e < g.E) group_bounds(g, e, a, b);
+    uint64_t m = __ballot(b > a);
+    const int n = __popcll(m);
+    if (slot < n) {
+      for (; slot > 0; --slot) m &= m - 1;
+      return e0 + __ffsll(static_cast<unsigned long long>(m)) - 1;
+    }
+    slot -= n;
+  }
+  return -1;
+}
+
+template <int KIND>
+struct Skinny {
+  static constexpr bool F8 = KIND != kRows;
+  static constexpr int kFrags = F8 ? 2 : 1;  // fragments of 16 columns per wavefront
+  static constexpr int kCols = 16 * kFrags;
+  static constexpr int kChunk = F8 ? 16 : 8;  // contraction elements per lane and load
+  static constexpr int kLoads = 4;            // loads per turn and fragment
+  static constexpr int kOcc = F8 ? 4 : 8;     // wavefronts per SIMD: 64 registers for bf16
+  static constexpr int kSpan = kLoads * kChunk * 4;  // contraction elements of a turn
+};
+
+template <int KIND>
+__global__ __launch_bounds__(kSkinnyThreads, Skinny<KIND>::kOcc) void grouped_skinny(GroupedMm g, int nb) {
+  using C = Skinny<KIND>;
+  constexpr bool F8 = C::F8;
+  __shared__ float part[kSkinnyWaves][16][C::kCols + 1];
+  const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave;
+  const int e = __builtin_amdgcn_readfirstlane(find_slot(g, blockIdx.x / nb, lane));
+  if (e < 0) return;
+  int a, b;
+  group_bounds(g, e, a, b);
+  const int n0 = (blockIdx.x % nb) * C::kCols, elem = F8 ? 1 : 2;
+  const int i16 = lane & 15, q = lane >> 4;
+  const int64_t ld = static_cast<int64_t>(g.K) * elem;
+  const uint8_t* wp[C::kFrags];
+#pragma unroll
+  for (int f = 0; f < C::kFrags; ++f)  // columns past N repeat the last
+    wp[f] = g.f + (static_cast<int64_t>(e) * g.N + min(n0 + f * 16 + i16, g.N - 1)) * ld + q * 16;
+  const int kb = (g.K + kBlock - 1) / kBlock;
+  const float* ws = F8 ? g.f_scale + (static_cast<int64_t>(e) * ((g.N + kBlock - 1) / kBlock) +
+                                      n0 / kBlock) * kb
+                       : nullptr;
+  for (int m0 = a; m0 < b; m0 += 16) {
+    int64_t src = -1;
+    if (m0 + i16 < b) src = source_row(g, m0 + i16);
+    const uint8_t* xp = g.r + (src < 0 ? 0 : src) * ld + q * 16;
+    f32x4_t acc[C::kFrags];
+#pragma unroll
+    for (int f = 0; f < C::kFrags; ++f) acc[f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = wv * C::kSpan; k0 < g.K; k0 += kSkinnyWaves * C::kSpan) {
+      u32x4_t w[C::kFrags][C::kLoads], x[C::kLoads];
+#pragma unroll
+      for (int u = 0; u < C::kLoads; ++u) {
+        const int k = k0 + u * 4 * C::kChunk;
+        const bool in = k + q * C::kChunk < g.K;
+        x[u] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int f = 0; f < C::kFrags; ++f) {
+          w[f][u] = u32x4_t{0, 0, 0, 0};
+          if (in)
+            w[f][u] = *reinterpret_cast<const u32x4_t*>(wp[f] + static_cast<int64_t>(k) * elem);
+        }
+        if (in && src >= 0)
+          x[u] = *reinterpret_cast<const u32x4_t*>(xp + static_cast<int64_t>(k) * elem);
+      }
+      if constexpr (F8) {
+#pragma unroll
+        for (int h = 0; h < C::kLoads / 2; ++h) {
+          const int blk = k0 / kBlock + h;
+          if (blk >= kb) break;
+          const float s = src >= 0 ? ws[blk] * g.r_scale[src * kb + blk] : 0.0f;
+          f32x4_t p[C::kFrags];
+#pragma unroll
+          for (int f = 0; f < C::kFrags; ++f) p[f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int u = 2 * h; u < 2 * h + 2; ++u)
+#pragma unroll
+            for (int v = 0; v < 4; v += 2) {
+              const bf16x8_t xb = codes_to_bf16(x[u][v], x[u][v + 1]);
+#pragma unroll
+              for (int f = 0; f < C::kFrags; ++f)
+                p[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    codes_to_bf16(w[f][u][v], w[f][u][v + 1]), xb, p[f], 0, 0, 0);
+            }
+#pragma unroll
+          for (int f = 0; f < C::kFrags; ++f)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[f][j] = fmaf(s, p[f][j], acc[f][j]);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < C::kLoads; ++u)
+#pragma unroll
+          for (int f = 0; f < C::kFrags; ++f)
+            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8_t, w[f][u]), __builtin_bit_cast(bf16x8_t, x[u]), acc[f],
+                0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < C::kFrags; ++f)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[wv][i16][f * 16 + q * 4 + j] = acc[f][j];
+    __syncthreads();
+#pragma unroll
+    for (int o = t; o < 16 * C::kCols; o += kSkinnyThreads) {
+      const int m = m0 + o / C::kCols, n = n0 + o % C::kCols;
+      if (m >= b || n >= g.N) continue;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kSkinnyWaves; ++w) v += part[w][o / C::kCols][o % C::kCols];
+      const int64_t at = static_cast<int64_t>(m) * g.N + n;
+      if (g.out_f32)
+        static_cast<float*>(g.out)[at] = v;
+      else
+        static_cast<uint16_t*>(g.out)[at] = f32_to_bf16(v);
+    }
+    __syncthreads();
+  }
+}
+
 }  // namespace
 
 size_t grouped_dw_workspace(int, int, int, int) { return 0; }
 
 hipError_t launch_grouped_mm(const GroupedMm& g, GroupedKind kind, hipStream_t stream) {
+  if ((kind == kGroupedRows || kind == kGroupedCodes) && few_rows(g)) {
+    const int cols = kind == kGroupedRows ? Skinny<kRows>::kCols : Skinny<kCodesF32>::kCols;
+    const int nb = (g.N + cols - 1) / cols;
+    const dim3 grid(static_cast<uint32_t>(nb * (g.E < g.P ? g.E : g.P))), block(kSkinnyThreads);
+    return kind == kGroupedRows
+               ? launch(grouped_skinny<kRows>, grid, block, 0, stream, g, nb)
+               : launch(grouped_skinny<kCodesF32>, grid, block, 0, stream, g, nb);
+  }
   const int cols = kind == kGroupedInput || kind == kGroupedWeights ? g.K : g.N;
   const int64_t nt = (cols + kBN - 1) / kBN;
   int64_t mt;
@@ -556,7 +785,9 @@ hipError_t launch_grouped_mm(const GroupedMm& g, GroupedKind kind, hipStream_t s
   switch (kind) {
     case kGroupedRows: return launch(grouped_tiles<kRows>, grid, block, 0, stream, g);
     case kGroupedInput: return launch(grouped_tiles<kInput>, grid, block, 0, stream, g);
-    case kGroupedWeights: return launch(grouped_tiles<kWeights>, grid, block, 0, stream, g);
+    case kGroupedWeights:
+      return g.rows ? launch(grouped_tiles<kWeightsBy>, grid, block, 0, stream, g)
+                    : launch(grouped_tiles<kWeights>, grid, block, 0, stream, g);
     case kGroupedCodes:
       return g.out_f32 ? launch(grouped_tiles<kCodesF32>, grid, block, 0, stream, g)
                        : launch(grouped_tiles<kCodes>, grid, block, 0, stream, g);
