@@ -37,9 +37,6 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 typedef const __attribute__((address_space(4))) int32_t const_i32;  // by scalar loads
 
-constexpr int kThreads = 512;  // 8 wavefronts
-constexpr int kWaves = kThreads / kWave;
-constexpr int kBN = 256;          // output columns per tile
 constexpr int kBlock = 128;       // columns (and weight rows) per scale
 
 // What a fetch past an operand's end reads.
@@ -103,6 +100,10 @@ __device__ __forceinline__ bf16x8_t codes_to_bf16(uint32_t lo, uint32_t hi) {
   return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return f32_to_bf16(lo) | (static_cast<uint32_t>(f32_to_bf16(hi)) << 16);
+}
+
 struct Group {
   int e, a, b;  // expert, its grouped positions
   int t;        // this workgroup's tile of the group
@@ -115,42 +116,63 @@ __device__ __forceinline__ void group_bounds(const GroupedMm& g, int e, int& a, 
   b = min(max(g.offsets[e + 1], a), g.P);
 }
 
-// Which group holds row tile `tile` (groups in ascending order, ceil(rows /
-// BM) tiles each): every thread takes two groups, a scan over the workgroup
-// gives their first tiles, and the owner tells the others.  e = -1 past the
-// last tile.
-template <int BM>
-__device__ Group find_group(const GroupedMm& g, int tile, int* sh) {
+// Which group holds row tile `tile`: every thread takes two groups, a scan
+// over the workgroup gives their first tiles, and the owner tells the others.
+// e = -1 past the last tile.  Groups have ceil(rows / BM) tiles, in ascending
+// order of the groups; with `tall_first`, the tiles of more than BM / 2 rows
+// come before all others.
+template <int BM, int THREADS>
+__device__ Group find_group(const GroupedMm& g, int64_t tile, bool tall_first, int* sh) {
+  constexpr int kPer = 1024 / THREADS, kWaves = THREADS / kWave;  // E <= 1024
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave;
-  int a[2] = {0, 0}, b[2] = {0, 0}, n[2] = {0, 0};
+  int a[kPer], b[kPer], n[kPer], low[kPer], inc = 0, inc_low = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (2 * t + i < g.E) {
-      group_bounds(g, 2 * t + i, a[i], b[i]);
-      n[i] = (b[i] - a[i] + BM - 1) / BM;
-    }
-  int inc = n[0] + n[1];
-  for (int off = 1; off < kWave; off <<= 1) {
-    const int v = __shfl_up(inc, off, kWave);
-    if (lane >= off) inc += v;
+  for (int i = 0; i < kPer; ++i) {
+    a[i] = b[i] = 0;
+    if (kPer * t + i < g.E) group_bounds(g, kPer * t + i, a[i], b[i]);
+    n[i] = (b[i] - a[i] + BM - 1) / BM;
+    const int rest = (b[i] - a[i]) % BM;
+    low[i] = tall_first && rest > 0 && rest <= BM / 2;  // its last tile goes to the end
+    n[i] -= low[i];
+    inc += n[i];
+    inc_low += low[i];
   }
-  if (t == 0) sh[kWaves] = -1;
-  if (lane == kWave - 1) sh[wv] = inc;
+  const int mine = inc, mine_low = inc_low;
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int v = __shfl_up(inc, off, kWave), u = __shfl_up(inc_low, off, kWave);
+    if (lane >= off) {
+      inc += v;
+      inc_low += u;
+    }
+  }
+  if (t == 0) sh[2 * kWaves] = -1;
+  if (lane == kWave - 1) {
+    sh[wv] = inc;
+    sh[kWaves + wv] = inc_low;
+  }
   __syncthreads();
-  int first = inc - n[0] - n[1];
-  for (int w = 0; w < wv; ++w) first += sh[w];
+  int first = inc - mine, first_low = inc_low - mine_low;
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wv) {
+      first += sh[w];
+      first_low += sh[kWaves + w];
+    }
+    first_low += sh[w];  // behind all the others
+  }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (tile >= first && tile < first + n[i]) {
-      sh[kWaves] = 2 * t + i;
-      sh[kWaves + 1] = a[i];
-      sh[kWaves + 2] = b[i];
-      sh[kWaves + 3] = tile - first;
+  for (int i = 0; i < kPer; ++i) {
+    const bool mid = tile >= first && tile < first + n[i], end = low[i] && tile == first_low;
+    if (mid || end) {
+      sh[2 * kWaves] = kPer * t + i;
+      sh[2 * kWaves + 1] = a[i];
+      sh[2 * kWaves + 2] = b[i];
+      sh[2 * kWaves + 3] = mid ? static_cast<int>(tile) - first : n[i];
     }
     first += n[i];
+    first_low += low[i];
   }
   __syncthreads();
-  Group r{sh[kWaves], sh[kWaves + 1], sh[kWaves + 2], sh[kWaves + 3]};
+  Group r{sh[2 * kWaves], sh[2 * kWaves + 1], sh[2 * kWaves + 2], sh[2 * kWaves + 3]};
   __syncthreads();
   return r;
 }
@@ -171,19 +193,19 @@ struct Cfg {
   static constexpr int SR = SB / 2;    // the same as bf16 elements
   static constexpr int KK = SB / 64;   // matrix instructions' halves of a stage
   static constexpr int CPR = SB / 16;  // 16-byte chunks of it
-  static constexpr int BM = WM * RF * 16;
+  static constexpr int Waves = WM * WN, Threads = Waves * kWave;
+  static constexpr int BM = WM * RF * 16, BN = WN * FF * 16;
   static constexpr bool DW = KIND == kWeights || KIND == kWeightsBy;
   static constexpr bool RT = DW;                    // R contiguous along m
   static constexpr bool FT = DW || KIND == kInput;  // F contiguous along n
   static constexpr bool F8 = KIND == kCodes || KIND == kCodesF32;
-  static constexpr int RBytes = BM * SB, FBytes = kBN * SB;
-  static constexpr int SBytes = F8 ? kThreads * 4 : 0;  // a stage's row scales
+  static constexpr int RBytes = BM * SB, FBytes = BN * SB;
+  static constexpr int SBytes = F8 ? Threads * 4 : 0;  // a stage's row scales
   static constexpr int Stage = RBytes + FBytes + SBytes;
-  static constexpr int RI = RBytes >= 8192 ? RBytes / 8192 : 1;  // fetches per wavefront, stage
-  static constexpr int FI = FBytes / 8192;
+  static constexpr int RI = RBytes >= Waves * 1024 ? RBytes / (Waves * 1024) : 1;  // fetches per wavefront, stage
+  static constexpr int FI = FBytes / (Waves * 1024);
   static constexpr int Fetches = RI + FI + (F8 ? 1 : 0);
-  static_assert(WM * WN == kWaves && WN * FF * 16 == kBN, "tile");
-  static_assert(Stage * NST <= 160 * 1024 - 256, "LDS");
+  static_assert(Stage * NST <= 160 * 1024, "LDS");
 };
 
 // Swizzle of the [row][128 bytes] layout: chunk c of row r is stored at
@@ -243,7 +265,7 @@ __device__ __forceinline__ u32x4_t frag_mn(const uint8_t* st, int col0, int kk, 
   return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Output tile [m0, mend) x [n0, n0 + 256) of a group whose contraction is
+// Output tile [m0, mend) x [n0, n0 + BN) of a group whose contraction is
 // [0, red) (kWeights: positions [ga, gb)).
 template <class C>
 __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend, int n0, int ga,
@@ -277,7 +299,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     return ((((c >> 1) ^ mn_swz(row)) << 1) | (c & 1)) * 8;
   };
   using WR = std::integral_constant<int, C::RT ? C::BM : 128>;
-  using WF = std::integral_constant<int, kBN>;
+  using WF = std::integral_constant<int, C::BN>;
   using NR = std::integral_constant<int, C::RI>;
   using NF = std::integral_constant<int, C::FI>;
   if constexpr (C::RT) {
@@ -310,7 +332,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   }
   // gathered F: the next stage's entries of rows, this wavefront's consecutive
   // ones, by scalar loads (a vector load's wait would drain the fetches)
-  constexpr int kWaveRows = C::K == kWeightsBy ? C::FBytes / (kBN * 2) / kWaves : 1;
+  constexpr int kWaveRows = C::K == kWeightsBy ? C::FBytes / (C::BN * 2) / C::Waves : 1;
   uint32_t next_row[kWaveRows];
   auto load_rows = [&](int stage) {
 #pragma unroll
@@ -354,7 +376,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     } else {
 #pragma unroll
       for (int j = 0; j < C::FI; ++j) {  // two rows per fetch, half a wavefront each
-        static_assert(kWaveRows == 2 * C::FI, "rows per fetch");
+        static_assert(kWaveRows == 2 * C::FI, "rows of 512 bytes");
         const uint32_t r0 = next_row[2 * j], r1 = next_row[2 * j + 1];
         const int64_t b0 = r0 < g.row_limit ? static_cast<int64_t>(row_div(r0, g.div_magic)) : -1;
         const int64_t b1 = r1 < g.row_limit ? static_cast<int64_t>(row_div(r1, g.div_magic)) : -1;
@@ -445,7 +467,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
 #pragma unroll
         for (int j = 0; j < C::FF; ++j) {
           if constexpr (C::FT)
-            fa[j] = __builtin_bit_cast(bf16x8_t, frag_mn<kBN>(sf, nw + j * 16, kk, lane));
+            fa[j] = __builtin_bit_cast(bf16x8_t, frag_mn<C::BN>(sf, nw + j * 16, kk, lane));
           else
             fa[j] = __builtin_bit_cast(bf16x8_t, frag_k<C::SB>(sf, nw + j * 16, kk, lane));
         }
@@ -470,26 +492,26 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     // matrix instructions run, the other reads its operands from LDS.  Three
     // stages are in flight; a stage's buffer is fetched into after its last
     // reader has its data.
-    static_assert(C::KK == 1 && !C::F8 && C::NST == 4, "buffers");
-    issue(0, 0);
-    issue(1, 1);
-    issue(2, 2);
-    wait_and_meet<2 * C::Fetches>();  // stage 0 is here
-    if (wv >= kWaves / 2) asm volatile("s_barrier" ::: "memory");
+    static_assert(C::KK == 1 && !C::F8, "one matrix instruction a stage");
+#pragma unroll
+    for (int s = 0; s < C::NST - 1; ++s) issue(s, s);
+    wait_and_meet<(C::NST - 2) * C::Fetches>();  // stage 0 is here
+    if (wv >= C::Waves / 2) asm volatile("s_barrier" ::: "memory");
+    int buf = 0;
     for (int s = 0; s < stages; ++s) {
-      const uint8_t* st = smem + (s & 3) * C::Stage;
+      const uint8_t* st = smem + buf * C::Stage;
       bf16x8_t fa[C::FF], rb[C::RF];
 #pragma unroll
       for (int j = 0; j < C::FF; ++j)
         fa[j] = __builtin_bit_cast(
-            bf16x8_t, C::FT ? frag_mn<kBN>(st + C::RBytes, nw + j * 16, 0, lane)
+            bf16x8_t, C::FT ? frag_mn<C::BN>(st + C::RBytes, nw + j * 16, 0, lane)
                             : frag_k<C::SB>(st + C::RBytes, nw + j * 16, 0, lane));
 #pragma unroll
       for (int i = 0; i < C::RF; ++i)
         rb[i] = __builtin_bit_cast(bf16x8_t, C::RT ? frag_mn<C::BM>(st, mw + i * 16, 0, lane)
                                                    : frag_k<C::SB>(st, mw + i * 16, 0, lane));
-      issue(s + 3, (s + 3) & 3);
-      wait_fetches<2 * C::Fetches>();  // this wavefront's part of stage s + 1
+      issue(s + C::NST - 1, buf == 0 ? C::NST - 1 : buf - 1);
+      wait_fetches<(C::NST - 2) * C::Fetches>();  // this wavefront's part of stage s + 1
       reads_and_meet();
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -501,8 +523,9 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       __builtin_amdgcn_sched_barrier(0);
       asm volatile("s_barrier" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
+      buf = buf == C::NST - 1 ? 0 : buf + 1;
     }
-    if (wv < kWaves / 2) asm volatile("s_barrier" ::: "memory");
+    if (wv < C::Waves / 2) asm volatile("s_barrier" ::: "memory");
     wait_and_meet<0>();  // no fetch into LDS outlives the tile
   } else {
     // ---- the loop: NST - 1 stages in flight; one meeting per stage, after
@@ -519,25 +542,36 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     wait_and_meet<0>();  // no fetch into LDS outlives the tile
   }
 
-  // ---- store: lane holds columns n .. n + 3 of row m
+  // ---- store: a lane holds columns 4 q .. 4 q + 3 of row m of each fragment
+  // (q = lane / 16).  float32: 16 bytes each, 64 in a row of the store.  bf16:
+  // the odd 16-lane rows of one fragment trade places with the even ones of
+  // the next, after which a lane has 8 columns of one of them: 64 bytes in a
+  // row again (stores of 8 bytes per lane, 32 in a row, took twice the time).
   const int cols = C::FT ? g.K : g.N;
+  const int q = lane >> 4;
 #pragma unroll
   for (int i = 0; i < C::RF; ++i) {
     const int m = m0 + mw + i * 16 + (lane & 15);
-    if (m >= mend) continue;
-    const int64_t row = C::DW ? static_cast<int64_t>(e) * g.N + m : m;
+    const int64_t row = (C::DW ? static_cast<int64_t>(e) * g.N + m : m) * cols;
+    if (g.out_f32) {
 #pragma unroll
-    for (int j = 0; j < C::FF; ++j) {
-      const int n = n0 + nw + j * 16 + (lane >> 4) * 4;
-      if (n >= cols) continue;
-      const f32x4_t v = acc[i][j];
-      if (g.out_f32) {
-        *reinterpret_cast<f32x4_t*>(static_cast<float*>(g.out) + row * cols + n) = v;
-      } else {
-        uint2 w;
-        w.x = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
-        w.y = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + row * cols + n) = w;
+      for (int j = 0; j < C::FF; ++j) {
+        const int n = n0 + nw + j * 16 + q * 4;
+        if (m < mend && n < cols)
+          *reinterpret_cast<f32x4_t*>(static_cast<float*>(g.out) + row + n) = acc[i][j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < C::FF; j += 2) {
+        const f32x4_t u = acc[i][j], v = acc[i][j + 1];
+        const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(u[0], u[1]),
+                                                        pack_bf16(v[0], v[1]), false, false);
+        const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16(u[2], u[3]),
+                                                        pack_bf16(v[2], v[3]), false, false);
+        const int n = n0 + nw + (j + (q & 1)) * 16 + (q >> 1) * 8;
+        if (m < mend && n < cols)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + row + n) =
+              make_uint4(x[0], y[0], x[1], y[1]);
       }
     }
   }
@@ -558,7 +592,7 @@ uint32_t tile_grid(int64_t tiles) {
 
 // Row tiles are 256 high; a group's last one takes the smallest height that
 // holds its rows.
-constexpr int kBM = 256;
+constexpr int kBM = 256, kBN = 256, kThreads = 512;
 template <int KIND>
 using T256 = std::conditional_t<(KIND <= kWeightsBy), Cfg<KIND, 2, 4, 8, 4, 4, 64, true>,
                                 Cfg<KIND, 2, 4, 8, 4, 2>>;
@@ -569,34 +603,45 @@ using T64 = Cfg<KIND, 1, 8, 4, 2, 3>;
 template <int KIND>
 using T32 = Cfg<KIND, 1, 8, 2, 2, 4>;
 
+// From this many rows a group on (on average) the products bound the call, and
+// the tallest tiles go first, so that the last ones to run are short; below,
+// the weights' bytes do, and tiles in the groups' order mix both kinds of work.
+constexpr int kTallFirstRows = 192;
+
 constexpr int cmax(int a, int b) { return a > b ? a : b; }
-template <class C>
-constexpr int lds_of() { return C::Stage * C::NST; }
+template <class... C>
+constexpr int lds_of() {
+  int m = 0;
+  ((m = cmax(m, C::Stage * C::NST)), ...);
+  return m;
+}
 
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
   constexpr bool kDw = KIND == kWeights || KIND == kWeightsBy;
-  constexpr int kLds = kDw
-                           ? cmax(lds_of<T256<KIND>>(), lds_of<T128<KIND>>())
-                           : cmax(cmax(lds_of<T256<KIND>>(), lds_of<T128<KIND>>()),
-                                  cmax(lds_of<T64<KIND>>(), lds_of<T32<KIND>>()));
-  __shared__ __align__(1024) uint8_t smem[kLds];
-  const int cols = kDw || KIND == kInput ? g.K : g.N;
-  const int nt = (cols + kBN - 1) / kBN;
-  const int64_t id = my_tile();
   if constexpr (kDw) {
-    const int mt = (g.N + kBM - 1) / kBM;
+    using T = T256<KIND>;
+    using U = T128<KIND>;
+    __shared__ __align__(1024) uint8_t smem[lds_of<T, U>()];
+    const int64_t id = my_tile();
+    const int nt = (g.K + kBN - 1) / kBN, mt = (g.N + kBM - 1) / kBM;
     const int e = static_cast<int>(id / (mt * nt)), r = static_cast<int>(id % (mt * nt));
     if (e >= g.E) return;
     int a, b;
     group_bounds(g, e, a, b);
     const int m0 = (r / nt) * kBM, n0 = (r % nt) * kBN;
     if (g.N - m0 > 128)
-      tile<T256<KIND>>(g, smem, e, m0, g.N, n0, a, b);
+      tile<T>(g, smem, e, m0, g.N, n0, a, b);
     else
-      tile<T128<KIND>>(g, smem, e, m0, g.N, n0, a, b);
+      tile<U>(g, smem, e, m0, g.N, n0, a, b);
   } else {
-    const Group gr = find_group<kBM>(g, static_cast<int>(id / nt), reinterpret_cast<int*>(smem));
+    __shared__ __align__(1024)
+        uint8_t smem[lds_of<T256<KIND>, T128<KIND>, T64<KIND>, T32<KIND>>()];
+    const int64_t id = my_tile();
+    const int nt = ((KIND == kInput ? g.K : g.N) + kBN - 1) / kBN;
+    const bool tall_first = g.P >= kTallFirstRows * g.E;
+    const Group gr =
+        find_group<kBM, kThreads>(g, id / nt, tall_first, reinterpret_cast<int*>(smem));
     if (gr.e < 0) return;
     const int m0 = gr.a + gr.t * kBM, n0 = static_cast<int>(id % nt) * kBN;
     const int rows = gr.b - m0;
@@ -782,15 +827,14 @@ hipError_t launch_grouped_mm(const GroupedMm& g, GroupedKind kind, hipStream_t s
   else  // the most row tiles any grouping of P rows can have
     mt = g.P / kBM + (g.E < g.P ? g.E : g.P);
   const dim3 grid(tile_grid(mt * nt)), block(kThreads);
+  auto go = [&](auto kernel) { return launch(kernel, grid, block, 0, stream, g); };
   switch (kind) {
-    case kGroupedRows: return launch(grouped_tiles<kRows>, grid, block, 0, stream, g);
-    case kGroupedInput: return launch(grouped_tiles<kInput>, grid, block, 0, stream, g);
+    case kGroupedRows: return go(grouped_tiles<kRows>);
+    case kGroupedInput: return go(grouped_tiles<kInput>);
     case kGroupedWeights:
-      return g.rows ? launch(grouped_tiles<kWeightsBy>, grid, block, 0, stream, g)
-                    : launch(grouped_tiles<kWeights>, grid, block, 0, stream, g);
+      return g.rows ? go(grouped_tiles<kWeightsBy>) : go(grouped_tiles<kWeights>);
     case kGroupedCodes:
-      return g.out_f32 ? launch(grouped_tiles<kCodesF32>, grid, block, 0, stream, g)
-                       : launch(grouped_tiles<kCodes>, grid, block, 0, stream, g);
+      return g.out_f32 ? go(grouped_tiles<kCodesF32>) : go(grouped_tiles<kCodes>);
   }
   return hipErrorNotSupported;
 }
