@@ -185,7 +185,9 @@ __device__ __forceinline__ int64_t source_row(const GroupedMm& g, int p) {
 }
 
 // WM x WN wavefronts, each with RF x FF fragments of 16 x 16 outputs.
-template <int KIND, int WM_, int WN_, int RF_, int FF_, int NST_, int SB_ = 128, bool PP_ = false>
+// NST stages of F in LDS and NSR (0: as many) of R.
+template <int KIND, int WM_, int WN_, int RF_, int FF_, int NST_, int SB_ = 128, bool PP_ = false,
+          int NSR_ = 0>
 struct Cfg {
   static constexpr int K = KIND, WM = WM_, WN = WN_, RF = RF_, FF = FF_, NST = NST_;
   static constexpr bool PP = PP_;      // the two halves of the workgroup in turn
@@ -202,10 +204,13 @@ struct Cfg {
   static constexpr int RBytes = BM * SB, FBytes = BN * SB;
   static constexpr int SBytes = F8 ? Threads * 4 : 0;  // a stage's row scales
   static constexpr int Stage = RBytes + FBytes + SBytes;
-  static constexpr int RI = RBytes >= Waves * 1024 ? RBytes / (Waves * 1024) : 1;  // fetches per wavefront, stage
+  static constexpr int NSR = NSR_ == 0 ? NST : NSR_;
+  static constexpr int Lds = NST * FBytes + NSR * (RBytes + SBytes);
+  // fetches per wavefront and stage; R's wrap around where they do not divide
+  static constexpr int RI = (RBytes + Waves * 1024 - 1) / (Waves * 1024);
   static constexpr int FI = FBytes / (Waves * 1024);
   static constexpr int Fetches = RI + FI + (F8 ? 1 : 0);
-  static_assert(Stage * NST <= 160 * 1024, "LDS");
+  static_assert(Lds <= 160 * 1024, "LDS");
 };
 
 // Swizzle of the [row][128 bytes] layout: chunk c of row r is stored at
@@ -363,16 +368,21 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       fs.p[j] = g.f + e * wsz + static_cast<int64_t>(n0 + row) * red_bytes + chunk;
     }
   }
-  auto issue = [&](int stage, int buf) {
-    const uint32_t lds = lds0 + buf * C::Stage;
+  // R's stage (with its row scales) to LDS at lds, F's to its own place
+  auto issue_r = [&](int stage, uint32_t lds) {
     if constexpr (C::RT)
       fetch<C::RI, kUnitMN>(rs, stage, red, lds, wv * C::RI, C::RBytes / 1024);
     else
       fetch<C::RI, kUnitK>(rs, stage, red_bytes, lds, wv * C::RI, C::RBytes / 1024);
+    if constexpr (C::F8)
+      dma4(stage < stages ? sp + stage * sstep : zero_block(),
+           lds + C::RBytes + wv * 256);
+  };
+  auto issue_f = [&](int stage, uint32_t lds) {
     if constexpr (!C::FT) {
-      fetch<C::FI, kUnitK>(fs, stage, red_bytes, lds + C::RBytes, wv * C::FI, C::FBytes / 1024);
+      fetch<C::FI, kUnitK>(fs, stage, red_bytes, lds, wv * C::FI, C::FBytes / 1024);
     } else if constexpr (C::K != kWeightsBy) {
-      fetch<C::FI, kUnitMN>(fs, stage, red, lds + C::RBytes, wv * C::FI, C::FBytes / 1024);
+      fetch<C::FI, kUnitMN>(fs, stage, red, lds, wv * C::FI, C::FBytes / 1024);
     } else {
 #pragma unroll
       for (int j = 0; j < C::FI; ++j) {  // two rows per fetch, half a wavefront each
@@ -382,13 +392,15 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
         const int64_t b1 = r1 < g.row_limit ? static_cast<int64_t>(row_div(r1, g.div_magic)) : -1;
         const int64_t src = lane < kWave / 2 ? b0 : b1;
         dma16(fs.off[j] != kNever && src >= 0 ? fs.p[j] + src * g.K * 2 : zero_block(),
-              lds + C::RBytes + (wv * C::FI + j) * 1024);
+              lds + (wv * C::FI + j) * 1024);
       }
       load_rows(stage + 1);
     }
-    if constexpr (C::F8)
-      dma4(stage < stages ? sp + stage * sstep : zero_block(),
-           lds + C::RBytes + C::FBytes + wv * 256);
+  };
+  // a stage as it lies in the rings of equal depth: R, row scales, F
+  auto issue = [&](int stage, int buf) {
+    issue_r(stage, lds0 + buf * C::Stage);
+    issue_f(stage, lds0 + buf * C::Stage + C::RBytes + C::SBytes);
   };
   if constexpr (C::K == kWeightsBy) load_rows(0);
 
@@ -403,11 +415,10 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     fsc = g.f_scale + (static_cast<int64_t>(e) * ((g.N + kBlock - 1) / kBlock) +
                        min(n0 + nw, g.N - 1) / kBlock) * stages;
 
-  auto math = [&](int stage, const uint8_t* st) {
-    const uint8_t *sr = st, *sf = st + C::RBytes;
+  auto math = [&](int stage, const uint8_t* sr, const uint8_t* sf) {
     if constexpr (C::K == kCodesF32) {
       const float ws = fsc[stage];
-      const float* rsc = reinterpret_cast<const float*>(sf + C::FBytes);
+      const float* rsc = reinterpret_cast<const float*>(sr + C::RBytes);
       bf16x8_t fa[C::FF][4];  // 16 codes of each half of the stage
 #pragma unroll
       for (int j = 0; j < C::FF; ++j)
@@ -439,7 +450,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       }
     } else if constexpr (C::F8) {
       const float ws = fsc[stage];
-      const float* rsc = reinterpret_cast<const float*>(sf + C::FBytes);
+      const float* rsc = reinterpret_cast<const float*>(sr + C::RBytes);
       i32x8_t fa[C::FF];
 #pragma unroll
       for (int j = 0; j < C::FF; ++j) {
@@ -504,8 +515,8 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
 #pragma unroll
       for (int j = 0; j < C::FF; ++j)
         fa[j] = __builtin_bit_cast(
-            bf16x8_t, C::FT ? frag_mn<C::BN>(st + C::RBytes, nw + j * 16, 0, lane)
-                            : frag_k<C::SB>(st + C::RBytes, nw + j * 16, 0, lane));
+            bf16x8_t, C::FT ? frag_mn<C::BN>(st + C::RBytes + C::SBytes, nw + j * 16, 0, lane)
+                            : frag_k<C::SB>(st + C::RBytes + C::SBytes, nw + j * 16, 0, lane));
 #pragma unroll
       for (int i = 0; i < C::RF; ++i)
         rb[i] = __builtin_bit_cast(bf16x8_t, C::RT ? frag_mn<C::BM>(st, mw + i * 16, 0, lane)
@@ -527,6 +538,24 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     }
     if (wv < C::Waves / 2) asm volatile("s_barrier" ::: "memory");
     wait_and_meet<0>();  // no fetch into LDS outlives the tile
+  } else if constexpr (C::NSR != C::NST) {
+    // ---- the loop with F fetched further ahead than R: weights come from HBM,
+    // the rows of x, which every column tile reads, mostly from a cache
+    static_assert(C::NSR == 2 && C::NST > 2, "R one stage ahead");
+    const uint32_t ldsr = lds0 + C::NST * C::FBytes;
+    constexpr int kR = C::RBytes + C::SBytes;
+    issue_r(0, ldsr);
+#pragma unroll
+    for (int s = 0; s < C::NST - 1; ++s) issue_f(s, lds0 + s * C::FBytes);
+    int buf = 0;
+    for (int s = 0; s < stages; ++s) {
+      wait_and_meet<(C::NST - 2) * C::FI>();  // all but the F stages after this one
+      issue_r(s + 1, ldsr + ((s + 1) & 1) * kR);
+      issue_f(s + C::NST - 1, lds0 + (buf == 0 ? C::NST - 1 : buf - 1) * C::FBytes);
+      math(s, smem + C::NST * C::FBytes + (s & 1) * kR, smem + buf * C::FBytes);
+      buf = buf == C::NST - 1 ? 0 : buf + 1;
+    }
+    wait_and_meet<0>();
   } else {
     // ---- the loop: NST - 1 stages in flight; one meeting per stage, after
     // which the buffer of the stage before is free
@@ -536,7 +565,8 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     for (int s = 0; s < stages; ++s) {
       wait_and_meet<(C::NST - 2) * C::Fetches>();
       issue(s + C::NST - 1, buf == 0 ? C::NST - 1 : buf - 1);
-      math(s, smem + buf * C::Stage);
+      const uint8_t* st = smem + buf * C::Stage;
+      math(s, st, st + C::RBytes + C::SBytes);
       buf = buf == C::NST - 1 ? 0 : buf + 1;
     }
     wait_and_meet<0>();  // no fetch into LDS outlives the tile
@@ -577,25 +607,29 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   }
 }
 
-// Workgroup -> tile: runs of kRun consecutive tiles go to one XCD (workgroups
-// are dealt to the 8 XCDs in turn), so the tiles that share a group's rows and
-// weights share an L2.
-constexpr int kXcds = 8, kRun = 4;
-__device__ __forceinline__ int64_t my_tile() {
+// Workgroup -> tile: runs of `run` consecutive tiles go to one XCD (workgroups
+// are dealt to the 8 XCDs in turn), so that tiles which share a group's rows
+// or weights share an L2.  Long runs share more, short ones balance groups of
+// unequal size: 16 where the products bound the call (64 groups of 512 rows,
+// 2048 x 2048: 322 us against 336 with 4), 4 elsewhere (the skewed prompt of
+// 256 groups over 4096 x 6144: 2437 us against 2529; weight gradients of
+// skewed groups 258 against 328).
+constexpr int kXcds = 8, kLongRun = 16, kShortRun = 4;
+__device__ __forceinline__ int64_t my_tile(int run) {
   const int xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
-  return (static_cast<int64_t>(i / kRun) * kXcds + xcd) * kRun + i % kRun;
+  return (static_cast<int64_t>(i / run) * kXcds + xcd) * run + i % run;
 }
 uint32_t tile_grid(int64_t tiles) {
-  constexpr int64_t step = kXcds * kRun;
+  constexpr int64_t step = kXcds * kLongRun;  // whole runs of either length
   return static_cast<uint32_t>((tiles + step - 1) / step * step);
 }
 
-// Row tiles are 256 high; a group's last one takes the smallest height that
+// Row tiles are 256 high (codes: 224); a group's last one takes the smallest height that
 // holds its rows.
-constexpr int kBM = 256, kBN = 256, kThreads = 512;
+constexpr int kBN = 256, kThreads = 512;
 template <int KIND>
-using T256 = std::conditional_t<(KIND <= kWeightsBy), Cfg<KIND, 2, 4, 8, 4, 4, 64, true>,
-                                Cfg<KIND, 2, 4, 8, 4, 2>>;
+using Tall = std::conditional_t<(KIND <= kWeightsBy), Cfg<KIND, 2, 4, 8, 4, 4, 64, true>,
+                                Cfg<KIND, 2, 4, 7, 4, 3, 128, false, 2>>;
 template <int KIND>
 using T128 = Cfg<KIND, 2, 4, 4, 4, 3>;
 template <int KIND>
@@ -612,7 +646,7 @@ constexpr int cmax(int a, int b) { return a > b ? a : b; }
 template <class... C>
 constexpr int lds_of() {
   int m = 0;
-  ((m = cmax(m, C::Stage * C::NST)), ...);
+  ((m = cmax(m, C::Lds)), ...);
   return m;
 }
 
@@ -620,10 +654,11 @@ template <int KIND>
 __global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
   constexpr bool kDw = KIND == kWeights || KIND == kWeightsBy;
   if constexpr (kDw) {
-    using T = T256<KIND>;
+    using T = Tall<KIND>;
     using U = T128<KIND>;
     __shared__ __align__(1024) uint8_t smem[lds_of<T, U>()];
-    const int64_t id = my_tile();
+    const int64_t id = my_tile(kShortRun);
+    constexpr int kBM = T::BM;
     const int nt = (g.K + kBN - 1) / kBN, mt = (g.N + kBM - 1) / kBM;
     const int e = static_cast<int>(id / (mt * nt)), r = static_cast<int>(id % (mt * nt));
     if (e >= g.E) return;
@@ -636,17 +671,18 @@ __global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
       tile<U>(g, smem, e, m0, g.N, n0, a, b);
   } else {
     __shared__ __align__(1024)
-        uint8_t smem[lds_of<T256<KIND>, T128<KIND>, T64<KIND>, T32<KIND>>()];
-    const int64_t id = my_tile();
-    const int nt = ((KIND == kInput ? g.K : g.N) + kBN - 1) / kBN;
+        uint8_t smem[lds_of<Tall<KIND>, T128<KIND>, T64<KIND>, T32<KIND>>()];
+    constexpr int kBM = Tall<KIND>::BM;
     const bool tall_first = g.P >= kTallFirstRows * g.E;
+    const int64_t id = my_tile(tall_first ? kLongRun : kShortRun);
+    const int nt = ((KIND == kInput ? g.K : g.N) + kBN - 1) / kBN;
     const Group gr =
         find_group<kBM, kThreads>(g, id / nt, tall_first, reinterpret_cast<int*>(smem));
     if (gr.e < 0) return;
     const int m0 = gr.a + gr.t * kBM, n0 = static_cast<int>(id % nt) * kBN;
     const int rows = gr.b - m0;
     if (rows > 128)
-      tile<T256<KIND>>(g, smem, gr.e, m0, min(gr.b, m0 + kBM), n0, gr.a, gr.b);
+      tile<Tall<KIND>>(g, smem, gr.e, m0, min(gr.b, m0 + kBM), n0, gr.a, gr.b);
     else if (rows > 64)
       tile<T128<KIND>>(g, smem, gr.e, m0, gr.b, n0, gr.a, gr.b);
     else if (rows > 32)
@@ -821,6 +857,7 @@ hipError_t launch_grouped_mm(const GroupedMm& g, GroupedKind kind, hipStream_t s
   }
   const int cols = kind == kGroupedInput || kind == kGroupedWeights ? g.K : g.N;
   const int64_t nt = (cols + kBN - 1) / kBN;
+  const int kBM = kind == kGroupedCodes ? Tall<kCodes>::BM : Tall<kRows>::BM;
   int64_t mt;
   if (kind == kGroupedWeights)
     mt = static_cast<int64_t>(g.E) * ((g.N + kBM - 1) / kBM);
