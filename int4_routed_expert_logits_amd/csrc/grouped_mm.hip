@@ -274,7 +274,7 @@ __device__ __forceinline__ u32x4_t frag_mn(const uint8_t* st, int col0, int kk, 
 // [0, red) (kWeights: positions [ga, gb)).
 template <class C>
 __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend, int n0, int ga,
-                     int gb) {
+                     int gb, void* out, bool out_f32) {
   const int t = threadIdx.x, lane = t & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(t / kWave);
   const int wm = wv % C::WM, wn = wv / C::WM;
@@ -583,12 +583,12 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   for (int i = 0; i < C::RF; ++i) {
     const int m = m0 + mw + i * 16 + (lane & 15);
     const int64_t row = (C::DW ? static_cast<int64_t>(e) * g.N + m : m) * cols;
-    if (g.out_f32) {
+    if (out_f32) {
 #pragma unroll
       for (int j = 0; j < C::FF; ++j) {
         const int n = n0 + nw + j * 16 + q * 4;
         if (m < mend && n < cols)
-          *reinterpret_cast<f32x4_t*>(static_cast<float*>(g.out) + row + n) = acc[i][j];
+          *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + row + n) = acc[i][j];
       }
     } else {
 #pragma unroll
@@ -600,7 +600,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
                                                         pack_bf16(v[2], v[3]), false, false);
         const int n = n0 + nw + (j + (q & 1)) * 16 + (q >> 1) * 8;
         if (m < mend && n < cols)
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + row + n) =
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row + n) =
               make_uint4(x[0], y[0], x[1], y[1]);
       }
     }
@@ -626,7 +626,7 @@ uint32_t tile_grid(int64_t tiles) {
 
 // Row tiles are 256 high (codes: 224); a group's last one takes the smallest height that
 // holds its rows.
-constexpr int kBN = 256, kThreads = 512;
+constexpr int kBN = 256, kThreads = 512, kCus = 256;
 template <int KIND>
 using Tall = std::conditional_t<(KIND <= kWeightsBy), Cfg<KIND, 2, 4, 8, 4, 4, 64, true>,
                                 Cfg<KIND, 2, 4, 7, 4, 3, 128, false, 2>>;
@@ -652,44 +652,111 @@ constexpr int lds_of() {
 
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
-  constexpr bool kDw = KIND == kWeights || KIND == kWeightsBy;
-  if constexpr (kDw) {
-    using T = Tall<KIND>;
-    using U = T128<KIND>;
-    __shared__ __align__(1024) uint8_t smem[lds_of<T, U>()];
-    const int64_t id = my_tile(kShortRun);
-    constexpr int kBM = T::BM;
-    const int nt = (g.K + kBN - 1) / kBN, mt = (g.N + kBM - 1) / kBM;
-    const int e = static_cast<int>(id / (mt * nt)), r = static_cast<int>(id % (mt * nt));
-    if (e >= g.E) return;
-    int a, b;
-    group_bounds(g, e, a, b);
-    const int m0 = (r / nt) * kBM, n0 = (r % nt) * kBN;
-    if (g.N - m0 > 128)
-      tile<T>(g, smem, e, m0, g.N, n0, a, b);
-    else
-      tile<U>(g, smem, e, m0, g.N, n0, a, b);
-  } else {
-    __shared__ __align__(1024)
-        uint8_t smem[lds_of<Tall<KIND>, T128<KIND>, T64<KIND>, T32<KIND>>()];
-    constexpr int kBM = Tall<KIND>::BM;
-    const bool tall_first = g.P >= kTallFirstRows * g.E;
-    const int64_t id = my_tile(tall_first ? kLongRun : kShortRun);
-    const int nt = ((KIND == kInput ? g.K : g.N) + kBN - 1) / kBN;
-    const Group gr =
-        find_group<kBM, kThreads>(g, id / nt, tall_first, reinterpret_cast<int*>(smem));
-    if (gr.e < 0) return;
-    const int m0 = gr.a + gr.t * kBM, n0 = static_cast<int>(id % nt) * kBN;
-    const int rows = gr.b - m0;
-    if (rows > 128)
-      tile<Tall<KIND>>(g, smem, gr.e, m0, min(gr.b, m0 + kBM), n0, gr.a, gr.b);
-    else if (rows > 64)
-      tile<T128<KIND>>(g, smem, gr.e, m0, gr.b, n0, gr.a, gr.b);
-    else if (rows > 32)
-      tile<T64<KIND>>(g, smem, gr.e, m0, gr.b, n0, gr.a, gr.b);
-    else
-      tile<T32<KIND>>(g, smem, gr.e, m0, gr.b, n0, gr.a, gr.b);
+  constexpr int kBM = Tall<KIND>::BM;
+  __shared__ __align__(1024)
+      uint8_t smem[lds_of<Tall<KIND>, T128<KIND>, T64<KIND>, T32<KIND>>()];
+  const bool tall_first = g.P >= kTallFirstRows * g.E;
+  const int64_t id = my_tile(tall_first ? kLongRun : kShortRun);
+  const int nt = ((KIND == kInput ? g.K : g.N) + kBN - 1) / kBN;
+  const Group gr =
+      find_group<kBM, kThreads>(g, id / nt, tall_first, reinterpret_cast<int*>(smem));
+  if (gr.e < 0) return;
+  const int m0 = gr.a + gr.t * kBM, n0 = static_cast<int>(id % nt) * kBN;
+  const int mend = min(gr.b, m0 + kBM);
+  auto run = [&](auto cfg) {
+    tile<decltype(cfg)>(g, smem, gr.e, m0, mend, n0, gr.a, gr.b, g.out, g.out_f32);
+  };
+  if (mend - m0 > 128)
+    run(Tall<KIND>{});
+  else if (mend - m0 > 64)
+    run(T128<KIND>{});
+  else if (mend - m0 > 32)
+    run(T64<KIND>{});
+  else
+    run(T32<KIND>{});
+}
+
+// Weights' gradients: every group's [N][K], its rows in g.split parts.  One
+// part: to dw.  More: float32 sums to workspace[part][E][N][K], joined by
+// join_parts.
+template <int KIND>
+__global__ __launch_bounds__(kThreads) void grouped_weight_tiles(GroupedMm g) {
+  using T = Tall<KIND>;
+  using U = T128<KIND>;
+  __shared__ __align__(1024) uint8_t smem[lds_of<T, U>()];
+  const int nt = (g.K + kBN - 1) / kBN, mt = (g.N + T::BM - 1) / T::BM;
+  const int64_t id = my_tile(kShortRun);
+  const int r = static_cast<int>(id % (mt * nt));
+  const int e = static_cast<int>(id / (mt * nt) % g.E), z = static_cast<int>(id / (mt * nt) / g.E);
+  if (z >= g.split) return;
+  int a, b;
+  group_bounds(g, e, a, b);
+  void* out = g.out;
+  bool out_f32 = g.out_f32;
+  if (g.split > 1) {
+    const int part = ((b - a) / g.split + 64) / 64 * 64;  // whole stages, split parts hold all
+    a = min(b, a + z * part);
+    b = min(b, a + part);
+    out = static_cast<float*>(g.workspace) + static_cast<int64_t>(z) * g.E * g.N * g.K;
+    out_f32 = true;
   }
+  const int m0 = (r / nt) * T::BM, n0 = (r % nt) * kBN;
+  if (g.N - m0 > 128)
+    tile<T>(g, smem, e, m0, g.N, n0, a, b, out, out_f32);
+  else
+    tile<U>(g, smem, e, m0, g.N, n0, a, b, out, out_f32);
+}
+
+// dw = the parts' sum, in their order; four elements per thread.
+__global__ __launch_bounds__(256) void join_parts(GroupedMm g) {
+  const int64_t n = static_cast<int64_t>(g.E) * g.N * g.K;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const float* p = static_cast<const float*>(g.workspace) + i;
+  f32x4_t v = *reinterpret_cast<const f32x4_t*>(p);
+  for (int z = 1; z < g.split; ++z) v += *reinterpret_cast<const f32x4_t*>(p + z * n);
+  if (g.out_f32) {
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(g.out) + i) = v;
+  } else {
+    const uint2 w = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + i) = w;
+  }
+}
+
+// Parts that each group's rows are cut into: where dw has less than a tile
+// for every CU, as many as fill them, of 256 rows on average at least.
+int weight_parts(int E, int P, int N, int K) {
+  const int64_t tiles = static_cast<int64_t>(E) * ((N + Tall<kWeights>::BM - 1) / Tall<kWeights>::BM) *
+                        ((K + kBN - 1) / kBN);
+  const int64_t fill = kCus / tiles, rows = P / E / 256;
+  const int64_t parts = fill < rows ? fill : rows;
+  return parts < 1 ? 1 : static_cast<int>(parts);
+}
+
+// Few tiles (narrow outputs, one group of middling size): 64 x 128 tiles of
+// four wavefronts, two workgroups per CU.  us, against the large tiles, by
+// their number: 36 tiles (1 group of 2048 rows, 1024 x 1024) 13.7 / 33.7, 72
+// (8 groups, 512 x 2048) 28.7 / 54.3, 144 (2048 x 2048) 53.0 / 55.6, 272 (one
+// group of 4096 rows, 4096 x 2048) 97 / 67.
+constexpr int kSmallTiles = 160;
+template <int KIND>
+using Small = Cfg<KIND, 2, 2, 2, 4, 3>;
+template <int KIND>
+__global__ __launch_bounds__(256, 2) void grouped_small(GroupedMm g) {
+  using T = Small<KIND>;
+  __shared__ __align__(1024) uint8_t smem[lds_of<T>()];
+  const int nt = ((KIND == kInput ? g.K : g.N) + T::BN - 1) / T::BN;
+  const int64_t id = my_tile(kShortRun);
+  const Group gr = find_group<T::BM, 256>(g, id / nt, false, reinterpret_cast<int*>(smem));
+  if (gr.e < 0) return;
+  const int m0 = gr.a + gr.t * T::BM;
+  tile<T>(g, smem, gr.e, m0, min(gr.b, m0 + T::BM), static_cast<int>(id % nt) * T::BN, gr.a, gr.b,
+          g.out, g.out_f32);
+}
+
+// The most row tiles of bm rows that any grouping of P rows can have.
+int64_t most_row_tiles(const GroupedMm& g, int bm) {
+  return g.P / bm + (g.E < g.P ? g.E : g.P);
 }
 
 // ---------------------------------------------------------------------------
@@ -844,10 +911,29 @@ __global__ __launch_bounds__(kSkinnyThreads, Skinny<KIND>::kOcc) void grouped_sk
 
 }  // namespace
 
-size_t grouped_dw_workspace(int, int, int, int) { return 0; }
+size_t grouped_dw_workspace(int E, int P, int N, int K) {
+  const int parts = weight_parts(E, P, N, K);
+  return parts > 1 ? static_cast<size_t>(parts) * E * N * K * sizeof(float) : 0;
+}
 
-hipError_t launch_grouped_mm(const GroupedMm& g, GroupedKind kind, hipStream_t stream) {
-  if ((kind == kGroupedRows || kind == kGroupedCodes) && few_rows(g)) {
+hipError_t launch_grouped_mm(const GroupedMm& args, GroupedKind kind, hipStream_t stream) {
+  GroupedMm g = args;
+  auto go = [&](auto kernel, int64_t tiles, int threads) {
+    return launch(kernel, dim3(tile_grid(tiles)), dim3(threads), 0, stream, g);
+  };
+  if (kind == kGroupedWeights) {
+    constexpr int bm = Tall<kWeights>::BM;
+    g.split = weight_parts(g.E, g.P, g.N, g.K);
+    const int64_t tiles = static_cast<int64_t>(g.E) * ((g.N + bm - 1) / bm) *
+                          ((g.K + kBN - 1) / kBN) * g.split;
+    const hipError_t e = g.rows ? go(grouped_weight_tiles<kWeightsBy>, tiles, kThreads)
+                                : go(grouped_weight_tiles<kWeights>, tiles, kThreads);
+    if (e != hipSuccess || g.split == 1) return e;
+    const int64_t n = static_cast<int64_t>(g.E) * g.N * g.K;
+    return launch(join_parts, dim3(static_cast<uint32_t>((n / 4 + 255) / 256)), dim3(256), 0, stream,
+                  g);
+  }
+  if (kind != kGroupedInput && few_rows(g)) {
     const int cols = kind == kGroupedRows ? Skinny<kRows>::kCols : Skinny<kCodesF32>::kCols;
     const int nb = (g.N + cols - 1) / cols;
     const dim3 grid(static_cast<uint32_t>(nb * (g.E < g.P ? g.E : g.P))), block(kSkinnyThreads);
@@ -855,25 +941,27 @@ hipError_t launch_grouped_mm(const GroupedMm& g, GroupedKind kind, hipStream_t s
                ? launch(grouped_skinny<kRows>, grid, block, 0, stream, g, nb)
                : launch(grouped_skinny<kCodesF32>, grid, block, 0, stream, g, nb);
   }
-  const int cols = kind == kGroupedInput || kind == kGroupedWeights ? g.K : g.N;
-  const int64_t nt = (cols + kBN - 1) / kBN;
-  const int kBM = kind == kGroupedCodes ? Tall<kCodes>::BM : Tall<kRows>::BM;
-  int64_t mt;
-  if (kind == kGroupedWeights)
-    mt = static_cast<int64_t>(g.E) * ((g.N + kBM - 1) / kBM);
-  else  // the most row tiles any grouping of P rows can have
-    mt = g.P / kBM + (g.E < g.P ? g.E : g.P);
-  const dim3 grid(tile_grid(mt * nt)), block(kThreads);
-  auto go = [&](auto kernel) { return launch(kernel, grid, block, 0, stream, g); };
-  switch (kind) {
-    case kGroupedRows: return go(grouped_tiles<kRows>);
-    case kGroupedInput: return go(grouped_tiles<kInput>);
-    case kGroupedWeights:
-      return g.rows ? go(grouped_tiles<kWeightsBy>) : go(grouped_tiles<kWeights>);
-    case kGroupedCodes:
-      return g.out_f32 ? go(grouped_tiles<kCodesF32>) : go(grouped_tiles<kCodes>);
+  const int cols = kind == kGroupedInput ? g.K : g.N;
+  const int bm = kind == kGroupedCodes ? Tall<kCodes>::BM : Tall<kRows>::BM;
+  const int64_t tiles = most_row_tiles(g, bm) * ((cols + kBN - 1) / kBN);
+  if (tiles < kSmallTiles) {
+    using S = Small<kRows>;
+    const int64_t small = most_row_tiles(g, S::BM) * ((cols + S::BN - 1) / S::BN);
+    switch (kind) {
+      case kGroupedRows: return go(grouped_small<kRows>, small, S::Threads);
+      case kGroupedInput: return go(grouped_small<kInput>, small, S::Threads);
+      default:
+        return g.out_f32 ? go(grouped_small<kCodesF32>, small, S::Threads)
+                         : go(grouped_small<kCodes>, small, S::Threads);
+    }
   }
-  return hipErrorNotSupported;
+  switch (kind) {
+    case kGroupedRows: return go(grouped_tiles<kRows>, tiles, kThreads);
+    case kGroupedInput: return go(grouped_tiles<kInput>, tiles, kThreads);
+    default:
+      return g.out_f32 ? go(grouped_tiles<kCodesF32>, tiles, kThreads)
+                       : go(grouped_tiles<kCodes>, tiles, kThreads);
+  }
 }
 
 }  // namespace moe

@@ -129,6 +129,7 @@ struct GroupedMm {
   void* out;
   void* workspace;
   int E, P, N, K;
+  int split;  // kGroupedWeights: parts of a group's rows, joined through workspace
   bool out_f32;
 };
 size_t grouped_dw_workspace(int E, int P, int N, int K);
