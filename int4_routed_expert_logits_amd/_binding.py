@@ -424,9 +424,10 @@ def _types():
     global _T, _raw_stream, _current_device
     if _T is None:
         import torch
-        # the handle itself: building a torch Stream takes longer than a launch
+        # the stream's handle and the device's index themselves: building a torch
+        # Stream takes as long as a launch
         _raw_stream = torch._C._cuda_getCurrentRawStream
-        _current_device = torch.cuda.current_device
+        _current_device = torch._C._cuda_getDevice
         _T = ((torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32), (torch.int32,),
               (torch.float8_e4m3fn, torch.uint8))
     return _T
@@ -436,15 +437,15 @@ def _take(fn: str, dev: int, name: str, t, dtypes, shape):
     """t's address, after checking it (None passes as NULL)."""
     if t is None:
         return None
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{fn}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{fn}: {name} is on {t.device}, not on the first tensor's GPU ({dev})")
-    if not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} is not contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{fn}: {name} is not contiguous")
 
 
 def _dim(fn: str, name: str, t, n: int):

@@ -49,17 +49,50 @@ __device__ __forceinline__ void store8(void* p, bool bf16, int64_t i, const floa
   }
 }
 
-// Sum over the workgroup in a fixed order; sh: kMaxWaves floats not used
-// since the last barrier.
-__device__ __forceinline__ float block_sum(float v, float* sh) {
-  v = group_sum(v, kWave);
-  const int waves = blockDim.x / kWave;
-  if (waves == 1) return v;
-  if (threadIdx.x % kWave == 0) sh[threadIdx.x / kWave] = v;
+// v of the lane that DPP control CTRL names, inside rows of 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+      0, static_cast<int>(__float_as_uint(v)), CTRL, 0xF, 0xF, false)));
+}
+// Sum over each row of 16 lanes (quad_perm [1,0,3,2] and [2,3,0,1],
+// row_half_mirror, row_mirror), every lane receiving it.
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  v += dpp<0x141>(v);
+  v += dpp<0x140>(v);
+  return v;
+}
+__device__ __forceinline__ float readlane(float v, int lane) {
+  return __uint_as_float(static_cast<uint32_t>(
+      __builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(v)), lane)));
+}
+
+// Sums of N values over the workgroup, in a fixed order (lanes and wavefronts
+// by DPP: the shuffles through LDS that this replaced were a third of the
+// gradient's time); sh: N x kMaxWaves floats not used since the last barrier.
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*sh)[kMaxWaves]) {
+  const int waves = blockDim.x / kWave, lane = threadIdx.x % kWave;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = row_sum(v[i]);
+    v[i] = (readlane(v[i], 0) + readlane(v[i], 16)) + (readlane(v[i], 32) + readlane(v[i], 48));
+  }
+  if (waves == 1) return;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sh[i][threadIdx.x / kWave] = v[i];
+  }
   __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < waves; ++w) s += sh[w];
-  return s;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = readlane(row_sum(lane < waves ? sh[i][lane & 15] : 0.0f), 0);
+}
+__device__ __forceinline__ float block_sum(float v, float (*sh)[kMaxWaves]) {
+  float one[1] = {v};
+  block_sums(one, sh);
+  return one[0];
 }
 
 __device__ __forceinline__ float sum_sq(const float (&v)[kV]) {
@@ -94,7 +127,7 @@ __global__ __launch_bounds__(1024) void norm_rows(BlockNorm g) {
   }
   if (g.y) {
     if (g.w_post) {
-      const float a = inv_rms(block_sum(sum_sq(y), sh[0]), g.d, g.eps);
+      const float a = inv_rms(block_sum(sum_sq(y), &sh[0]), g.d, g.eps);
 #pragma unroll
       for (int j = 0; j < kV; ++j) y[j] = w1[j] * (y[j] * a);
     }
@@ -103,30 +136,11 @@ __global__ __launch_bounds__(1024) void norm_rows(BlockNorm g) {
   }
   if (in && g.res_out) store8(g.res_out, g.res_bf16, at, r);
   if (g.w_pre) {
-    const float b = inv_rms(block_sum(in ? sum_sq(r) : 0.0f, sh[1]), g.d, g.eps);
+    const float b = inv_rms(block_sum(in ? sum_sq(r) : 0.0f, &sh[1]), g.d, g.eps);
 #pragma unroll
     for (int j = 0; j < kV; ++j) r[j] = w2[j] * (r[j] * b);
     if (in) store8(g.normed, g.normed_bf16, at, r);
   }
-}
-
-// Sums of five values over the workgroup, in a fixed order; sh: 5 x kMaxWaves
-// floats not used since the last barrier.
-__device__ __forceinline__ void block_sum5(float (&v)[5], float (*sh)[kMaxWaves]) {
-#pragma unroll
-  for (int i = 0; i < 5; ++i) v[i] = group_sum(v[i], kWave);
-  const int waves = blockDim.x / kWave;
-  if (waves == 1) return;
-  if (threadIdx.x % kWave == 0) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) sh[i][threadIdx.x / kWave] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 5; ++i) v[i] = 0.0f;
-  for (int w = 0; w < waves; ++w)
-#pragma unroll
-    for (int i = 0; i < 5; ++i) v[i] += sh[i][w];
 }
 
 // 8 values of a row as they lie in memory.
@@ -212,7 +226,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_rows(BlockNorm g) {
     if (ALL_BF16) read(row + gridDim.x);
     float a = 1.0f;
     if (g.y && g.w_post) {
-      a = inv_rms(block_sum(sum_sq(y), sh[odd][5]), g.d, g.eps);
+      a = inv_rms(block_sum(sum_sq(y), &sh[odd][5]), g.d, g.eps);
 #pragma unroll
       for (int j = 0; j < kV; ++j) y[j] *= a;  // yh
     }
@@ -228,7 +242,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_rows(BlockNorm g) {
       sum[3] = fmaf(q, v, sum[3]);
       sum[4] = fmaf(q, r[j], sum[4]);
     }
-    block_sum5(sum, sh[odd]);
+    block_sums(sum, sh[odd]);
     float mean_qt = sum[2];
     if (g.w_pre) {
       const float b = inv_rms(sum[0], g.d, g.eps);
@@ -275,6 +289,7 @@ __global__ __launch_bounds__(1024) void norm_grad_columns(BlockNorm g, int parts
   const int c = blockIdx.x * kWave + lane;
   float s1 = 0.0f, s2 = 0.0f;
   if (c < g.d)
+#pragma unroll 8
     for (int p = wv; p < parts; p += kMaxWaves) {
       const float* row = g.part + static_cast<int64_t>(p) * 2 * g.d;
       s1 += row[c];
