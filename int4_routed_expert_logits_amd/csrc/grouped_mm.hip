@@ -327,8 +327,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       rs.p[j] = g.r + src * red_bytes + chunk;
     }
     if constexpr (C::F8) {
-      const int row = t % C::BM;
-      const int64_t src = m0 + row < mend ? source_row(g, m0 + row) : -1;
+      const int64_t src = t < C::BM && m0 + t < mend ? source_row(g, m0 + t) : -1;
       if (src >= 0) {
         sp = reinterpret_cast<const uint8_t*>(g.r_scale + src * stages);
         sstep = 4;
