@@ -35,7 +35,9 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-typedef const __attribute__((address_space(4))) int32_t const_i32;  // by scalar loads
+// read by scalar loads: a vector load's wait would drain the fetches into LDS
+typedef const __attribute__((address_space(4))) int32_t const_i32;
+typedef const __attribute__((address_space(4))) float const_f32;
 
 constexpr int kBlock = 128;       // columns (and weight rows) per scale
 
@@ -335,7 +337,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     }
   }
   // gathered F: the next stage's entries of rows, this wavefront's consecutive
-  // ones, by scalar loads (a vector load's wait would drain the fetches)
+  // ones
   constexpr int kWaveRows = C::K == kWeightsBy ? C::FBytes / (C::BN * 2) / C::Waves : 1;
   uint32_t next_row[kWaveRows];
   auto load_rows = [&](int stage) {
@@ -409,14 +411,18 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
 #pragma unroll
     for (int j = 0; j < C::FF; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int mw = wm * C::RF * 16, nw = wn * C::FF * 16;
-  const float* fsc = nullptr;
-  if constexpr (C::F8)
-    fsc = g.f_scale + (static_cast<int64_t>(e) * ((g.N + kBlock - 1) / kBlock) +
-                       min(n0 + nw, g.N - 1) / kBlock) * stages;
+  const_f32* fsc = nullptr;  // this wavefront's row of weight scales
+  float ws_next = 0.0f;      // ... of the next stage
+  if constexpr (C::F8) {
+    fsc = (const_f32*)(g.f_scale + (static_cast<int64_t>(e) * ((g.N + kBlock - 1) / kBlock) +
+                                    min(n0 + nw, g.N - 1) / kBlock) * stages);
+    ws_next = fsc[0];
+  }
 
   auto math = [&](int stage, const uint8_t* sr, const uint8_t* sf) {
     if constexpr (C::K == kCodesF32) {
-      const float ws = fsc[stage];
+      const float ws = ws_next;
+      ws_next = fsc[min(stage + 1, stages - 1)];
       const float* rsc = reinterpret_cast<const float*>(sr + C::RBytes);
       bf16x8_t fa[C::FF][4];  // 16 codes of each half of the stage
 #pragma unroll
@@ -448,7 +454,8 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
         }
       }
     } else if constexpr (C::F8) {
-      const float ws = fsc[stage];
+      const float ws = ws_next;
+      ws_next = fsc[min(stage + 1, stages - 1)];
       const float* rsc = reinterpret_cast<const float*>(sr + C::RBytes);
       i32x8_t fa[C::FF];
 #pragma unroll
