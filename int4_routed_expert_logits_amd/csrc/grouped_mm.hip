@@ -187,9 +187,7 @@ __device__ __forceinline__ int64_t source_row(const GroupedMm& g, int p) {
 }
 
 // WM x WN wavefronts, each with RF x FF fragments of 16 x 16 outputs.
-// NST stages of F in LDS and NSR (0: as many) of R.
-template <int KIND, int WM_, int WN_, int RF_, int FF_, int NST_, int SB_ = 128, bool PP_ = false,
-          int NSR_ = 0>
+template <int KIND, int WM_, int WN_, int RF_, int FF_, int NST_, int SB_ = 128, bool PP_ = false>
 struct Cfg {
   static constexpr int K = KIND, WM = WM_, WN = WN_, RF = RF_, FF = FF_, NST = NST_;
   static constexpr bool PP = PP_;      // the two halves of the workgroup in turn
@@ -206,8 +204,7 @@ struct Cfg {
   static constexpr int RBytes = BM * SB, FBytes = BN * SB;
   static constexpr int SBytes = F8 ? Threads * 4 : 0;  // a stage's row scales
   static constexpr int Stage = RBytes + FBytes + SBytes;
-  static constexpr int NSR = NSR_ == 0 ? NST : NSR_;
-  static constexpr int Lds = NST * FBytes + NSR * (RBytes + SBytes);
+  static constexpr int Lds = Stage * NST;
   // fetches per wavefront and stage; R's wrap around where they do not divide
   static constexpr int RI = (RBytes + Waves * 1024 - 1) / (Waves * 1024);
   static constexpr int FI = FBytes / (Waves * 1024);
@@ -369,7 +366,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       fs.p[j] = g.f + e * wsz + static_cast<int64_t>(n0 + row) * red_bytes + chunk;
     }
   }
-  // R's stage (with its row scales) to LDS at lds, F's to its own place
+  // a stage as it lies in its buffer: R, row scales, F
   auto issue_r = [&](int stage, uint32_t lds) {
     if constexpr (C::RT)
       fetch<C::RI, kUnitMN>(rs, stage, red, lds, wv * C::RI, C::RBytes / 1024);
@@ -398,7 +395,6 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       load_rows(stage + 1);
     }
   };
-  // a stage as it lies in the rings of equal depth: R, row scales, F
   auto issue = [&](int stage, int buf) {
     issue_r(stage, lds0 + buf * C::Stage);
     issue_f(stage, lds0 + buf * C::Stage + C::RBytes + C::SBytes);
@@ -544,24 +540,6 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     }
     if (wv < C::Waves / 2) asm volatile("s_barrier" ::: "memory");
     wait_and_meet<0>();  // no fetch into LDS outlives the tile
-  } else if constexpr (C::NSR != C::NST) {
-    // ---- the loop with F fetched further ahead than R: weights come from HBM,
-    // the rows of x, which every column tile reads, mostly from a cache
-    static_assert(C::NSR == 2 && C::NST > 2, "R one stage ahead");
-    const uint32_t ldsr = lds0 + C::NST * C::FBytes;
-    constexpr int kR = C::RBytes + C::SBytes;
-    issue_r(0, ldsr);
-#pragma unroll
-    for (int s = 0; s < C::NST - 1; ++s) issue_f(s, lds0 + s * C::FBytes);
-    int buf = 0;
-    for (int s = 0; s < stages; ++s) {
-      wait_and_meet<(C::NST - 2) * C::FI>();  // all but the F stages after this one
-      issue_r(s + 1, ldsr + ((s + 1) & 1) * kR);
-      issue_f(s + C::NST - 1, lds0 + (buf == 0 ? C::NST - 1 : buf - 1) * C::FBytes);
-      math(s, smem + C::NST * C::FBytes + (s & 1) * kR, smem + buf * C::FBytes);
-      buf = buf == C::NST - 1 ? 0 : buf + 1;
-    }
-    wait_and_meet<0>();
   } else {
     // ---- the loop: NST - 1 stages in flight; one meeting per stage, after
     // which the buffer of the stage before is free
@@ -630,14 +608,16 @@ uint32_t tile_grid(int64_t tiles) {
   return static_cast<uint32_t>((tiles + step - 1) / step * step);
 }
 
-// Row tiles are 256 high (codes: 224); a group's last one takes the smallest height that
+// Row tiles are 256 high (codes widened to bf16: 128, whose operands'
+// widening would need more registers than there are); a group's last one takes the smallest height that
 // holds its rows.
 constexpr int kBN = 256, kThreads = 512, kCus = 256;
 template <int KIND>
-using Tall = std::conditional_t<(KIND <= kWeightsBy), Cfg<KIND, 2, 4, 8, 4, 4, 64, true>,
-                                Cfg<KIND, 2, 4, 7, 4, 3, 128, false, 2>>;
-template <int KIND>
 using T128 = Cfg<KIND, 2, 4, 4, 4, 3>;
+template <int KIND>
+using Tall = std::conditional_t<
+    (KIND <= kWeightsBy), Cfg<KIND, 2, 4, 8, 4, 4, 64, true>,
+    std::conditional_t<KIND == kCodes, Cfg<KIND, 2, 4, 8, 4, 2>, T128<KIND>>>;
 template <int KIND>
 using T64 = Cfg<KIND, 1, 8, 4, 2, 3>;
 template <int KIND>
@@ -948,7 +928,9 @@ hipError_t launch_grouped_mm(const GroupedMm& args, GroupedKind kind, hipStream_
                : launch(grouped_skinny<kCodesF32>, grid, block, 0, stream, g, nb);
   }
   const int cols = kind == kGroupedInput ? g.K : g.N;
-  const int bm = kind == kGroupedCodes ? Tall<kCodes>::BM : Tall<kRows>::BM;
+  const int bm =
+      kind == kGroupedCodes && g.out_f32 ? Tall<kCodesF32>::BM : Tall<kRows>::BM;
+  static_assert(Tall<kCodes>::BM == Tall<kRows>::BM, "tile height");
   const int64_t tiles = most_row_tiles(g, bm) * ((cols + kBN - 1) / kBN);
   if (tiles < kSmallTiles) {
     using S = Small<kRows>;
