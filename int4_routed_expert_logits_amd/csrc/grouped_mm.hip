@@ -106,6 +106,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return f32_to_bf16(lo) | (static_cast<uint32_t>(f32_to_bf16(hi)) << 16);
 }
 
+// The product of two fragments of 16 rows x 128 codes (two 16-byte chunks a
+// lane, in the same places of both): by the 8-bit matrix instruction, or exactly
+// as bf16.
+template <bool EXACT>
+__device__ __forceinline__ f32x4_t codes_product(const u32x4_t (&f)[2], const u32x4_t (&r)[2]) {
+  f32x4_t p{0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (EXACT) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int v = 0; v < 4; v += 2)
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(f[h][v], f[h][v + 1]),
+                                                    codes_to_bf16(r[h][v], r[h][v + 1]), p, 0, 0, 0);
+  } else {
+    p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        __builtin_bit_cast(i32x8_t, __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7)),
+        __builtin_bit_cast(i32x8_t, __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3, 4, 5, 6, 7)), p,
+        0, 0, 0, 0, 0, 0);
+  }
+  return p;
+}
+
 struct Group {
   int e, a, b;  // expert, its grouped positions
   int t;        // this workgroup's tile of the group
@@ -416,62 +438,47 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   }
 
   auto math = [&](int stage, const uint8_t* sr, const uint8_t* sf) {
-    if constexpr (C::K == kCodesF32) {
+    if constexpr (C::F8) {
+      // a block's product p = sum of 128 codes' products, scaled into acc.  One
+      // row of fragments behind the matrix instructions, so that none of them
+      // is waited for: row i's instructions, each followed by the scaling of row
+      // i - 1, with row i + 1 on its way from LDS.
       const float ws = ws_next;
       ws_next = fsc[min(stage + 1, stages - 1)];
-      const float* rsc = reinterpret_cast<const float*>(sr + C::RBytes);
-      bf16x8_t fa[C::FF][4];  // 16 codes of each half of the stage
+      const float* rsc = reinterpret_cast<const float*>(sr + C::RBytes) + mw + (lane & 15);
+      u32x4_t fa[C::FF][2], rb[2][2];
 #pragma unroll
       for (int j = 0; j < C::FF; ++j)
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const u32x4_t v = frag_k<C::SB>(sf, nw + j * 16, kk, lane);
-          fa[j][2 * kk] = codes_to_bf16(v[0], v[1]);
-          fa[j][2 * kk + 1] = codes_to_bf16(v[2], v[3]);
-        }
+        for (int h = 0; h < 2; ++h) fa[j][h] = frag_k<C::SB>(sf, nw + j * 16, h, lane);
 #pragma unroll
-      for (int i = 0; i < C::RF; ++i) {
-        bf16x8_t rb[4];
+      for (int h = 0; h < 2; ++h) rb[0][h] = frag_k<C::SB>(sr, mw, h, lane);
+      float sc[C::RF];
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const u32x4_t v = frag_k<C::SB>(sr, mw + i * 16, kk, lane);
-          rb[2 * kk] = codes_to_bf16(v[0], v[1]);
-          rb[2 * kk + 1] = codes_to_bf16(v[2], v[3]);
+      for (int i = 0; i < C::RF; ++i) sc[i] = rsc[i * 16] * ws;
+      f32x4_t p[2][C::FF];
+#pragma unroll
+      for (int i = 0; i <= C::RF; ++i) {
+        const int cur = i & 1, old = cur ^ 1;
+        if (i + 1 < C::RF) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            rb[old][h] = frag_k<C::SB>(sr, mw + (i + 1) * 16, h, lane);
         }
-        const float s = rsc[mw + i * 16 + (lane & 15)] * ws;
 #pragma unroll
         for (int j = 0; j < C::FF; ++j) {
-          f32x4_t p{0.0f, 0.0f, 0.0f, 0.0f};
+          if (i < C::RF) p[cur][j] = codes_product<C::K == kCodesF32>(fa[j], rb[cur]);
+          if (i > 0) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[j][h], rb[h], p, 0, 0, 0);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, p[q], acc[i][j][q]);
+            for (int q = 0; q < 4; ++q)
+              acc[i - 1][j][q] = fmaf(sc[i - 1], p[old][j][q], acc[i - 1][j][q]);
+          }
+          if (C::K == kCodes && i > 0 && i < C::RF) {  // in this order: one product, one scaling
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          }
         }
-      }
-    } else if constexpr (C::F8) {
-      const float ws = ws_next;
-      ws_next = fsc[min(stage + 1, stages - 1)];
-      const float* rsc = reinterpret_cast<const float*>(sr + C::RBytes);
-      i32x8_t fa[C::FF];
-#pragma unroll
-      for (int j = 0; j < C::FF; ++j) {
-        const u32x4_t lo = frag_k<C::SB>(sf, nw + j * 16, 0, lane), hi = frag_k<C::SB>(sf, nw + j * 16, 1, lane);
-        fa[j] = __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-      }
-#pragma unroll
-      for (int i = 0; i < C::RF; ++i) {
-        const u32x4_t lo = frag_k<C::SB>(sr, mw + i * 16, 0, lane), hi = frag_k<C::SB>(sr, mw + i * 16, 1, lane);
-        const i32x8_t rb =
-            __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        const float s = rsc[mw + i * 16 + (lane & 15)] * ws;
-#pragma unroll
-        for (int j = 0; j < C::FF; ++j) {
-          const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              fa[j], rb, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, p[q], acc[i][j][q]);
-        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
 #pragma unroll
