@@ -130,7 +130,8 @@ __device__ __forceinline__ f32x4_t codes_product(const u32x4_t (&f)[2], const u3
 
 struct Group {
   int e, a, b;  // expert, its grouped positions
-  int t;        // this workgroup's tile of the group
+  int t;        // this workgroup's row tile of the group
+  int n;        // the group's row tiles that come together with it
 };
 
 // The group's bounds as the kernels take them: whatever offsets holds, they
@@ -191,12 +192,14 @@ __device__ Group find_group(const GroupedMm& g, int64_t tile, bool tall_first, i
       sh[2 * kWaves + 1] = a[i];
       sh[2 * kWaves + 2] = b[i];
       sh[2 * kWaves + 3] = mid ? static_cast<int>(tile) - first : n[i];
+      sh[2 * kWaves + 4] = mid ? n[i] : 0;
     }
     first += n[i];
     first_low += low[i];
   }
   __syncthreads();
-  Group r{sh[2 * kWaves], sh[2 * kWaves + 1], sh[2 * kWaves + 2], sh[2 * kWaves + 3]};
+  Group r{sh[2 * kWaves], sh[2 * kWaves + 1], sh[2 * kWaves + 2], sh[2 * kWaves + 3],
+          sh[2 * kWaves + 4]};
   __syncthreads();
   return r;
 }
@@ -615,6 +618,21 @@ uint32_t tile_grid(int64_t tiles) {
   return static_cast<uint32_t>((tiles + step - 1) / step * step);
 }
 
+// Tile r of a group's mt x nt: four row tiles at a time, column by column, so
+// that a run of tiles shares both its rows and its weights.
+struct Place {
+  int m, n;
+};
+__device__ __forceinline__ Place place(int r, int mt, int nt) {
+  constexpr int kHigh = 4;
+  const int band = r / (kHigh * nt), h = min(kHigh, mt - band * kHigh), i = r - band * kHigh * nt;
+  return {band * kHigh + i % h, i / h};
+}
+// ... of the tile that find_group found (n = 0: one on its own, at row tile t).
+__device__ __forceinline__ Place place(const Group& gr, int col, int nt) {
+  return gr.n ? place(gr.t * nt + col, gr.n, nt) : Place{gr.t, col};
+}
+
 // Row tiles are 256 high (codes widened to bf16: 128, whose operands'
 // widening would need more registers than there are); a group's last one takes the smallest height that
 // holds its rows.
@@ -654,7 +672,8 @@ __global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
   const Group gr =
       find_group<kBM, kThreads>(g, id / nt, tall_first, reinterpret_cast<int*>(smem));
   if (gr.e < 0) return;
-  const int m0 = gr.a + gr.t * kBM, n0 = static_cast<int>(id % nt) * kBN;
+  const Place at = place(gr, static_cast<int>(id % nt), nt);
+  const int m0 = gr.a + at.m * kBM, n0 = at.n * kBN;
   const int mend = min(gr.b, m0 + kBM);
   auto run = [&](auto cfg) {
     tile<decltype(cfg)>(g, smem, gr.e, m0, mend, n0, gr.a, gr.b, g.out, g.out_f32);
@@ -693,7 +712,8 @@ __global__ __launch_bounds__(kThreads) void grouped_weight_tiles(GroupedMm g) {
     out = static_cast<float*>(g.workspace) + static_cast<int64_t>(z) * g.E * g.N * g.K;
     out_f32 = true;
   }
-  const int m0 = (r / nt) * T::BM, n0 = (r % nt) * kBN;
+  const Place at = place(r, mt, nt);
+  const int m0 = at.m * T::BM, n0 = at.n * kBN;
   if (g.N - m0 > 128)
     tile<T>(g, smem, e, m0, g.N, n0, a, b, out, out_f32);
   else
@@ -742,9 +762,9 @@ __global__ __launch_bounds__(256, 2) void grouped_small(GroupedMm g) {
   const int64_t id = my_tile(kShortRun);
   const Group gr = find_group<T::BM, 256>(g, id / nt, false, reinterpret_cast<int*>(smem));
   if (gr.e < 0) return;
-  const int m0 = gr.a + gr.t * T::BM;
-  tile<T>(g, smem, gr.e, m0, min(gr.b, m0 + T::BM), static_cast<int>(id % nt) * T::BN, gr.a, gr.b,
-          g.out, g.out_f32);
+  const Place at = place(gr, static_cast<int>(id % nt), nt);
+  const int m0 = gr.a + at.m * T::BM;
+  tile<T>(g, smem, gr.e, m0, min(gr.b, m0 + T::BM), at.n * T::BN, gr.a, gr.b, g.out, g.out_f32);
 }
 
 // The most row tiles of bm rows that any grouping of P rows can have.
