@@ -142,6 +142,7 @@ moe_status moe_swiglu_grad(int32_t P, int32_t f, const void* gu, const void* dh,
  * (the shared expert's rows have dout itself).  A slot with inv_perm outside
  * [0, T * top_k) has dtopk_w 0 and writes no row of dy.
  *  y   [T*top_k][d] (y_dt), grouped order; dy out, same type, may be y itself
+ *  inv_perm as moe_union writes it: no position twice
  *  dtopk_w out [T][top_k] float32 */
 moe_status moe_combine_grad(const moe_shape* shape, int32_t T, const void* dout, moe_dtype out_dt,
                             const void* y, moe_dtype y_dt, const int32_t* inv_perm,

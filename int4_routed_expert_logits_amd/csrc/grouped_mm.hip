@@ -5,19 +5,26 @@
 // and the first of them over e4m3 codes with a float32 scale per 128 columns
 // of a row and per 128 x 128 weights.
 //
-// All four are one loop: D[m][n] = sum_k R[m][k] F[n][k] over a 256-column
-// tile of one group, R being the operand whose index is the output's row and
-// F the one whose index is its column.  A stage of the loop is 128 bytes of
-// the contraction (64 bf16, 128 codes) of every row of R and F in LDS,
+// All four are one loop: D[m][n] = sum_k R[m][k] F[n][k] over a tile of one
+// group (256 x 256 where it has the rows), R being the operand whose index is
+// the output's row and F the one whose index is its column.  A stage of the
+// loop is 64 or 128 bytes of the contraction of every row of R and F in LDS,
 // fetched by global_load_lds.  An operand that is contiguous along the
-// contraction is stored [row][128 bytes]; one that is contiguous along its
-// own index (W of `input`, both operands of `weights`) is stored
-// [64 of the contraction][its columns] and read with the transposing
-// ds_read_b64_tr_b16, so no operand is ever transposed in memory.
+// contraction is stored [row][stage]; one that is contiguous along its own
+// index (W of `input`, both operands of `weights`) is stored [stage][its
+// columns] and read with the transposing ds_read_b64_tr_b16, so no operand is
+// ever transposed in memory.
 // Chunks past an operand's end are fetched from a zero block, so no tail of
 // K, N or a group's rows needs a branch in the arithmetic, and both operands
 // are zero there (no 0 * inf).  F goes to the matrix instruction's A side:
 // a lane then holds four consecutive columns of one output row.
+//
+// What bounds it (measured): with few rows a group, the weights' bytes (8 rows
+// over 8 of 256 experts, 403 MB: 73 us, 5.5 TB/s; the skewed 2048-token prompt,
+// 13.0 GB: 2.44 ms, 5.3 TB/s).  With many, LDS: a 32-deep stage of a 256 x 256
+// tile takes 1024 cycles of the matrix cores and about 1280 of LDS (96 KB of
+// fragment reads, 32 KB of fetches), and a loop of 8192 rows over one 4096 x
+// 4096 matrix runs at 1170 TFLOP/s in all.
 #include <type_traits>
 
 #include "common.h"
@@ -141,7 +148,7 @@ __device__ __forceinline__ void group_bounds(const GroupedMm& g, int e, int& a, 
   b = min(max(g.offsets[e + 1], a), g.P);
 }
 
-// Which group holds row tile `tile`: every thread takes two groups, a scan
+// Which group holds row tile `tile`: every thread takes a few groups, a scan
 // over the workgroup gives their first tiles, and the owner tells the others.
 // e = -1 past the last tile.  Groups have ceil(rows / BM) tiles, in ascending
 // order of the groups; with `tall_first`, the tiles of more than BM / 2 rows
@@ -237,7 +244,7 @@ struct Cfg {
   static_assert(Lds <= 160 * 1024, "LDS");
 };
 
-// Swizzle of the [row][128 bytes] layout: chunk c of row r is stored at
+// Swizzle of the [row][stage] layout with 128-byte stages: chunk c of row r is stored at
 // c ^ ((r >> 1) & 7), so the 16 rows a fragment read touches at once lie in
 // different banks.  The DMA writes LDS in lane order; the lanes pick their
 // sources accordingly.
@@ -246,7 +253,7 @@ template <int SB>
 __device__ __forceinline__ int kc_slot(int row, int chunk) {
   return SB == 128 ? chunk ^ ((row >> 1) & 7) : chunk ^ ((row >> 2) & 3);
 }
-// ... of the [64][columns] layout: 32-byte segment s of row r is stored at
+// ... of the [stage][columns] layout: 32-byte segment s of row r is stored at
 // s ^ f(r), f from the three bits in which the eight rows that a transposing
 // read of half a wavefront touches differ.
 __device__ __forceinline__ int mn_swz(int row) { return (row & 3) | (((row >> 3) & 1) << 2); }
@@ -281,7 +288,7 @@ __device__ __forceinline__ u32x4_t frag_k(const uint8_t* st, int row0, int kk, i
   return *reinterpret_cast<const u32x4_t*>(st + row * SB +
                                            (kc_slot<SB>(row, kk * 4 + (lane >> 4)) << 4));
 }
-// ... of the [64][width] layout: 16 columns x 32 of the contraction.  Two
+// ... of the [stage][width] layout: 16 columns x 32 of the contraction.  Two
 // transposing reads; in each, 16 lanes name four rows of 16 columns and get
 // four rows of their own column.
 template <int WIDTH>
@@ -514,7 +521,8 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     // each on every SIMD) run half a stage apart, so that while one half's
     // matrix instructions run, the other reads its operands from LDS.  Three
     // stages are in flight; a stage's buffer is fetched into after its last
-    // reader has its data.
+    // reader has its data.  (64-deep stages with one meeting each, both halves
+    // at once: 1.7 us a stage where two of these take 1.5.)
     static_assert(C::KK == 1 && !C::F8, "one matrix instruction a stage");
 #pragma unroll
     for (int s = 0; s < C::NST - 1; ++s) issue(s, s);
@@ -633,9 +641,10 @@ __device__ __forceinline__ Place place(const Group& gr, int col, int nt) {
   return gr.n ? place(gr.t * nt + col, gr.n, nt) : Place{gr.t, col};
 }
 
-// Row tiles are 256 high (codes widened to bf16: 128, whose operands'
-// widening would need more registers than there are); a group's last one takes the smallest height that
-// holds its rows.
+// Row tiles are 256 high (codes widened to bf16: 128, as both the codes and
+// their bf16 values sit in registers); a group's last one takes the smallest
+// height that holds its rows.  The short ones are bound by their fetches and
+// keep three or four stages in LDS.
 constexpr int kBN = 256, kThreads = 512, kCus = 256;
 template <int KIND>
 using T128 = Cfg<KIND, 2, 4, 4, 4, 3>;
@@ -739,8 +748,9 @@ __global__ __launch_bounds__(256) void join_parts(GroupedMm g) {
 // Parts that each group's rows are cut into: where dw has less than a tile
 // for every CU, as many as fill them, of 256 rows on average at least.
 int weight_parts(int E, int P, int N, int K) {
-  const int64_t tiles = static_cast<int64_t>(E) * ((N + Tall<kWeights>::BM - 1) / Tall<kWeights>::BM) *
-                        ((K + kBN - 1) / kBN);
+  constexpr int bm = Tall<kWeights>::BM;
+  const int64_t tiles =
+      static_cast<int64_t>(E) * ((N + bm - 1) / bm) * ((K + kBN - 1) / kBN);
   const int64_t fill = kCus / tiles, rows = P / E / 256;
   const int64_t parts = fill < rows ? fill : rows;
   return parts < 1 ? 1 : static_cast<int>(parts);
@@ -773,15 +783,17 @@ int64_t most_row_tiles(const GroupedMm& g, int bm) {
 }
 
 // ---------------------------------------------------------------------------
-// A few rows (few_rows): bound by reading the weights once.  A
-// workgroup takes 16 columns of one group; its four wavefronts take turns
-// along K (256 bytes of a weight row each), load their weights straight into
-// the matrix instruction's A registers -- 16 rows x 64 bytes a load, eight
-// loads in flight -- and the group's rows of x into its B registers, 16 at a
-// time, and join their sums through LDS in a fixed order.  There is nothing
-// to share through LDS, so the loads need no barrier, and with no more than
-// 64 registers a CU holds 32 wavefronts.  e4m3 codes are widened to bf16
-// (exact) whatever y's type is: at these sizes that costs nothing.
+// A few rows (few_rows): bound by reading the weights once.  A workgroup takes
+// 16 columns of one group (codes: 32); its four wavefronts take turns along K
+// (256 bytes of a weight row each), load their weights straight into the matrix
+// instruction's A registers -- 16 rows x 64 bytes a load, four loads at once --
+// and the group's rows of x into its B registers, 16 at a time, and join their
+// sums through LDS in a fixed order.  There is nothing to share through LDS, so
+// the loads need no barrier, and bf16's 64 registers let a CU hold 32
+// wavefronts (eight loads at once and half as many wavefronts: 82 us against
+// 74 for one token; non-temporal loads: 90).  e4m3 codes are widened to bf16
+// (exact) whatever y's type is; two fragments of columns share the widening of
+// x (8 tokens over 256 experts of 4096 x 6144: 258 us, 5.6 TB/s; one: 333).
 // ---------------------------------------------------------------------------
 
 // Against the tiles, us per call (one N = 4096, K = 6144 bf16 expert; 64 of
@@ -823,7 +835,8 @@ struct Skinny {
 };
 
 template <int KIND>
-__global__ __launch_bounds__(kSkinnyThreads, Skinny<KIND>::kOcc) void grouped_skinny(GroupedMm g, int nb) {
+__global__ __launch_bounds__(kSkinnyThreads, Skinny<KIND>::kOcc) void grouped_skinny(GroupedMm g,
+                                                                                   int nb) {
   using C = Skinny<KIND>;
   constexpr bool F8 = C::F8;
   __shared__ float part[kSkinnyWaves][16][C::kCols + 1];

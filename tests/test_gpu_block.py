@@ -558,6 +558,43 @@ def test_block_norm_grad(gpu_lib, T, d, form, dts):
         assert v is None or torch.equal(v, again[k]), k
 
 
+@pytest.mark.parametrize("form", [NORM_FORMS[1], NORM_FORMS[2]])
+@pytest.mark.parametrize("dts", [(BF16, BF16, BF16), (F32, F32, F32)])
+def test_block_norm_grad_in_place(gpu_lib, form, dts):
+    """dy over y, and dres over dr or over res: the rows fetched ahead are read
+    before any row of theirs is written (more rows than workgroups)."""
+    T, d = 700, 2056
+    ydt, rdt, ndt = dts
+    c, scale, eps = norm_case(T, d, form, ydt, rdt, ndt, 17)
+    want = grad_outputs(c, T, d, ydt, rdt)
+    run_norm_grad(c, want, T, d, scale, eps)
+    for over in ("dr", "res"):
+        m = dict(c, y=c["y"].clone(), dr=c["dr"].clone(), res=c["res"].clone())
+        o = grad_outputs(m, T, d, ydt, rdt)
+        o["dy"], o["dres"] = m["y"], m[over]
+        run_norm_grad(m, o, T, d, scale, eps)
+        for k, v in want.items():
+            assert v is None or torch.equal(v, o[k]), (over, k)
+
+
+def test_block_norm_grad_outputs_may_be_left_out(gpu_lib):
+    """Each output alone equals the same output among all; without sums over the
+    rows no workspace is needed."""
+    T, d = 40, 320
+    c, scale, eps = norm_case(T, d, NORM_FORMS[1], BF16, BF16, BF16, 18)
+    want = grad_outputs(c, T, d, BF16, BF16)
+    run_norm_grad(c, want, T, d, scale, eps)
+    for k, v in want.items():
+        o = dict.fromkeys(want)
+        o[k] = torch.empty_like(v)
+        if k in ("dy", "dres"):
+            moe.moe_block_norm_grad(c["y"], c["res"], c["dr"], c["dn"], o["dy"], o["dres"], None,
+                                    None, None, c["w_post"], c["w_pre"], c["gate"], scale, eps)
+        else:
+            run_norm_grad(c, o, T, d, scale, eps)
+        assert torch.equal(o[k], v), k
+
+
 def test_block_norm_grad_of_no_rows_is_zero(gpu_lib):
     d = 72
     e = torch.empty((0, d), dtype=BF16, device="cuda")
@@ -585,3 +622,47 @@ def test_block_norm_rows_of_zeros(gpu_lib):
                                u["dn"])
     for k in ("dres", "dy"):
         check(o[k], want[k], 64 * U32 * want[k].abs(), k)
+
+
+def test_more_rows_than_one_turn_of_a_grid(gpu_lib):
+    """Row-wise calls on more rows than their largest grid takes at once: the
+    first and last rows equal the same rows alone."""
+    g = gen(90)
+
+    def ends(big, small):
+        return torch.equal(torch.cat([big[:3], big[-3:]]), small)
+
+    T, d = (1 << 21) + 5, 8
+    x = torch.zeros((T, d), dtype=BF16, device="cuda")
+    some = rand(g, 6, d)
+    x[:3], x[-3:] = some[:3], some[3:]
+    w = torch.ones(d, device="cuda")
+    big, small = torch.empty_like(x), torch.empty_like(some)
+    moe.moe_block_norm(None, x, None, big, w_pre=w)
+    moe.moe_block_norm(None, some, None, small, w_pre=w)
+    assert ends(big, small)
+    for block_rows, shape in ((1, ((1 << 26) + 7, 16)), (128, ((1 << 22) + 7, 1, 16))):
+        x = torch.zeros(shape, dtype=BF16, device="cuda")
+        some = rand(g, 6, *shape[1:])
+        x[:3], x[-3:] = some[:3], some[3:]
+        out = []
+        for t in (x, some):
+            c = torch.full(t.shape, 9, dtype=torch.uint8, device="cuda")
+            s = torch.zeros((*t.shape[:-1], 1), device="cuda")
+            moe.moe_blockscale_quantize(t, block_rows, c, s)
+            out.append((c, s))
+        assert ends(out[0][0], out[1][0]) and ends(out[0][1], out[1][1])
+        assert int((out[0][1] == 0).sum()) == 0  # a scale for every block
+    del x, out
+    P, f = (1 << 21) + 5, 2056
+    gu = torch.zeros((P, 2 * f), dtype=BF16, device="cuda")
+    some = rand(g, 6, 2 * f)
+    gu[:3], gu[-3:] = some[:3], some[3:]
+    big, small = (torch.empty((n, f), dtype=BF16, device="cuda") for n in (P, 6))
+    moe.moe_swiglu(gu, big)
+    moe.moe_swiglu(some, small)
+    assert ends(big, small)
+    dgu = torch.empty((6, 2 * f), dtype=BF16, device="cuda")
+    moe.moe_swiglu_grad(some, small, dgu)
+    moe.moe_swiglu_grad(gu, big, gu)
+    assert ends(gu, dgu)
