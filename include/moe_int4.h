@@ -27,6 +27,8 @@
  *                   one-time conversion of a checkpoint)
  *   moe_pack_experts one-time byte bijection of the expert blocks into the
  *                   tiled layout the FFN kernels stream
+ * (moe_int4_block.h has the layer on float and 8-bit weights, its gradients and
+ * the norms around it.)
  *
  * Conventions common to every call:
  *  - Every pointer argument except `shape` is a DEVICE pointer owned by the
