@@ -23,7 +23,8 @@
  * anything is enqueued.  Results do not depend on the order in which
  * workgroups run (no atomics), so a call repeated on the same inputs gives the
  * same bits.  Tensors are row-major without gaps; bf16 and f32 arrays are
- * 16-byte aligned, e4m3 codes too, int32 and float32 vectors 4-byte.
+ * 16-byte aligned, e4m3 codes and the norms' weights too, int32 arrays, scales
+ * and the weights' gradients of the norms 4-byte.
  *
  * Rows grouped by expert: position p belongs to expert e when
  *   offsets[e] <= p < offsets[e + 1],
@@ -51,8 +52,9 @@ extern "C" {
  *  N, K      output and input columns; multiples of 8, 8..65536
  *  x         [x_rows][K] bf16; x_rows >= P without rows
  *  rows      [P] int32 or NULL; an entry outside [0, x_rows * rows_div) stands
- *            for a row of zeros.  x_rows * rows_div <= 2^24
- *  rows_div  1..256 (1 without rows)
+ *            for a row of zeros (its results are zeros, NaN where the weights
+ *            are not finite).  x_rows * rows_div <= 2^24
+ *  rows_div  1..256 (1 without rows, unless P is 0)
  *  w         [E][N][K] bf16
  *  y         out [P][N], bf16 or f32; must not overlap an input */
 moe_status moe_grouped_mm(int32_t E, int32_t P, int32_t N, int32_t K, const void* x,
@@ -103,7 +105,8 @@ moe_status moe_blockscale_quantize(int32_t n_mats, int32_t R, int32_t K, const v
 /* moe_grouped_mm over e4m3 codes:
  *   y[p][n] = sum_b xs[row(p)][b] * ws[e][n / 128][b] *
  *             sum over k in block b of wq[e][n][k] * xq[row(p)][k]
- * with any float32 scales (not only moe_blockscale_quantize's).
+ * with any float32 scales (not only moe_blockscale_quantize's); the product of
+ * the two scales is taken first, in float32, so it is to be finite.
  *  N a multiple of 8 and K of 16, 16..65536
  *  xq [x_rows][K], xs [x_rows][ceil(K/128)], wq [E][N][K],
  *  ws [E][ceil(N/128)][ceil(K/128)]; rows as in moe_grouped_mm

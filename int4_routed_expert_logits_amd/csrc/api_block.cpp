@@ -36,7 +36,7 @@ moe_status check_sizes(int32_t E, int32_t P, int32_t N, int32_t K, int k_step) {
 // The gathered operand's rows.
 moe_status check_rows(int32_t P, int32_t x_rows, const int32_t* rows, int32_t rows_div) {
   if (x_rows < 0 || rows_div < 1) return MOE_ERR_SHAPE;
-  if (!rows && (x_rows < P || rows_div != 1)) return MOE_ERR_SHAPE;
+  if (!rows && P > 0 && (x_rows < P || rows_div != 1)) return MOE_ERR_SHAPE;
   if (rows_div > kMaxRowsDiv || static_cast<int64_t>(x_rows) * rows_div > kMaxPositions)
     return MOE_ERR_UNSUPPORTED;
   return aligned(rows, 4) ? MOE_OK : MOE_ERR_ALIGN;

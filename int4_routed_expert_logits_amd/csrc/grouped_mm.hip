@@ -889,7 +889,7 @@ __global__ __launch_bounds__(kSkinnyThreads, Skinny<KIND>::kOcc) void grouped_sk
         for (int h = 0; h < C::kLoads / 2; ++h) {
           const int blk = k0 / kBlock + h;
           if (blk >= kb) break;
-          const float s = src >= 0 ? ws[blk] * g.r_scale[src * kb + blk] : 0.0f;
+          const float s = ws[blk] * (src >= 0 ? g.r_scale[src * kb + blk] : 0.0f);
           f32x4_t p[C::kFrags];
 #pragma unroll
           for (int f = 0; f < C::kFrags; ++f) p[f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};

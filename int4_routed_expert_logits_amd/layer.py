@@ -178,10 +178,22 @@ class FloatLayerBuffers:
             workspace=new(max(B.moe_route_workspace_bytes(sh, T), 256), dtype=torch.uint8))
 
 
+def _check_float(fn: str, x, experts: FloatExperts, buf: FloatLayerBuffers):
+    if tuple(x.shape) != (buf.T, buf.shape.d):
+        raise ValueError(f"{fn}: x has shape {tuple(x.shape)}, the buffers hold "
+                         f"{(buf.T, buf.shape.d)}")
+    if (experts.shared_gate_up is None) != (buf.y_shared is None):
+        raise ValueError(f"{fn}: the shape and the weights disagree about a shared expert")
+    if (experts.scales is None) != (buf.codes is None):
+        raise ValueError(f"{fn}: 8-bit experts take buffers allocated with codes=True, bf16 ones "
+                         "without")
+
+
 def run_layer_float(x, w_router, bias, experts: FloatExperts, buf: FloatLayerBuffers, stream=None):
     """The layer for x [T, d] bf16 on float or 8-bit experts: route and union,
     gate and up products over the gathered tokens, SwiGLU, down products,
     combine."""
+    _check_float("run_layer_float", x, experts, buf)
     sh, b, k = buf.shape, buf, buf.shape.top_k
     B.moe_route_union(sh, x, w_router, bias, b.topk_idx, b.topk_w, b.counts, b.offsets, b.perm,
                       b.inv_perm, b.active, b.n_active, b.workspace, stream)
@@ -255,6 +267,9 @@ def run_layer_float_grad(dout, x, experts: FloatExperts, buf: FloatLayerBuffers,
     """Gradient of the run_layer_float call that filled buf (bf16 experts and y)
     for dout [T, d] bf16 of its output: the experts' weights, topk_w, and x
     through the experts (x through the router is the caller's, from dtopk_w)."""
+    _check_float("run_layer_float_grad", x, experts, buf)
+    if experts.scales is not None:
+        raise ValueError("run_layer_float_grad: 8-bit experts have no gradient")
     sh, b, k = buf.shape, buf, buf.shape.top_k
     B.moe_combine_grad(sh, dout, b.y, b.inv_perm, b.topk_w, g.dy, g.dtopk_w, stream)
     B.moe_grouped_mm_dw(g.dy, b.h, b.offsets, g.ddown, g.workspace, stream=stream)
@@ -292,10 +307,17 @@ def run_block(res, norms: BlockNorms, layer, normed, res_out, next_norms=None, n
     buffer of the type it takes), such as run_layer or run_layer_float with the
     rest bound.  With next_norms, next_normed gets the next block's pre norm in
     the same pass; hand it to the next block as `layer`'s input (its first norm
-    is then done: call layer on it and moe_block_norm)."""
+    is then done: call layer on it and moe_block_norm).  The post norm and the
+    next pre norm then share their eps; without a post norm the next one's holds."""
+    eps = norms.eps
+    if next_norms is not None and next_norms.eps != eps:
+        if norms.w_post is not None:
+            raise ValueError(f"run_block: a post norm with eps {eps} and a next pre norm with "
+                             f"{next_norms.eps} are not one pass")
+        eps = next_norms.eps
     B.moe_block_norm(None, res, None, normed, w_pre=norms.w_pre, eps=norms.eps, stream=stream)
     out = layer(normed)
     B.moe_block_norm(out, res, res_out, next_normed, norms.w_post,
                      None if next_norms is None else next_norms.w_pre, norms.gate, norms.scale,
-                     norms.eps, stream)
+                     eps, stream)
     return res_out

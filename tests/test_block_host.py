@@ -12,6 +12,7 @@ import torch
 import block_ref as ref
 import int4_routed_expert_logits_amd as moe
 from int4_routed_expert_logits_amd import _binding as B
+from int4_routed_expert_logits_amd import layer as L
 
 P = 1 << 20  # a 256-byte aligned stand-in address (never dereferenced)
 MIS = P + 4
@@ -187,6 +188,8 @@ def test_block_norm_grad_workspace(lib):
 def test_calls_without_work_return_ok(lib):
     """No rows: nothing to enqueue, and no pointer is needed but the ones checked."""
     assert lib.moe_grouped_mm(*edit(MM, P=0, x=None, w=None, y=None, off=None)) == B.MOE_OK
+    # an empty rows tensor has no address
+    assert lib.moe_grouped_mm(*edit(MM, P=0, rows=None, div=2)) == B.MOE_OK
     assert lib.moe_grouped_mm_dx(*edit(DX, P=0, dy=None, w=None, dx=None, off=None)) == B.MOE_OK
     assert lib.moe_blockscale_mm(*edit(BS, P=0, xq=None, wq=None, y=None, off=None)) == B.MOE_OK
     assert lib.moe_blockscale_quantize(0, 5, 64, None, H, 1, None, None, None) == B.MOE_OK
@@ -209,6 +212,35 @@ def test_binding_checks_tensors():
         moe.moe_blockscale_mm(bf(4, 8, 2), None, bf(2, 8, 8), None, off, bf(4, 8))
     with pytest.raises(ValueError, match="neither y nor res"):
         moe.moe_block_norm(None, None, None, None)
+
+
+def test_layer_checks_its_arguments():
+    """Before anything is enqueued (these tensors are not on a GPU)."""
+    E, d, f, T = 4, 64, 64, 3
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    ex = L.FloatExperts(bf(E, 2 * f, d), bf(E, d, f))
+    buf = L.FloatLayerBuffers.allocate(moe.Shape(d, f, E, 2, 64, 0), T, device="cpu")
+    codes = L.FloatLayerBuffers.allocate(moe.Shape(d, f, E, 2, 64, 0), T, codes=True, device="cpu")
+    grads = L.FloatLayerGrads.allocate(buf, ex)
+    wr = torch.zeros(E, d)
+    with pytest.raises(ValueError, match="x has shape"):
+        L.run_layer_float(bf(T + 1, d), wr, None, ex, buf)
+    with pytest.raises(ValueError, match="x has shape"):
+        L.run_layer_float_grad(bf(T, d), bf(T - 1, d), ex, buf, grads)
+    with pytest.raises(ValueError, match="codes=True"):
+        L.run_layer_float(bf(T, d), wr, None, ex, codes)
+    ex.scales = (torch.zeros(E, 1, 1), torch.zeros(E, 1, 1))
+    with pytest.raises(ValueError, match="codes=True"):
+        L.run_layer_float(bf(T, d), wr, None, ex, buf)
+    with pytest.raises(ValueError, match="no gradient"):
+        L.run_layer_float_grad(bf(T, d), bf(T, d), ex, codes, grads)
+    ex.shared_gate_up = bf(1, 2 * f, d)
+    with pytest.raises(ValueError, match="shared expert"):
+        L.run_layer_float(bf(T, d), wr, None, ex, codes)
+    norms = L.BlockNorms(torch.ones(d), torch.ones(d), eps=1e-5)
+    with pytest.raises(ValueError, match="eps"):
+        L.run_block(bf(T, d), norms, lambda n: n, bf(T, d), bf(T, d), L.BlockNorms(torch.ones(d)),
+                    bf(T, d))
 
 
 # ----------------------------------------------------------------------------

@@ -170,7 +170,7 @@ def test_block_around_a_layer(gpu_lib, kind):
     norms = L.BlockNorms(w[0], w[1], gate, 0.5, 1e-5)
     res = rand(g, T, d)
     normed, res_out, nxt = (torch.empty((T, d), dtype=BF16, device="cuda") for _ in range(3))
-    L.run_block(res, norms, layer, normed, res_out, L.BlockNorms(w[2]), nxt)
+    L.run_block(res, norms, layer, normed, res_out, L.BlockNorms(w[2], eps=1e-5), nxt)
     _, wn = ref.block_norm(None, up(res), None, up(w[0]), None, 1.0, 1e-5)
     check(normed, wn, (HALF + (d + 16) * U32) * wn.abs(), "normed")
     alone = layer(normed).clone()
@@ -179,6 +179,37 @@ def test_block_around_a_layer(gpu_lib, kind):
     small = (d + 32) * U32
     check(res_out, wr, HALF * wr.abs() + small * ((wr - up(res)).abs() + wr.abs()) + 1e-6, "res")
     check(nxt, wn, HALF * wn.abs() + 4 * small * wn.abs() + 1e-5, "next")
+
+
+def test_block_without_a_post_norm_takes_the_next_eps(gpu_lib):
+    """eps decides these norms: the rows' squares are far below it."""
+    T, d = 3, 64
+    g = gen(21)
+    res, out = rand(g, T, d, scale=1e-3), rand(g, T, d, scale=1e-3)
+    w = [1 + rand(g, d, dt=F32, scale=0.1) for _ in range(2)]
+    normed, res_out, nxt = (torch.empty((T, d), dtype=BF16, device="cuda") for _ in range(3))
+    L.run_block(res, L.BlockNorms(w[0], eps=1e-2), lambda n: out, normed, res_out,
+                L.BlockNorms(w[1], eps=1e-4), nxt)
+    wr, wn = ref.block_norm(up(out), up(res), None, up(w[1]), None, 1.0, 1e-4)
+    # three float32 roundings of r and the d squares of its sum
+    check(res_out, wr, (HALF + 3 * U32) * wr.abs(), "res")
+    check(nxt, wn, (HALF + 3 * U32) * wn.abs() + (d + 16) * U32 * wn.abs() + 1e-9, "next")
+
+
+def test_layer_of_no_tokens(gpu_lib):
+    """T = 0: nothing to route, empty outputs, zero gradients of every weight."""
+    sh = SHAPES["shared"]
+    x, wr, bias, ex = make(sh, 0, 70)
+    b = L.FloatLayerBuffers.allocate(sh, 0)
+    assert L.run_layer_float(x, wr, bias, ex, b).shape == (0, sh.d)
+    g = L.FloatLayerGrads.allocate(b, ex)
+    for t in (g.dgate_up, g.ddown, g.dshared_gate_up, g.dshared_down):
+        t.fill_(7.0)
+    L.run_layer_float_grad(rand(gen(71), 0, sh.d), x, ex, b, g)
+    for t in (g.dgate_up, g.ddown, g.dshared_gate_up, g.dshared_down):
+        assert (t == 0).all()
+    q = L.FloatLayerBuffers.allocate(sh, 0, codes=True)
+    assert L.run_layer_float(x, wr, bias, L.FloatExperts.quantize(ex), q).shape == (0, sh.d)
 
 
 def test_captured_and_replayed(gpu_lib):
