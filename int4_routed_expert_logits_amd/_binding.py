@@ -415,8 +415,9 @@ def moe_cache_layer_decode(cache: int, x, w_router, bias, shared, topk_idx, topk
 # GPU, on `stream` or on that GPU's current stream.
 # ----------------------------------------------------------------------------
 
-# set by _types(), which every call below makes first
+# set by _types(), which every call below makes first (once: `_T or _types()`)
 _T = _raw_stream = _current_device = None
+_CODES = {}  # torch type -> moe_dtype
 
 
 def _types():
@@ -428,6 +429,7 @@ def _types():
         # Stream takes as long as a launch
         _raw_stream = torch._C._cuda_getCurrentRawStream
         _current_device = torch._C._cuda_getDevice
+        _CODES.update({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
         _T = ((torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32), (torch.int32,),
               (torch.float8_e4m3fn, torch.uint8))
     return _T
@@ -482,14 +484,14 @@ def _run(fn: str, dev: int, stream, *args):
 
 
 def _rows_args(fn, dev, P, rows):
-    return None if rows is None else _take(fn, dev, "rows", rows, _types()[3], (P,))
+    return None if rows is None else _take(fn, dev, "rows", rows, (_T or _types())[3], (P,))
 
 
 def moe_grouped_mm(x, w, offsets, y, rows=None, rows_div: int = 1, stream=None):
     """y[p] = w[e] x[rows[p] // rows_div] (x[p] without rows): x [X, K] bf16,
     w [E, N, K] bf16, offsets [E + 1] and rows [P] int32, y [P, N] bf16/f32."""
     fn, dev = "moe_grouped_mm", x.get_device()
-    bf16, _, floats, i32, _ = _types()
+    bf16, _, floats, i32, _ = _T or _types()
     E, N, K = _dim(fn, "w", w, 3)
     P, X = _dim(fn, "y", y, 2)[0], _dim(fn, "x", x, 2)[0]
     _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "x", x, bf16, (X, K)), X,
@@ -501,7 +503,7 @@ def moe_grouped_mm(x, w, offsets, y, rows=None, rows_div: int = 1, stream=None):
 def moe_grouped_mm_dx(dy, w, offsets, dx, stream=None):
     """dx[p] = w[e]^T dy[p]: dy [P, N] bf16, w [E, N, K] bf16, dx [P, K] bf16/f32."""
     fn, dev = "moe_grouped_mm_dx", dy.get_device()
-    bf16, _, floats, i32, _ = _types()
+    bf16, _, floats, i32, _ = _T or _types()
     E, N, K = _dim(fn, "w", w, 3)
     P = _dim(fn, "dx", dx, 2)[0]
     _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "dy", dy, bf16, (P, N)),
@@ -519,7 +521,7 @@ def moe_grouped_mm_dw(dy, x, offsets, dw, workspace=None, rows=None, rows_div: i
     """dw[e] = sum over e's positions of dy[p] x[row(p)]^T: dy [P, N] and
     x [X, K] bf16, dw [E, N, K] bf16/f32 (all of it written)."""
     fn, dev = "moe_grouped_mm_dw", dy.get_device()
-    bf16, _, floats, i32, _ = _types()
+    bf16, _, floats, i32, _ = _T or _types()
     E, N, K = _dim(fn, "dw", dw, 3)
     P, X = _dim(fn, "dy", dy, 2)[0], _dim(fn, "x", x, 2)[0]
     ws, nws = _workspace(fn, dev, workspace)
@@ -534,7 +536,7 @@ def moe_blockscale_quantize(x, block_rows: int, codes, scales, stream=None):
     (float8_e4m3fn or uint8) and float32 scales per 128 columns: [.., R, K/128]
     for block_rows 1, [.., R/128, K/128] for 128 (rounded up)."""
     fn, dev = "moe_blockscale_quantize", x.get_device()
-    _, f32, floats, _, codes_t = _types()
+    _, f32, floats, _, codes_t = _T or _types()
     if x.dim() not in (2, 3):
         raise ValueError(f"{fn}: x has {x.dim()} dimensions, not 2 or 3")
     *lead, R, K = x.shape
@@ -548,7 +550,7 @@ def moe_blockscale_mm(xq, xs, wq, ws, offsets, y, rows=None, rows_div: int = 1, 
     """moe_grouped_mm over e4m3 codes: xq [X, K] with xs [X, K/128], wq
     [E, N, K] with ws [E, N/128, K/128] (rounded up), y [P, N] bf16/f32."""
     fn, dev = "moe_blockscale_mm", xq.get_device()
-    _, f32, floats, i32, codes_t = _types()
+    _, f32, floats, i32, codes_t = _T or _types()
     E, N, K = _dim(fn, "wq", wq, 3)
     P, X, kb = _dim(fn, "y", y, 2)[0], _dim(fn, "xq", xq, 2)[0], -(-K // 128)
     _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "xq", xq, codes_t, (X, K)),
@@ -560,7 +562,7 @@ def moe_blockscale_mm(xq, xs, wq, ws, offsets, y, rows=None, rows_div: int = 1, 
 
 
 def _n_rows(fn, dev, n_rows):
-    return None if n_rows is None else _take(fn, dev, "n_rows", n_rows, _types()[3], (1,))
+    return None if n_rows is None else _take(fn, dev, "n_rows", n_rows, (_T or _types())[3], (1,))
 
 
 def moe_swiglu(gu, h, n_rows=None, stream=None):
@@ -568,14 +570,14 @@ def moe_swiglu(gu, h, n_rows=None, stream=None):
     f32; n_rows: device int32 [1], rows from it on are left as they were."""
     fn, dev = "moe_swiglu", gu.get_device()
     P, f = _dim(fn, "h", h, 2)
-    _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, _types()[2], (P, 2 * f)),
+    _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, (_T or _types())[2], (P, 2 * f)),
          _take(fn, dev, "h", h, (gu.dtype,), (P, f)), _code(gu.dtype), _n_rows(fn, dev, n_rows))
 
 
 def moe_swiglu_quantize(gu, codes, scales, n_rows=None, stream=None):
     """moe_swiglu's result as e4m3 codes [P, f] and scales [P, f/128] (rounded up)."""
     fn, dev = "moe_swiglu_quantize", gu.get_device()
-    _, f32, floats, _, codes_t = _types()
+    _, f32, floats, _, codes_t = _T or _types()
     P, f = _dim(fn, "codes", codes, 2)
     _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, floats, (P, 2 * f)), _code(gu.dtype),
          _take(fn, dev, "codes", codes, codes_t, (P, f)),
@@ -586,7 +588,7 @@ def moe_swiglu_grad(gu, dh, dgu, n_rows=None, stream=None):
     """moe_swiglu's gradient: gu, dgu [P, 2 f], dh [P, f], one type; dgu may be gu."""
     fn, dev = "moe_swiglu_grad", gu.get_device()
     P, f = _dim(fn, "dh", dh, 2)
-    _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, _types()[2], (P, 2 * f)),
+    _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, (_T or _types())[2], (P, 2 * f)),
          _take(fn, dev, "dh", dh, (gu.dtype,), (P, f)),
          _take(fn, dev, "dgu", dgu, (gu.dtype,), (P, 2 * f)), _code(gu.dtype), _n_rows(fn, dev, n_rows))
 
@@ -595,21 +597,21 @@ def moe_combine_grad(shape, dout, y, inv_perm, topk_w, dy, dtopk_w, stream=None)
     """moe_combine's gradient: dout [T, d], y and dy [T * k, d] (bf16/f32, one
     type; dy may be y), inv_perm [T * k] int32, topk_w and dtopk_w [T, k] f32."""
     fn, dev = "moe_combine_grad", dout.get_device()
-    _, f32, floats, i32, _ = _types()
+    _, f32, floats, i32, _ = _T or _types()
     sh = _shape(shape)
-    T, n = _dim(fn, "dout", dout, 2)[0], dout.shape[0] * sh.top_k
-    _run(fn, dev, stream, ctypes.byref(sh), T,
-         _take(fn, dev, "dout", dout, floats, (T, sh.d)), _code(dout.dtype),
-         _take(fn, dev, "y", y, floats, (n, sh.d)), _code(y.dtype),
+    k, d, ydt = sh.top_k, sh.d, y.dtype
+    T = _dim(fn, "dout", dout, 2)[0]
+    n, by_slot = T * k, (T, k)
+    _run(fn, dev, stream, ctypes.byref(sh), T, _take(fn, dev, "dout", dout, floats, (T, d)),
+         _code(dout.dtype), _take(fn, dev, "y", y, floats, (n, d)), _code(ydt),
          _take(fn, dev, "inv_perm", inv_perm, i32, (n,)),
-         _take(fn, dev, "topk_w", topk_w, f32, (T, sh.top_k)),
-         _take(fn, dev, "dy", dy, (y.dtype,), (n, sh.d)),
-         _take(fn, dev, "dtopk_w", dtopk_w, f32, (T, sh.top_k)))
+         _take(fn, dev, "topk_w", topk_w, f32, by_slot), _take(fn, dev, "dy", dy, (ydt,), (n, d)),
+         _take(fn, dev, "dtopk_w", dtopk_w, f32, by_slot))
 
 
 def _norm_args(fn, y, res, w_post, w_pre, gate, scale):
     """The first arguments of the block norm calls and the sizes they check by."""
-    bf16, f32, floats, _, _ = _types()
+    bf16, f32, floats, _, _ = _T or _types()
     first = y if y is not None else res
     if first is None:
         raise ValueError(f"{fn}: neither y nor res")
@@ -632,7 +634,7 @@ def moe_block_norm(y, res, res_out, normed, w_post=None, w_pre=None, gate=None, 
     y's without res), w_post, w_pre [d] f32, gate [1 or T, d] of y's type.  Any
     of y, res, res_out, w_post, gate and (w_pre with normed) may be None."""
     fn = "moe_block_norm"
-    _, _, floats, _, _ = _types()
+    _, _, floats, _, _ = _T or _types()
     dev, T, d, _, rdt, head, w2 = _norm_args(fn, y, res, w_post, w_pre, gate, scale)
     if res is None and res_out is not None:
         rdt = res_out.dtype
@@ -642,10 +644,10 @@ def moe_block_norm(y, res, res_out, normed, w_post=None, w_pre=None, gate=None, 
 
 
 def _code(dtype) -> int:
-    bf16, f32, *_ = _types()
-    if dtype not in bf16 + f32:
+    code = _CODES.get(dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    return MOE_BF16 if dtype in bf16 else MOE_F32
+    return code
 
 
 def moe_block_norm_grad_workspace_bytes(T: int, d: int) -> int:
@@ -658,7 +660,7 @@ def moe_block_norm_grad(y, res, dr, dn, dy, dres, dw_post, dw_pre, dgate, w_post
     its type; or None) and dn (of normed): dy, dres [T, d], dw_post, dw_pre [d],
     dgate of gate's shape, each None where not wanted."""
     fn = "moe_block_norm_grad"
-    _, f32, floats, _, _ = _types()
+    _, f32, floats, _, _ = _T or _types()
     dev, T, d, ydt, rdt, head, w2 = _norm_args(fn, y, res, w_post, w_pre, gate, scale)
     if res is None:
         rdt = dr.dtype if dr is not None else dres.dtype if dres is not None else rdt
