@@ -140,6 +140,7 @@ struct Group {
   int e, a, b;  // expert, its grouped positions
   int t;        // this workgroup's row tile of the group
   int n;        // the group's row tiles that come together with it
+  int high;     // how many of them, the first ones, are kExtraRows higher
 };
 
 // The group's bounds as the kernels take them: whatever offsets holds, they
@@ -153,18 +154,24 @@ __device__ __forceinline__ void group_bounds(const GroupedMm& g, int e, int& a, 
 // over the workgroup gives their first tiles, and the owner tells the others.
 // e = -1 past the last tile.  Groups have ceil(rows / BM) tiles, in ascending
 // order of the groups; with `tall_first`, the tiles of more than BM / 2 rows
-// come before all others.
-template <int BM, int THREADS>
+// come before all others.  EXTRA: the last tile's rows are spread over the
+// others, EXTRA each, where they suffice.
+template <int BM, int THREADS, int EXTRA = 0>
 __device__ Group find_group(const GroupedMm& g, int64_t tile, bool tall_first, int* sh) {
   constexpr int kPer = 1024 / THREADS, kWaves = THREADS / kWave;  // E <= 1024
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave;
-  int a[kPer], b[kPer], n[kPer], low[kPer], inc = 0, inc_low = 0;
+  int a[kPer], b[kPer], n[kPer], low[kPer], high[kPer], inc = 0, inc_low = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    a[i] = b[i] = 0;
+    a[i] = b[i] = high[i] = 0;
     if (kPer * t + i < g.E) group_bounds(g, kPer * t + i, a[i], b[i]);
     n[i] = (b[i] - a[i] + BM - 1) / BM;
-    const int rest = (b[i] - a[i]) % BM;
+    int rest = (b[i] - a[i]) % BM;
+    if (EXTRA > 0 && rest > 0 && rest <= EXTRA * (n[i] - 1)) {
+      high[i] = (rest + EXTRA - 1) / (EXTRA > 0 ? EXTRA : 1);
+      rest = 0;
+      --n[i];
+    }
     low[i] = tall_first && rest > 0 && rest <= BM / 2;  // its last tile goes to the end
     n[i] -= low[i];
     inc += n[i];
@@ -201,13 +208,14 @@ __device__ Group find_group(const GroupedMm& g, int64_t tile, bool tall_first, i
       sh[2 * kWaves + 2] = b[i];
       sh[2 * kWaves + 3] = mid ? static_cast<int>(tile) - first : n[i];
       sh[2 * kWaves + 4] = mid ? n[i] : 0;
+      sh[2 * kWaves + 5] = high[i];
     }
     first += n[i];
     first_low += low[i];
   }
   __syncthreads();
   Group r{sh[2 * kWaves], sh[2 * kWaves + 1], sh[2 * kWaves + 2], sh[2 * kWaves + 3],
-          sh[2 * kWaves + 4]};
+          sh[2 * kWaves + 4], sh[2 * kWaves + 5]};
   __syncthreads();
   return r;
 }
@@ -648,7 +656,12 @@ __device__ __forceinline__ Place place(const Group& gr, int col, int nt) {
 
 // Row tiles are 256 high (codes widened to bf16: 128, as both the codes and
 // their bf16 values sit in registers); a group's last one takes the smallest
-// height that holds its rows.  The short ones are bound by their fetches and
+// height that holds its rows.  Where bf16 rows left over are at most 64 for
+// each full tile, as many of those as it takes are 320 high instead (160
+// accumulators a lane, 247 registers): a tile of few rows would read all of the
+// weights once more (64 groups of about 512 rows over 2048 x 2048 341 us without,
+// 318 with; one of 4200 rows over 4096 x 4096 161 and 121; the skewed prompt
+// 2440 and 2410).  Codes have no registers left for it.  The short ones are bound by their fetches and
 // keep three or four stages in LDS.
 constexpr int kBN = 256, kThreads = 512, kCus = 256;
 template <int KIND>
@@ -657,6 +670,8 @@ template <int KIND>
 using Tall = std::conditional_t<
     (KIND <= kWeightsBy), Cfg<KIND, 2, 4, 8, 4, 4, 64, true>,
     std::conditional_t<KIND == kCodes, Cfg<KIND, 2, 4, 8, 4, 2>, T128<KIND>>>;
+template <int KIND>
+using High = Cfg<KIND, 2, 4, 10, 4, 4, 64, true>;
 template <int KIND>
 using T64 = Cfg<KIND, 1, 8, 4, 2, 3>;
 template <int KIND>
@@ -677,21 +692,28 @@ constexpr int lds_of() {
 
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
-  constexpr int kBM = Tall<KIND>::BM;
+  constexpr int kBM = Tall<KIND>::BM, kExtra = KIND <= kInput ? High<KIND>::BM - kBM : 0;
   __shared__ __align__(1024)
-      uint8_t smem[lds_of<Tall<KIND>, T128<KIND>, T64<KIND>, T32<KIND>>()];
+      uint8_t smem[lds_of<std::conditional_t<(kExtra > 0), High<KIND>, Tall<KIND>>, T128<KIND>,
+                          T64<KIND>, T32<KIND>>()];
   const bool tall_first = g.P >= kTallFirstRows * g.E;
   const int64_t id = my_tile(tall_first ? kLongRun : kShortRun);
   const int nt = ((KIND == kInput ? g.K : g.N) + kBN - 1) / kBN;
   const Group gr =
-      find_group<kBM, kThreads>(g, id / nt, tall_first, reinterpret_cast<int*>(smem));
+      find_group<kBM, kThreads, kExtra>(g, id / nt, tall_first, reinterpret_cast<int*>(smem));
   if (gr.e < 0) return;
   const Place at = place(gr, static_cast<int>(id % nt), nt);
-  const int m0 = gr.a + at.m * kBM, n0 = at.n * kBN;
-  const int mend = min(gr.b, m0 + kBM);
+  const int m0 = gr.a + at.m * kBM + min(at.m, gr.high) * kExtra, n0 = at.n * kBN;
+  const int mend = min(gr.b, m0 + kBM + (at.m < gr.high ? kExtra : 0));
   auto run = [&](auto cfg) {
     tile<decltype(cfg)>(g, smem, gr.e, m0, mend, n0, gr.a, gr.b, g.out, g.out_f32);
   };
+  if constexpr (kExtra > 0) {
+    if (mend - m0 > kBM) {
+      run(High<KIND>{});
+      return;
+    }
+  }
   if (mend - m0 > 128)
     run(Tall<KIND>{});
   else if (mend - m0 > 64)

@@ -66,8 +66,15 @@ COUNTS = {
     "many": [i % 5 for i in range(300)],
     "last_of_1024": [0] * 1023 + [7],
     "none": [0, 0, 0],
+    # around every height of the large tiles (tall ones first, and in order)
+    "heights": [257, 288, 289, 320, 321, 512, 513, 576, 640, 641, 768, 900, 960, 961, 1, 33, 65,
+                129, 255, 256],
 }
-SIZES = [(8, 8), (64, 64), (72, 200), (264, 136), (512, 320)]  # N, K
+COUNTS["heights_of_200"] = [n for h in COUNTS["heights"] for n in (h, *[0] * 9)]
+SIZES = [(8, 8), (64, 64), (72, 200), (264, 136), (512, 320), (1544, 72), (72, 1544)]  # N, K
+# enough tiles for the large ones: forward, input gradient
+HEIGHTS = [("heights", 5), ("heights_of_200", 3)]
+HEIGHTS_DX = [("heights", 6), ("heights_of_200", 2)]
 MM = [("one", 0), ("one", 4), ("empty_ends", 2), ("edges", 1), ("edges", 3), ("edges", 4),
       ("long", 2), ("long", 4), ("many", 0), ("many", 2), ("last_of_1024", 2), ("none", 1)]
 
@@ -92,7 +99,7 @@ def mm_case(counts, size, gather, tail, seed):
 
 @pytest.mark.parametrize("out", [BF16, F32])
 @pytest.mark.parametrize("gather,tail", [(False, 0), (True, 5)])
-@pytest.mark.parametrize("counts,size", MM)
+@pytest.mark.parametrize("counts,size", MM + HEIGHTS)
 def test_grouped_mm(gpu_lib, counts, size, gather, tail, out):
     say(f"grouped_mm {counts} {SIZES[size]} gather={gather} tail={tail} {out}")
     c = mm_case(counts, size, gather, tail, 11 * size + gather)
@@ -105,7 +112,7 @@ def test_grouped_mm(gpu_lib, counts, size, gather, tail, out):
 
 
 @pytest.mark.parametrize("out", [BF16, F32])
-@pytest.mark.parametrize("counts,size", MM)
+@pytest.mark.parametrize("counts,size", MM + HEIGHTS_DX)
 def test_grouped_mm_dx(gpu_lib, counts, size, out):
     say(f"grouped_mm_dx {counts} {SIZES[size]} {out}")
     c = mm_case(counts, size, False, 3, 100 + size)
@@ -127,7 +134,7 @@ def run_dw(c, out, dw=None):
 
 @pytest.mark.parametrize("out", [BF16, F32])
 @pytest.mark.parametrize("gather,tail", [(False, 0), (True, 5)])
-@pytest.mark.parametrize("counts,size", [m for m in MM if m[0] != "last_of_1024"])
+@pytest.mark.parametrize("counts,size", [m for m in MM + [("heights", 3)] if m[0] != "last_of_1024"])
 def test_grouped_mm_dw(gpu_lib, counts, size, gather, tail, out):
     say(f"grouped_mm_dw {counts} {SIZES[size]} gather={gather} tail={tail} {out}")
     c = mm_case(counts, size, gather, tail, 200 + 11 * size + gather)
@@ -294,7 +301,7 @@ def blockscale_ref(c):
 
 @pytest.mark.parametrize("out", [BF16, F32])
 @pytest.mark.parametrize("gather,tail", [(False, 0), (True, 5)])
-@pytest.mark.parametrize("counts,size", MM)
+@pytest.mark.parametrize("counts,size", MM + HEIGHTS)
 def test_blockscale_mm(gpu_lib, counts, size, gather, tail, out):
     """float32: exact products, a float32 sum, and per block one product of the
     scales and one fused multiply-add: K + 2 operations' roundings.  bf16: a
