@@ -428,12 +428,15 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       fetch<C::FI, kUnitMN>(fs, stage, red, lds, wv * C::FI, C::FBytes / 1024);
     } else {
 #pragma unroll
-      for (int j = 0; j < C::FI; ++j) {  // two rows per fetch, half a wavefront each
-        static_assert(kWaveRows == 2 * C::FI, "rows of 512 bytes");
-        const uint32_t r0 = next_row[2 * j], r1 = next_row[2 * j + 1];
-        const int64_t b0 = r0 < g.row_limit ? static_cast<int64_t>(row_div(r0, g.div_magic)) : -1;
-        const int64_t b1 = r1 < g.row_limit ? static_cast<int64_t>(row_div(r1, g.div_magic)) : -1;
-        const int64_t src = lane < kWave / 2 ? b0 : b1;
+      for (int j = 0; j < C::FI; ++j) {  // kPer rows per fetch, as many parts of a wavefront
+        constexpr int kPer = kWaveRows / C::FI;
+        int64_t src = -1;
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) {
+          const uint32_t s = next_row[kPer * j + r];
+          const int64_t b = s < g.row_limit ? static_cast<int64_t>(row_div(s, g.div_magic)) : -1;
+          if (lane / (kWave / kPer) == r) src = b;
+        }
         dma16(fs.off[j] != kNever && src >= 0 ? fs.p[j] + src * g.K * 2 : zero_block(),
               lds + (wv * C::FI + j) * 1024);
       }
@@ -727,25 +730,23 @@ __global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
 // The gradient's tile of a group without rows: zeros, a row of the tile per
 // wavefront (bf16: two).  Through the fragments' stores, of 64 bytes in each of
 // 16 rows, 2.2 GB of them took 456 us, so 405.
+template <class C>
 __device__ void zero_tile(const GroupedMm& g, int e, int m0, int mend, int n0, void* out,
                           bool out_f32) {
-  const int size = out_f32 ? 4 : 2, per = 16 / size, lanes = kBN / per;
+  const int size = out_f32 ? 4 : 2, per = 16 / size, lanes = C::BN / per;
   const int c = n0 + static_cast<int>(threadIdx.x) % lanes * per;
   if (c >= g.K) return;
   uint8_t* p = static_cast<uint8_t*>(out) + (static_cast<int64_t>(e) * g.N * g.K + c) * size;
-  for (int m = m0 + static_cast<int>(threadIdx.x) / lanes; m < mend; m += kThreads / lanes)
+  for (int m = m0 + static_cast<int>(threadIdx.x) / lanes; m < mend; m += C::Threads / lanes)
     *reinterpret_cast<uint4*>(p + static_cast<int64_t>(m) * g.K * size) = make_uint4(0, 0, 0, 0);
 }
 
 // Weights' gradients: every group's [N][K], its rows in g.split parts.  One
 // part: to dw.  More: float32 sums to workspace[part][E][N][K], joined by
 // join_parts.
-template <int KIND>
-__global__ __launch_bounds__(kThreads) void grouped_weight_tiles(GroupedMm g) {
-  using T = Tall<KIND>;
-  using U = T128<KIND>;
-  __shared__ __align__(1024) uint8_t smem[lds_of<T, U>()];
-  const int nt = (g.K + kBN - 1) / kBN, mt = (g.N + T::BM - 1) / T::BM;
+template <class T, class U>
+__device__ __forceinline__ void weight_tile(const GroupedMm& g, uint8_t* smem) {
+  const int nt = (g.K + T::BN - 1) / T::BN, mt = (g.N + T::BM - 1) / T::BM;
   const int64_t id = my_tile(kShortRun);
   const int r = static_cast<int>(id % (mt * nt));
   const int e = static_cast<int>(id / (mt * nt) % g.E), z = static_cast<int>(id / (mt * nt) / g.E);
@@ -762,13 +763,28 @@ __global__ __launch_bounds__(kThreads) void grouped_weight_tiles(GroupedMm g) {
     out_f32 = true;
   }
   const Place at = place(r, mt, nt);
-  const int m0 = at.m * T::BM, n0 = at.n * kBN;
+  const int m0 = at.m * T::BM, n0 = at.n * T::BN;
   if (a >= b)
-    zero_tile(g, e, m0, min(g.N, m0 + T::BM), n0, out, out_f32);
-  else if (g.N - m0 > 128)
+    zero_tile<T>(g, e, m0, min(g.N, m0 + T::BM), n0, out, out_f32);
+  else if (g.N - m0 > U::BM)
     tile<T>(g, smem, e, m0, g.N, n0, a, b, out, out_f32);
   else
     tile<U>(g, smem, e, m0, g.N, n0, a, b, out, out_f32);
+}
+template <int KIND>
+__global__ __launch_bounds__(kThreads) void grouped_weight_tiles(GroupedMm g) {
+  __shared__ __align__(1024) uint8_t smem[lds_of<Tall<KIND>, T128<KIND>>()];
+  weight_tile<Tall<KIND>, T128<KIND>>(g, smem);
+}
+
+// Few weights (SmallDw): 128 x 128 tiles of four wavefronts, so that fewer
+// parts of the rows fill the chip.
+template <int KIND>
+using SmallDw = Cfg<KIND, 2, 2, 4, 4, 3>;
+template <int KIND>
+__global__ __launch_bounds__(256) void grouped_weight_small(GroupedMm g) {
+  __shared__ __align__(1024) uint8_t smem[SmallDw<KIND>::Lds];
+  weight_tile<SmallDw<KIND>, SmallDw<KIND>>(g, smem);
 }
 
 // dw = the parts' sum, in their order; four elements per thread.
@@ -787,15 +803,42 @@ __global__ __launch_bounds__(256) void join_parts(GroupedMm g) {
   }
 }
 
-// Parts that each group's rows are cut into: where dw has less than a tile
-// for every CU, as many as fill them, of 256 rows on average at least.
-int weight_parts(int E, int P, int N, int K) {
-  constexpr int bm = Tall<kWeights>::BM;
-  const int64_t tiles =
-      static_cast<int64_t>(E) * ((N + bm - 1) / bm) * ((K + kBN - 1) / kBN);
-  const int64_t fill = kCus / tiles, rows = P / E / 256;
-  const int64_t parts = fill < rows ? fill : rows;
-  return parts < 1 ? 1 : static_cast<int>(parts);
+// How a weight gradient is laid out: 256 x 256 or 128 x 128 tiles, and where
+// those are too few for the CUs, each group's rows in as many parts as fill
+// them, of 256 rows on average at least.
+struct WeightPlan {
+  bool small;
+  int64_t tiles;  // of one part
+  int parts;
+  int64_t ns;  // expected
+};
+// Time of a plan: its rounds of tiles (a row of a tile's contraction takes 30 or
+// 11 ns, its ends 5 us), whole ones for one group; with several, which are
+// seldom even, their mean and the rest of a group of two and a half times
+// that; the parts' sums written and read.  us, 128 x 128 against 256 x 256 tiles: 4096
+// rows, 1024 x 1024 27 / 38, 2048 x 2048 54 / 62; 16384 rows, 2560 x 2560 327 /
+// 242, 4096 x 3840 653 / 456; 8 groups of 1024 rows, 1024 x 1280 51 / 43, skewed
+// 55 / 79; 32 of 512, 512 x 768 35 / 27, skewed 47 / 84; 16 of 2048, skewed,
+// 2048 x 1024 231 / 181.
+WeightPlan weight_plan(int E, int P, int N, int K, bool small) {
+  using T = Tall<kWeights>;
+  using S = SmallDw<kWeights>;
+  const int bm = small ? S::BM : T::BM, bn = small ? S::BN : T::BN;
+  WeightPlan p{small, static_cast<int64_t>(E) * ((N + bm - 1) / bm) * ((K + bn - 1) / bn), 1, 0};
+  const int64_t fill = kCus / p.tiles, mean = P / E;
+  const int64_t parts = fill < mean / 256 ? fill : mean / 256;
+  if (parts > 1) p.parts = static_cast<int>(parts);
+  const int64_t rows_ns = mean / p.parts * (small ? 11 : 30), all = p.tiles * p.parts;
+  if (E == 1)
+    p.ns = (all + kCus - 1) / kCus * (rows_ns + 5000);
+  else
+    p.ns = (all > kCus ? all : kCus) * (rows_ns + 5000) / kCus + rows_ns * 3 / 2;
+  if (p.parts > 1) p.ns += 3000 + static_cast<int64_t>(E) * N * K * p.parts * 8 / 4500;
+  return p;
+}
+WeightPlan weight_plan(int E, int P, int N, int K) {
+  const WeightPlan a = weight_plan(E, P, N, K, false), b = weight_plan(E, P, N, K, true);
+  return b.ns < a.ns ? b : a;
 }
 
 // Few tiles (narrow outputs, one group of middling size): 64 x 128 tiles of
@@ -980,7 +1023,7 @@ __global__ __launch_bounds__(kSkinnyThreads, Skinny<KIND>::kOcc) void grouped_sk
 }  // namespace
 
 size_t grouped_dw_workspace(int E, int P, int N, int K) {
-  const int parts = weight_parts(E, P, N, K);
+  const int parts = weight_plan(E, P, N, K).parts;
   return parts > 1 ? static_cast<size_t>(parts) * E * N * K * sizeof(float) : 0;
 }
 
@@ -990,12 +1033,14 @@ hipError_t launch_grouped_mm(const GroupedMm& args, GroupedKind kind, hipStream_
     return launch(kernel, dim3(tile_grid(tiles)), dim3(threads), 0, stream, g);
   };
   if (kind == kGroupedWeights) {
-    constexpr int bm = Tall<kWeights>::BM;
-    g.split = weight_parts(g.E, g.P, g.N, g.K);
-    const int64_t tiles = static_cast<int64_t>(g.E) * ((g.N + bm - 1) / bm) *
-                          ((g.K + kBN - 1) / kBN) * g.split;
-    const hipError_t e = g.rows ? go(grouped_weight_tiles<kWeightsBy>, tiles, kThreads)
-                                : go(grouped_weight_tiles<kWeights>, tiles, kThreads);
+    const WeightPlan p = weight_plan(g.E, g.P, g.N, g.K);
+    g.split = p.parts;
+    const int64_t tiles = p.tiles * p.parts;
+    const hipError_t e =
+        p.small ? (g.rows ? go(grouped_weight_small<kWeightsBy>, tiles, 256)
+                          : go(grouped_weight_small<kWeights>, tiles, 256))
+                : (g.rows ? go(grouped_weight_tiles<kWeightsBy>, tiles, kThreads)
+                          : go(grouped_weight_tiles<kWeights>, tiles, kThreads));
     if (e != hipSuccess || g.split == 1) return e;
     const int64_t n = static_cast<int64_t>(g.E) * g.N * g.K;
     return launch(join_parts, dim3(static_cast<uint32_t>((n / 4 + 255) / 256)), dim3(256), 0, stream,

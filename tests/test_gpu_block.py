@@ -70,11 +70,16 @@ COUNTS = {
     "heights": [257, 288, 289, 320, 321, 512, 513, 576, 640, 641, 768, 900, 960, 961, 1, 33, 65,
                 129, 255, 256],
 }
+COUNTS["eight"] = [0, 1, 63, 64, 65, 200, 300, 107]
+COUNTS["parts"] = [4100]
 COUNTS["heights_of_200"] = [n for h in COUNTS["heights"] for n in (h, *[0] * 9)]
-SIZES = [(8, 8), (64, 64), (72, 200), (264, 136), (512, 320), (1544, 72), (72, 1544)]  # N, K
+SIZES = [(8, 8), (64, 64), (72, 200), (264, 136), (512, 320), (1544, 72), (72, 1544),
+         (1416, 1552), (1352, 1552), (2320, 2456)]  # N, K
 # enough tiles for the large ones: forward, input gradient
 HEIGHTS = [("heights", 5), ("heights_of_200", 3)]
 HEIGHTS_DX = [("heights", 6), ("heights_of_200", 2)]
+# large tiles of a weight gradient: whole, short, in two parts of the rows
+LARGE_DW = [("heights", 3), ("eight", 7), ("eight", 8), ("parts", 9)]
 MM = [("one", 0), ("one", 4), ("empty_ends", 2), ("edges", 1), ("edges", 3), ("edges", 4),
       ("long", 2), ("long", 4), ("many", 0), ("many", 2), ("last_of_1024", 2), ("none", 1)]
 
@@ -134,7 +139,8 @@ def run_dw(c, out, dw=None):
 
 @pytest.mark.parametrize("out", [BF16, F32])
 @pytest.mark.parametrize("gather,tail", [(False, 0), (True, 5)])
-@pytest.mark.parametrize("counts,size", [m for m in MM + [("heights", 3)] if m[0] != "last_of_1024"])
+@pytest.mark.parametrize("counts,size",
+                         [m for m in MM + LARGE_DW if m[0] != "last_of_1024"])
 def test_grouped_mm_dw(gpu_lib, counts, size, gather, tail, out):
     say(f"grouped_mm_dw {counts} {SIZES[size]} gather={gather} tail={tail} {out}")
     c = mm_case(counts, size, gather, tail, 200 + 11 * size + gather)
