@@ -21,7 +21,7 @@
 //
 // What bounds it (measured): with few rows a group, the weights' bytes (8 rows
 // over 8 of 256 experts, 403 MB: 73 us, 5.5 TB/s; the skewed 2048-token prompt,
-// 13.0 GB: 2.44 ms, 5.3 TB/s).  With many, LDS: a 32-deep stage of a 256 x 256
+// 13.0 GB: 2.41 ms, 5.4 TB/s).  With many, LDS: a 32-deep stage of a 256 x 256
 // tile takes 1024 cycles of the matrix cores and as many of LDS (96 KB of
 // fragment reads, 32 KB of fetches at 128 bytes a cycle), one half's reads
 // against the other's products; 8192 rows over one 4096 x 4096 matrix run at
@@ -630,8 +630,9 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
 // or weights share an L2.  Long runs share more, short ones balance groups of
 // unequal size: 16 where the products bound the call (64 groups of 512 rows,
 // 2048 x 2048: 322 us against 336 with 4), 4 elsewhere (the skewed prompt of
-// 256 groups over 4096 x 6144: 2437 us against 2529; weight gradients of
-// skewed groups 258 against 328).
+// 256 groups over 4096 x 6144: 2437 us against 2529; weight gradients within 8%
+// either way: 64 even groups of 2048 x 1024 260 us against 236, skewed 271 and
+// 268, 256 skewed ones 335 and 351).
 constexpr int kXcds = 8, kLongRun = 16, kShortRun = 4;
 __device__ __forceinline__ int64_t my_tile(int run) {
   const int xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
