@@ -49,6 +49,7 @@
 
 #include "common.h"
 #include "launch.h"
+#include "lds_dma.h"
 
 #pragma clang fp contract(off)
 
@@ -759,8 +760,6 @@ __device__ __forceinline__ bf16x8_t minus136_x3() {
 
 constexpr int kSt2A = kBigM * 128;                      // A, 16 KB
 
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
 // Byte offset of A[row][8 * seg ..] in a stage.
 __device__ __forceinline__ int a2_off(int row, int seg) {
   return row * 128 + ((seg ^ ((row >> 1) & 7)) << 4);
@@ -785,26 +784,6 @@ struct Big2Src {
 // DMA instructions per group and wavefront.
 template <class C, bool MX>
 constexpr int big2_dmas() { return 4 + C::kRuns + 1 + (MX ? 0 : 1); }
-
-// LDS byte address of a pointer into a __shared__ array.
-__device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8*)p));
-}
-
-// One LDS DMA instruction: every active lane's 16 (or 4) bytes at g go to LDS
-// at m0 + 16 (or 4) * lane.  Written as asm rather than the builtin: the
-// compiler's own wait bookkeeping cannot tell the three stages apart and
-// would wait for every fetch in flight before each read of a stage; these
-// fetches are waited for explicitly (wait_vm_lgkm0) instead.  The statement
-// has no register outputs; the address register is read when it issues.
-__device__ __forceinline__ void dma16(const uint8_t* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds)
-               : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(const uint8_t* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds)
-               : "memory", "m0");
-}
 
 template <class C, bool MX>
 __device__ __forceinline__ void big2_issue(const Big2Src& src, int grp, uint8_t* st, int wv,

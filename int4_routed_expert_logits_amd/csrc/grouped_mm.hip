@@ -30,6 +30,7 @@
 
 #include "common.h"
 #include "launch.h"
+#include "lds_dma.h"
 
 namespace moe {
 
@@ -41,7 +42,6 @@ typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 // read by scalar loads: a vector load's wait would drain the fetches into LDS
 typedef const __attribute__((address_space(4))) int32_t const_i32;
@@ -55,24 +55,6 @@ __device__ const uint4 g_zero[8] = {};
 // kCodesF32: the codes multiplied as bf16, for float32 results.
 // kWeightsBy: kWeights with x gathered through rows.
 enum Kind { kRows, kInput, kWeights, kWeightsBy, kCodes, kCodesF32 };
-
-// LDS byte address of a pointer into a __shared__ array.
-__device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8*)p));
-}
-
-// One LDS DMA instruction: every lane's 16 (or 4) bytes at g go to LDS at
-// m0 + 16 (or 4) * lane.  Asm, as the compiler would wait for all of them
-// before each LDS read; the loop waits for a stage's fetches itself.  No
-// register outputs.
-__device__ __forceinline__ void dma16(const uint8_t* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds)
-               : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(const uint8_t* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds)
-               : "memory", "m0");
-}
 
 // This wavefront's fetches but the newest N done and its LDS reads back, then
 // every wavefront of the workgroup here.
