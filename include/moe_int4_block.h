@@ -110,12 +110,8 @@ moe_status moe_blockscale_quantize(int32_t n_mats, int32_t R, int32_t K, const v
  *  N a multiple of 8 and K of 16, 16..65536
  *  xq [x_rows][K], xs [x_rows][ceil(K/128)], wq [E][N][K],
  *  ws [E][ceil(N/128)][ceil(K/128)]; rows as in moe_grouped_mm
- *  y  out [P][N].  f32: products are exact and summed in float32 (the codes are
- *     multiplied as bf16, which holds every e4m3 value).  bf16: a block's
- *     products are summed by the 8-bit matrix instructions, at twice that rate;
- *     they carry about 16 bits of a block's sum (1.4e-5 of the result rms
- *     measured), which the rounding to bf16 covers a hundred times; the blocks'
- *     sums are added in float32. */
+ *  y  out [P][N].  The codes are multiplied as bf16, which holds every e4m3
+ *     value: products are exact, and summed in float32 for either type of y. */
 moe_status moe_blockscale_mm(int32_t E, int32_t P, int32_t N, int32_t K, const uint8_t* xq,
                              const float* xs, int32_t x_rows, const int32_t* rows,
                              int32_t rows_div, const uint8_t* wq, const float* ws,

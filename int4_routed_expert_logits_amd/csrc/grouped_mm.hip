@@ -41,7 +41,6 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 // read by scalar loads: a vector load's wait would drain the fetches into LDS
 typedef const __attribute__((address_space(4))) int32_t const_i32;
@@ -52,9 +51,8 @@ constexpr int kBlock = 128;       // columns (and weight rows) per scale
 // What a fetch past an operand's end reads.
 __device__ const uint4 g_zero[8] = {};
 
-// kCodesF32: the codes multiplied as bf16, for float32 results.
 // kWeightsBy: kWeights with x gathered through rows.
-enum Kind { kRows, kInput, kWeights, kWeightsBy, kCodes, kCodesF32 };
+enum Kind { kRows, kInput, kWeights, kWeightsBy, kCodes };
 
 // This wavefront's fetches but the newest N done and its LDS reads back, then
 // every wavefront of the workgroup here.
@@ -97,24 +95,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // The product of two fragments of 16 rows x 128 codes (two 16-byte chunks a
-// lane, in the same places of both): by the 8-bit matrix instruction, or exactly
-// as bf16.
-template <bool EXACT>
+// lane, in the same places of both), as bf16: exact products, float32 sums.
+// The 8-bit matrix instructions have twice the rate, but align the products of
+// neighbouring codes to the largest before they add them: where a block's large
+// products cancel, what is left came out 5% off (448 * 448 - 448 * 448 beside
+// products of integers up to 15), more than a bf16 result's own rounding.
 __device__ __forceinline__ f32x4_t codes_product(const u32x4_t (&f)[2], const u32x4_t (&r)[2]) {
   f32x4_t p{0.0f, 0.0f, 0.0f, 0.0f};
-  if constexpr (EXACT) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int v = 0; v < 4; v += 2)
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(f[h][v], f[h][v + 1]),
-                                                    codes_to_bf16(r[h][v], r[h][v + 1]), p, 0, 0, 0);
-  } else {
-    p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-        __builtin_bit_cast(i32x8_t, __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7)),
-        __builtin_bit_cast(i32x8_t, __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3, 4, 5, 6, 7)), p,
-        0, 0, 0, 0, 0, 0);
-  }
+    for (int v = 0; v < 4; v += 2)
+      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(f[h][v], f[h][v + 1]),
+                                                  codes_to_bf16(r[h][v], r[h][v + 1]), p, 0, 0, 0);
   return p;
 }
 
@@ -223,7 +216,7 @@ struct Cfg {
   static constexpr bool DW = KIND == kWeights || KIND == kWeightsBy;
   static constexpr bool RT = DW;                    // R contiguous along m
   static constexpr bool FT = DW || KIND == kInput;  // F contiguous along n
-  static constexpr bool F8 = KIND == kCodes || KIND == kCodesF32;
+  static constexpr bool F8 = KIND == kCodes;
   static constexpr int RBytes = BM * SB, FBytes = BN * SB;
   static constexpr int SBytes = F8 ? Threads * 4 : 0;  // a stage's row scales
   static constexpr int Stage = RBytes + FBytes + SBytes;
@@ -475,15 +468,11 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
         }
 #pragma unroll
         for (int j = 0; j < C::FF; ++j) {
-          if (i < C::RF) p[cur][j] = codes_product<C::K == kCodesF32>(fa[j], rb[cur]);
+          if (i < C::RF) p[cur][j] = codes_product(fa[j], rb[cur]);
           if (i > 0) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               acc[i - 1][j][q] = fmaf(sc[i - 1], p[old][j][q], acc[i - 1][j][q]);
-          }
-          if (C::K == kCodes && i > 0 && i < C::RF) {  // in this order: one product, one scaling
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -640,8 +629,10 @@ __device__ __forceinline__ Place place(const Group& gr, int col, int nt) {
   return gr.n ? place(gr.t * nt + col, gr.n, nt) : Place{gr.t, col};
 }
 
-// Row tiles are 256 high (codes widened to bf16: 128, as both the codes and
-// their bf16 values sit in registers); a group's last one takes the smallest
+// Row tiles are 256 high (codes: 128, as both the codes and their bf16 values
+// sit in registers; 256 x 128 tiles, two after the other, took 1671 us for the
+// skewed prompt and 364 for 64 skewed groups over 2048 x 2048, where these take
+// 1612 and 331); a group's last one takes the smallest
 // height that holds its rows.  Where bf16 rows left over are at most 64 for
 // each full tile, as many of those as it takes are 320 high instead (160
 // accumulators a lane, 247 registers): a tile of few rows would read all of the
@@ -653,9 +644,7 @@ constexpr int kBN = 256, kThreads = 512, kCus = 256;
 template <int KIND>
 using T128 = Cfg<KIND, 2, 4, 4, 4, 3>;
 template <int KIND>
-using Tall = std::conditional_t<
-    (KIND <= kWeightsBy), Cfg<KIND, 2, 4, 8, 4, 4, 64, true>,
-    std::conditional_t<KIND == kCodes, Cfg<KIND, 2, 4, 8, 4, 2>, T128<KIND>>>;
+using Tall = std::conditional_t<KIND == kCodes, T128<KIND>, Cfg<KIND, 2, 4, 8, 4, 4, 64, true>>;
 template <int KIND>
 using High = Cfg<KIND, 2, 4, 10, 4, 4, 64, true>;
 template <int KIND>
@@ -860,7 +849,7 @@ int64_t most_row_tiles(const GroupedMm& g, int bm) {
 // the loads need no barrier, and bf16's 64 registers let a CU hold 32
 // wavefronts (eight loads at once and half as many wavefronts: 82 us against
 // 74 for one token; non-temporal loads: 90).  e4m3 codes are widened to bf16
-// (exact) whatever y's type is; two fragments of columns share the widening of
+// (exact); two fragments of columns share the widening of
 // x (8 tokens over 256 experts of 4096 x 6144: 258 us, 5.6 TB/s; one: 333).
 // ---------------------------------------------------------------------------
 
@@ -1030,17 +1019,15 @@ hipError_t launch_grouped_mm(const GroupedMm& args, GroupedKind kind, hipStream_
                   g);
   }
   if (kind != kGroupedInput && few_rows(g)) {
-    const int cols = kind == kGroupedRows ? Skinny<kRows>::kCols : Skinny<kCodesF32>::kCols;
+    const int cols = kind == kGroupedRows ? Skinny<kRows>::kCols : Skinny<kCodes>::kCols;
     const int nb = (g.N + cols - 1) / cols;
     const dim3 grid(static_cast<uint32_t>(nb * (g.E < g.P ? g.E : g.P))), block(kSkinnyThreads);
     return kind == kGroupedRows
                ? launch(grouped_skinny<kRows>, grid, block, 0, stream, g, nb)
-               : launch(grouped_skinny<kCodesF32>, grid, block, 0, stream, g, nb);
+               : launch(grouped_skinny<kCodes>, grid, block, 0, stream, g, nb);
   }
   const int cols = kind == kGroupedInput ? g.K : g.N;
-  const int bm =
-      kind == kGroupedCodes && g.out_f32 ? Tall<kCodesF32>::BM : Tall<kRows>::BM;
-  static_assert(Tall<kCodes>::BM == Tall<kRows>::BM, "tile height");
+  const int bm = kind == kGroupedCodes ? Tall<kCodes>::BM : Tall<kRows>::BM;
   const int64_t tiles = most_row_tiles(g, bm) * ((cols + kBN - 1) / kBN);
   if (tiles < kSmallTiles) {
     using S = Small<kRows>;
@@ -1048,17 +1035,13 @@ hipError_t launch_grouped_mm(const GroupedMm& args, GroupedKind kind, hipStream_
     switch (kind) {
       case kGroupedRows: return go(grouped_small<kRows>, small, S::Threads);
       case kGroupedInput: return go(grouped_small<kInput>, small, S::Threads);
-      default:
-        return g.out_f32 ? go(grouped_small<kCodesF32>, small, S::Threads)
-                         : go(grouped_small<kCodes>, small, S::Threads);
+      default: return go(grouped_small<kCodes>, small, S::Threads);
     }
   }
   switch (kind) {
     case kGroupedRows: return go(grouped_tiles<kRows>, tiles, kThreads);
     case kGroupedInput: return go(grouped_tiles<kInput>, tiles, kThreads);
-    default:
-      return g.out_f32 ? go(grouped_tiles<kCodesF32>, tiles, kThreads)
-                       : go(grouped_tiles<kCodes>, tiles, kThreads);
+    default: return go(grouped_tiles<kCodes>, tiles, kThreads);
   }
 }
 
