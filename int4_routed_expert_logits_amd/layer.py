@@ -187,14 +187,32 @@ def _check_float(fn: str, x, experts: FloatExperts, buf: FloatLayerBuffers):
     if (experts.scales is None) != (buf.codes is None):
         raise ValueError(f"{fn}: 8-bit experts take buffers allocated with codes=True, bf16 ones "
                          "without")
+    _check_tensor(fn, "x", x, torch.bfloat16, x.shape, buf.gu.device)
+
+
+def _check_tensor(fn: str, name: str, t, dtype, shape, device):
+    """What moe_route_union, which takes addresses, cannot see of a tensor."""
+    if t is None:
+        raise ValueError(f"{fn}: {name} is missing")
+    if t.dtype != dtype:
+        raise TypeError(f"{fn}: {name} is {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, the buffers on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not contiguous")
 
 
 def run_layer_float(x, w_router, bias, experts: FloatExperts, buf: FloatLayerBuffers, stream=None):
-    """The layer for x [T, d] bf16 on float or 8-bit experts: route and union,
-    gate and up products over the gathered tokens, SwiGLU, down products,
-    combine."""
-    _check_float("run_layer_float", x, experts, buf)
-    sh, b, k = buf.shape, buf, buf.shape.top_k
+    """The layer for x [T, d] bf16 on float or 8-bit experts: route and union
+    (w_router [E, d] and bias [E] or None, float32), gate and up products over
+    the gathered tokens, SwiGLU, down products, combine."""
+    fn, sh, b, k = "run_layer_float", buf.shape, buf, buf.shape.top_k
+    _check_float(fn, x, experts, buf)
+    _check_tensor(fn, "w_router", w_router, torch.float32, (sh.n_experts, sh.d), b.gu.device)
+    if bias is not None:
+        _check_tensor(fn, "bias", bias, torch.float32, (sh.n_experts,), b.gu.device)
     B.moe_route_union(sh, x, w_router, bias, b.topk_idx, b.topk_w, b.counts, b.offsets, b.perm,
                       b.inv_perm, b.active, b.n_active, b.workspace, stream)
     if experts.scales is None:

@@ -1,0 +1,77 @@
+"""What layer.py's calls on float and 8-bit experts see to before anything is
+enqueued (no GPU needed: no call here gets as far as the library)."""
+import pytest
+import torch
+
+import int4_routed_expert_logits_amd as moe
+from int4_routed_expert_logits_amd import _binding as B
+from int4_routed_expert_logits_amd import layer as L
+
+BF16 = torch.bfloat16
+E, D, F, T = 4, 128, 64, 3
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    """Any call of the library's binding ends the test."""
+    def enqueued(*a, **k):
+        raise AssertionError("the library was called")
+    for name in B.EXPORTS:
+        if callable(getattr(B, name, None)) and not name.endswith("_bytes"):
+            monkeypatch.setattr(B, name, enqueued)
+
+
+def bf(*shape, device="cpu"):
+    return torch.zeros(shape, dtype=BF16, device=device)
+
+
+def layer(codes=False):
+    sh = moe.Shape(D, F, E, 2, 64, 0)
+    buf = L.FloatLayerBuffers.allocate(sh, T, codes=codes, device="cpu")
+    if codes:
+        q = lambda *s: torch.zeros(s, dtype=torch.float8_e4m3fn)  # noqa: E731
+        return L.FloatExperts(q(E, 2 * F, D), q(E, D, F),
+                              scales=(torch.zeros(E, 1, 1), torch.zeros(E, 1, 1))), buf
+    return L.FloatExperts(bf(E, 2 * F, D), bf(E, D, F)), buf
+
+
+X_BAD = [
+    ("float32", lambda: bf(T, D).float(), TypeError, "x is torch.float32"),
+    ("expanded", lambda: bf(D).expand(T, D), ValueError, "x is not contiguous"),
+    ("strided", lambda: bf(T, 2 * D)[:, :D], ValueError, "x is not contiguous"),
+    ("transposed", lambda: bf(D, T).t(), ValueError, "x is not contiguous"),
+    ("elsewhere", lambda: bf(T, D, device="meta"), ValueError, "x is on meta"),
+]
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("what,x,error,match", X_BAD, ids=[b[0] for b in X_BAD])
+def test_layer_refuses_an_x_it_would_read_past(no_library, what, x, error, match, codes):
+    ex, buf = layer(codes)
+    with pytest.raises(error, match=match):
+        L.run_layer_float(x(), torch.zeros(E, D), None, ex, buf)
+    if not codes:
+        with pytest.raises(error, match=match):
+            L.run_layer_float_grad(bf(T, D), x(), ex, buf, L.FloatLayerGrads.allocate(buf, ex))
+
+
+ROUTER_BAD = [
+    ("few experts", lambda: torch.zeros(E - 1, D), None, ValueError, "w_router has shape"),
+    ("few columns", lambda: torch.zeros(E, D // 2), None, ValueError, "w_router has shape"),
+    ("bf16", lambda: bf(E, D), None, TypeError, "w_router is torch.bfloat16"),
+    ("transposed", lambda: torch.zeros(D, E).t(), None, ValueError, "w_router is not contiguous"),
+    ("short bias", lambda: torch.zeros(E, D), lambda: torch.zeros(E - 1), ValueError, "bias has shape"),
+    ("float64 bias", lambda: torch.zeros(E, D), lambda: torch.zeros(E).double(), TypeError,
+     "bias is torch.float64"),
+    ("strided bias", lambda: torch.zeros(E, D), lambda: torch.zeros(2 * E)[::2], ValueError,
+     "bias is not contiguous"),
+    ("no router", lambda: None, None, ValueError, "w_router is missing"),
+]
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("what,wr,bias,error,match", ROUTER_BAD, ids=[b[0] for b in ROUTER_BAD])
+def test_layer_refuses_a_router_it_would_read_past(no_library, what, wr, bias, error, match, codes):
+    ex, buf = layer(codes)
+    with pytest.raises(error, match=match):
+        L.run_layer_float(bf(T, D), wr(), bias and bias(), ex, buf)
