@@ -109,7 +109,11 @@ class FloatExperts:
 
     @classmethod
     def quantize(cls, e: "FloatExperts", stream=None) -> "FloatExperts":
-        """e's bf16 weights as codes and scales (moe_blockscale_quantize)."""
+        """e's bf16 weights as codes and scales (moe_blockscale_quantize), ready
+        on `stream`.  Their memory is the current stream's: another one waits for
+        what is queued there first, and holds on to all it touches."""
+        side = _torch_stream(stream, e.gate_up.device)
+
         def q(w):
             if w is None:
                 return None, None
@@ -117,10 +121,23 @@ class FloatExperts:
             codes = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
             scales = torch.empty((n, -(-r // 128), -(-k // 128)), device=w.device)
             B.moe_blockscale_quantize(w, 128, codes, scales, stream)
+            if side is not None:
+                for t in (w, codes, scales):
+                    t.record_stream(side)
             return codes, scales
+
+        if side is not None:
+            side.wait_stream(torch.cuda.current_stream(e.gate_up.device))
         (gu, gus), (dn, dns) = q(e.gate_up), q(e.down)
         (sgu, sgus), (sdn, sdns) = q(e.shared_gate_up), q(e.shared_down)
         return cls(gu, dn, sgu, sdn, (gus, dns), None if sgu is None else (sgus, sdns))
+
+
+def _torch_stream(stream, device):
+    """`stream` (a torch stream, a raw handle or None) as torch's own; None for None."""
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
 
 
 @dataclasses.dataclass

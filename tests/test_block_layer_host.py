@@ -75,3 +75,49 @@ def test_layer_refuses_a_router_it_would_read_past(no_library, what, wr, bias, e
     ex, buf = layer(codes)
     with pytest.raises(error, match=match):
         L.run_layer_float(bf(T, D), wr(), bias and bias(), ex, buf)
+
+
+# ----------------------------------------------------------------------------
+# streams, by what is asked of them
+# ----------------------------------------------------------------------------
+
+class Stream:
+    """Records what is asked of it."""
+    cuda_stream = 77
+
+    def __init__(self, log, name):
+        self.log, self.name = log, name
+
+    def wait_stream(self, other):
+        self.log.append(("wait", self.name, other.name))
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """(log, a side stream): the log of waits, calls and recorded tensors."""
+    log = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream(log, "current"))
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, s: log.append(("record", s.name, t.data_ptr())))
+    return log, Stream(log, "side")
+
+
+def test_quantize_on_a_stream_waits_and_keeps_its_memory(streams, monkeypatch):
+    """The memory it allocates belongs to the current stream: the side stream
+    waits for the work queued there before it writes, and no tensor that it
+    touches is handed out again before it is done."""
+    log, side = streams
+    monkeypatch.setattr(B, "moe_blockscale_quantize",
+                        lambda w, rows, codes, scales, stream: log.append(
+                            ("write", w.data_ptr(), codes.data_ptr(), scales.data_ptr(), stream)))
+    ex = L.FloatExperts(bf(E, 2 * F, D), bf(E, D, F), bf(1, 2 * F, D), bf(1, D, F))
+    q = L.FloatExperts.quantize(ex, side)
+    assert log[0] == ("wait", "side", "current")
+    writes = [e for e in log if e[0] == "write"]
+    assert len(writes) == 4 and all(e[-1] is side for e in writes)
+    recorded = {e[2] for e in log if e[0] == "record" and e[1] == "side"}
+    assert recorded == {p for e in writes for p in e[1:-1]}
+    assert q.gate_up.shape == ex.gate_up.shape and q.shared_scales[1].shape == (1, 1, 1)
+    log.clear()
+    L.FloatExperts.quantize(ex)
+    assert [e[0] for e in log] == ["write"] * 4  # on the current stream: nothing to wait for
