@@ -12,6 +12,7 @@ given), and ``run_block`` any of them between its norms and residual.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Optional
 
@@ -340,7 +341,7 @@ def run_block(res, norms: BlockNorms, layer, normed, res_out, next_norms=None, n
     """res_out = res + scale * gate * norm(layer(norm(res))) for the residual
     stream res [T, d]; layer: a function of the normed tokens [T, d] (normed, a
     buffer of the type it takes), such as run_layer or run_layer_float with the
-    rest bound.  With next_norms, next_normed gets the next block's pre norm in
+    rest bound; it is called with `stream` as the current one.  With next_norms, next_normed gets the next block's pre norm in
     the same pass; hand it to the next block as `layer`'s input (its first norm
     is then done: call layer on it and moe_block_norm).  The post norm and the
     next pre norm then share their eps; without a post norm the next one's holds."""
@@ -351,7 +352,9 @@ def run_block(res, norms: BlockNorms, layer, normed, res_out, next_norms=None, n
                              f"{next_norms.eps} are not one pass")
         eps = next_norms.eps
     B.moe_block_norm(None, res, None, normed, w_pre=norms.w_pre, eps=norms.eps, stream=stream)
-    out = layer(normed)
+    side = _torch_stream(stream, res.device)
+    with contextlib.nullcontext() if side is None else torch.cuda.stream(side):
+        out = layer(normed)
     B.moe_block_norm(out, res, res_out, next_normed, norms.w_post,
                      None if next_norms is None else next_norms.w_pre, norms.gate, norms.scale,
                      eps, stream)

@@ -121,3 +121,31 @@ def test_quantize_on_a_stream_waits_and_keeps_its_memory(streams, monkeypatch):
     log.clear()
     L.FloatExperts.quantize(ex)
     assert [e[0] for e in log] == ["write"] * 4  # on the current stream: nothing to wait for
+
+
+def test_block_runs_its_layer_on_its_stream(streams, monkeypatch):
+    """A layer that names no stream reads `normed` behind the norm that writes it."""
+    log, side = streams
+    now = ["current"]
+
+    class On:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            now.append("current" if self.s is None else self.s.name)
+
+        def __exit__(self, *a):
+            now.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(B, "moe_block_norm", lambda *a, **k: log.append(
+        ("norm", (k.get("stream") or a[-1]).name)))
+
+    def inner(n):
+        log.append(("layer", now[-1]))
+        return n
+
+    t = bf(T, D)
+    L.run_block(t, L.BlockNorms(torch.ones(D)), inner, bf(T, D), bf(T, D), stream=side)
+    assert log == [("norm", "side"), ("layer", "side"), ("norm", "side")] and now == ["current"]

@@ -58,3 +58,30 @@ def test_quantize_may_be_followed_by_freeing_the_weights(gpu_lib):
     junk = [torch.full(shape, 3.0, dtype=BF16, device="cuda") for _ in range(4)]
     torch.cuda.current_stream().wait_stream(side)
     assert same_codes(got, want) and len(junk) == 4
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_block_on_a_side_stream(gpu_lib, handle):
+    """run_block's norms, and a layer that names no stream, in order on `stream`,
+    behind work that is queued there: the same as on the current one."""
+    sh, T = moe.Shape(320, 192, 8, 2, 64, 192), 40
+    g, d, f, E = gen(3), 320, 192, 8
+    ex = L.FloatExperts(rand(g, E, 2 * f, d, scale=0.05), rand(g, E, d, f, scale=0.07),
+                        rand(g, 1, 2 * f, d, scale=0.05), rand(g, 1, d, f, scale=0.07))
+    wr, res = rand(g, E, d, dt=torch.float32, scale=0.05), rand(g, T, d)
+    norms = L.BlockNorms(torch.rand(d, generator=g).cuda(), torch.rand(d, generator=g).cuda())
+
+    def block(stream):
+        buf = L.FloatLayerBuffers.allocate(sh, T)
+        normed, out = (torch.zeros((T, d), dtype=BF16, device="cuda") for _ in range(2))
+        torch.cuda.synchronize()
+        s = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(BUSY)
+        L.run_block(res, norms, lambda n: L.run_layer_float(n, wr, None, ex, buf), normed, out,
+                    stream=stream and (stream.cuda_stream if handle else stream))
+        torch.cuda.synchronize()
+        return out
+
+    want = block(None)
+    assert torch.equal(block(torch.cuda.Stream()), want) and (want != 0).any()
