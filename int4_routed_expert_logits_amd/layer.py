@@ -208,6 +208,16 @@ def _check_float(fn: str, x, experts: FloatExperts, buf: FloatLayerBuffers):
     _check_tensor(fn, "x", x, torch.bfloat16, x.shape, buf.gu.device)
 
 
+def _gpu_of(t):
+    """A context with t's GPU as the current one, for the calls that launch there
+    (moe_route_union, moe_combine; the others go by their tensors)."""
+    B._T or B._types()
+    dev = t.get_device()
+    if dev < 0 or dev == B._current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
 def _check_tensor(fn: str, name: str, t, dtype, shape, device):
     """What moe_route_union, which takes addresses, cannot see of a tensor."""
     if t is None:
@@ -231,8 +241,9 @@ def run_layer_float(x, w_router, bias, experts: FloatExperts, buf: FloatLayerBuf
     _check_tensor(fn, "w_router", w_router, torch.float32, (sh.n_experts, sh.d), b.gu.device)
     if bias is not None:
         _check_tensor(fn, "bias", bias, torch.float32, (sh.n_experts,), b.gu.device)
-    B.moe_route_union(sh, x, w_router, bias, b.topk_idx, b.topk_w, b.counts, b.offsets, b.perm,
-                      b.inv_perm, b.active, b.n_active, b.workspace, stream)
+    with _gpu_of(b.gu):
+        B.moe_route_union(sh, x, w_router, bias, b.topk_idx, b.topk_w, b.counts, b.offsets, b.perm,
+                          b.inv_perm, b.active, b.n_active, b.workspace, stream)
     if experts.scales is None:
         B.moe_grouped_mm(x, experts.gate_up, b.offsets, b.gu, b.perm, k, stream)
         B.moe_swiglu(b.gu, b.h, b.n_rows, stream)
@@ -255,7 +266,8 @@ def run_layer_float(x, w_router, bias, experts: FloatExperts, buf: FloatLayerBuf
             B.moe_swiglu_quantize(b.gu_shared, hq, hs, stream=stream)
             B.moe_blockscale_mm(hq, hs, experts.shared_down, dns, b.all_rows, b.y_shared,
                                 stream=stream)
-    B.moe_combine(sh, b.y, b.y_shared, b.inv_perm, b.topk_w, b.out, stream)
+    with _gpu_of(b.gu):
+        B.moe_combine(sh, b.y, b.y_shared, b.inv_perm, b.topk_w, b.out, stream)
     return b.out
 
 
@@ -321,7 +333,8 @@ def run_layer_float_grad(dout, x, experts: FloatExperts, buf: FloatLayerBuffers,
                             stream=stream)
         B.moe_grouped_mm_dx(g.dgu_shared, experts.shared_gate_up, b.all_rows, g.dx_shared, stream)
     # a token's gradient is the sum over its slots: the combine with weights of 1
-    B.moe_combine(sh, g.dx_slots, g.dx_shared, b.inv_perm, g.ones, g.dx, stream)
+    with _gpu_of(b.gu):
+        B.moe_combine(sh, g.dx_slots, g.dx_shared, b.inv_perm, g.ones, g.dx, stream)
     return g
 
 
@@ -341,10 +354,11 @@ def run_block(res, norms: BlockNorms, layer, normed, res_out, next_norms=None, n
     """res_out = res + scale * gate * norm(layer(norm(res))) for the residual
     stream res [T, d]; layer: a function of the normed tokens [T, d] (normed, a
     buffer of the type it takes), such as run_layer or run_layer_float with the
-    rest bound; it is called with `stream` as the current one.  With next_norms, next_normed gets the next block's pre norm in
-    the same pass; hand it to the next block as `layer`'s input (its first norm
-    is then done: call layer on it and moe_block_norm).  The post norm and the
-    next pre norm then share their eps; without a post norm the next one's holds."""
+    rest bound; it is called with `stream` as the current one.  With next_norms,
+    next_normed gets the next block's pre norm in the same pass; hand it to the
+    next block as `layer`'s input (its first norm is then done: call layer on it
+    and moe_block_norm).  The post norm and the next pre norm then share their
+    eps; without a post norm the next one's holds."""
     eps = norms.eps
     if next_norms is not None and next_norms.eps != eps:
         if norms.w_post is not None:

@@ -149,3 +149,41 @@ def test_block_runs_its_layer_on_its_stream(streams, monkeypatch):
     t = bf(T, D)
     L.run_block(t, L.BlockNorms(torch.ones(D)), inner, bf(T, D), bf(T, D), stream=side)
     assert log == [("norm", "side"), ("layer", "side"), ("norm", "side")] and now == ["current"]
+
+
+# ----------------------------------------------------------------------------
+# another GPU than the current one
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_layer_runs_on_its_buffers_gpu(monkeypatch, current):
+    """moe_route_union and moe_combine launch on the current GPU: the layer and
+    its gradient make their buffers' GPU current, and leave the other one so."""
+    at = [current]
+
+    class On:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            at.append(self.d)
+
+        def __exit__(self, *a):
+            at.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(B, "_current_device", lambda: at[-1])
+    monkeypatch.setattr(B, "_T", B._T or B._types())
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1)
+    calls = []
+    for name in B.EXPORTS:
+        if callable(getattr(B, name, None)) and not name.endswith("_bytes"):
+            monkeypatch.setattr(B, name, lambda *a, name=name, **k: calls.append((name, at[-1])))
+    for codes in (False, True):
+        ex, buf = layer(codes)
+        L.run_layer_float(bf(T, D), torch.zeros(E, D), None, ex, buf)
+        if not codes:
+            L.run_layer_float_grad(bf(T, D), bf(T, D), ex, buf, L.FloatLayerGrads.allocate(buf, ex))
+    by_address = [(n, d) for n, d in calls if n in ("moe_route_union", "moe_combine")]
+    assert len(by_address) == 5 and all(d == 1 for _, d in by_address), by_address
+    assert at == [current]
