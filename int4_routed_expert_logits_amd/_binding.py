@@ -450,11 +450,23 @@ def _take(fn: str, dev: int, name: str, t, dtypes, shape):
     raise ValueError(f"{fn}: {name} is not contiguous")
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
 def _dim(fn: str, name: str, t, n: int):
+    """t's shape, of n sizes that int32 holds (ctypes would wrap larger ones)."""
     shape = t.shape
     if len(shape) != n:
         raise ValueError(f"{fn}: {name} has {len(shape)} dimensions, not {n}")
+    if max(shape) > _INT32_MAX:
+        raise MoeError(fn, MOE_ERR_UNSUPPORTED)
     return shape
+
+
+def _int32(fn: str, v: int) -> int:
+    if not -_INT32_MAX <= v <= _INT32_MAX:
+        raise MoeError(fn, MOE_ERR_UNSUPPORTED)
+    return v
 
 
 def _workspace(fn: str, dev: int, t):
@@ -495,7 +507,8 @@ def moe_grouped_mm(x, w, offsets, y, rows=None, rows_div: int = 1, stream=None):
     E, N, K = _dim(fn, "w", w, 3)
     P, X = _dim(fn, "y", y, 2)[0], _dim(fn, "x", x, 2)[0]
     _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "x", x, bf16, (X, K)), X,
-         _rows_args(fn, dev, P, rows), rows_div, _take(fn, dev, "w", w, bf16, (E, N, K)),
+         _rows_args(fn, dev, P, rows), _int32(fn, rows_div),
+         _take(fn, dev, "w", w, bf16, (E, N, K)),
          _take(fn, dev, "offsets", offsets, i32, (E + 1,)),
          _take(fn, dev, "y", y, floats, (P, N)), _code(y.dtype))
 
@@ -513,6 +526,8 @@ def moe_grouped_mm_dx(dy, w, offsets, dx, stream=None):
 
 
 def moe_grouped_mm_dw_workspace_bytes(E: int, P: int, N: int, K: int) -> int:
+    if max(E, P, N, K) > _INT32_MAX or min(E, P, N, K) < 0:
+        return 0
     return load().moe_grouped_mm_dw_workspace_bytes(E, P, N, K)
 
 
@@ -526,7 +541,8 @@ def moe_grouped_mm_dw(dy, x, offsets, dw, workspace=None, rows=None, rows_div: i
     P, X = _dim(fn, "dy", dy, 2)[0], _dim(fn, "x", x, 2)[0]
     ws, nws = _workspace(fn, dev, workspace)
     _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "dy", dy, bf16, (P, N)),
-         _take(fn, dev, "x", x, bf16, (X, K)), X, _rows_args(fn, dev, P, rows), rows_div,
+         _take(fn, dev, "x", x, bf16, (X, K)), X,
+         _rows_args(fn, dev, P, rows), _int32(fn, rows_div),
          _take(fn, dev, "offsets", offsets, i32, (E + 1,)),
          _take(fn, dev, "dw", dw, floats, (E, N, K)), _code(dw.dtype), ws, nws)
 
@@ -539,10 +555,10 @@ def moe_blockscale_quantize(x, block_rows: int, codes, scales, stream=None):
     _, f32, floats, _, codes_t = _T or _types()
     if x.dim() not in (2, 3):
         raise ValueError(f"{fn}: x has {x.dim()} dimensions, not 2 or 3")
-    *lead, R, K = x.shape
+    *lead, R, K = _dim(fn, "x", x, x.dim())
     sr = R if block_rows == 1 else -(-R // 128)
     _run(fn, dev, stream, lead[0] if lead else 1, R, K, _take(fn, dev, "x", x, floats, x.shape),
-         _code(x.dtype), block_rows, _take(fn, dev, "codes", codes, codes_t, x.shape),
+         _code(x.dtype), _int32(fn, block_rows), _take(fn, dev, "codes", codes, codes_t, x.shape),
          _take(fn, dev, "scales", scales, f32, (*lead, sr, -(-K // 128))))
 
 
@@ -554,7 +570,8 @@ def moe_blockscale_mm(xq, xs, wq, ws, offsets, y, rows=None, rows_div: int = 1, 
     E, N, K = _dim(fn, "wq", wq, 3)
     P, X, kb = _dim(fn, "y", y, 2)[0], _dim(fn, "xq", xq, 2)[0], -(-K // 128)
     _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "xq", xq, codes_t, (X, K)),
-         _take(fn, dev, "xs", xs, f32, (X, kb)), X, _rows_args(fn, dev, P, rows), rows_div,
+         _take(fn, dev, "xs", xs, f32, (X, kb)), X,
+         _rows_args(fn, dev, P, rows), _int32(fn, rows_div),
          _take(fn, dev, "wq", wq, codes_t, (E, N, K)),
          _take(fn, dev, "ws", ws, f32, (E, -(-N // 128), kb)),
          _take(fn, dev, "offsets", offsets, i32, (E + 1,)),
@@ -651,6 +668,8 @@ def _code(dtype) -> int:
 
 
 def moe_block_norm_grad_workspace_bytes(T: int, d: int) -> int:
+    if max(T, d) > _INT32_MAX or min(T, d) < 0:
+        return 0
     return load().moe_block_norm_grad_workspace_bytes(T, d)
 
 
