@@ -311,14 +311,16 @@ __global__ __launch_bounds__(1024) void norm_grad_columns(BlockNorm g, int parts
     s2 += sh[1][w][lane];
   }
   const bool cast = g.gate && g.gate_rows == 1;
+  // no rows: zeros, also where the gate or w_post is not finite
+  const float scale = parts > 0 ? g.scale : 0.0f;
   float gate = 1.0f;
-  if (cast)
+  if (cast && parts > 0)
     gate = g.y_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(g.gate)[c])
                     : static_cast<const float*>(g.gate)[c];
-  if (g.dw_post) g.dw_post[c] = g.scale * gate * s1;
+  if (g.dw_post) g.dw_post[c] = scale * gate * s1;
   if (g.dw_pre) g.dw_pre[c] = s2;
   if (cast && g.dgate) {
-    const float v = g.scale * (g.w_post ? g.w_post[c] : 1.0f) * s1;
+    const float v = scale * (g.w_post && parts > 0 ? g.w_post[c] : 1.0f) * s1;
     if (g.y_bf16)
       static_cast<uint16_t*>(g.dgate)[c] = f32_to_bf16(v);
     else
