@@ -18,3 +18,32 @@ def test_norm_gradients_of_no_rows_are_zero_beside_nonfinite_weights(gpu_lib, dt
     dw, dg = [poison((d,), F32) for _ in range(2)], poison((1, d), dt)
     moe.moe_block_norm_grad(e, e, e, e, e.clone(), e.clone(), dw[0], dw[1], dg, w, w, gate)
     assert (dw[0] == 0).all() and (dw[1] == 0).all() and (dg == 0).all()
+
+
+def kernels_of(call):
+    """Names of the kernels that a call launches."""
+    call()
+    torch.cuda.synchronize()
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as p:
+        call()
+        torch.cuda.synchronize()
+    return [e.key for e in p.key_averages()]
+
+
+@pytest.mark.parametrize("y,res,pre,ahead", [
+    (BF16, BF16, None, True), (BF16, BF16, BF16, True), (None, BF16, BF16, True),
+    (BF16, None, BF16, True), (BF16, BF16, F32, False), (F32, F32, None, False),
+    (None, F32, BF16, False), (BF16, F32, None, False)])
+def test_norm_gradient_of_bf16_rows_fetches_ahead(gpu_lib, y, res, pre, ahead):
+    """The kernel that reads the next row early (its second argument) is for rows
+    of bf16, whatever type is given for a row that is not there."""
+    T, d = 8, 520
+    row = lambda dt: None if dt is None else torch.ones((T, d), dtype=dt, device="cuda")  # noqa: E731
+    w = torch.ones(d, device="cuda")
+    rdt = res or y
+    dy, dres = row(y), row(rdt)
+    names = kernels_of(lambda: moe.moe_block_norm_grad(
+        row(y), row(res), row(rdt), row(pre), dy, dres, None, None, None,
+        w if y and not res else None, w if pre else None))
+    [name] = [n for n in names if "norm_grad_rows" in n]
+    assert name.split("<")[1].split(",")[1].strip() == ("true" if ahead else "false"), name
