@@ -350,22 +350,23 @@ class BlockNorms:
 
 
 def run_block(res, norms: BlockNorms, layer, normed, res_out, next_norms=None, next_normed=None,
-              stream=None):
+              stream=None, normed_ready=False):
     """res_out = res + scale * gate * norm(layer(norm(res))) for the residual
     stream res [T, d]; layer: a function of the normed tokens [T, d] (normed, a
     buffer of the type it takes), such as run_layer or run_layer_float with the
     rest bound; it is called with `stream` as the current one.  With next_norms,
-    next_normed gets the next block's pre norm in the same pass; hand it to the
-    next block as `layer`'s input (its first norm is then done: call layer on it
-    and moe_block_norm).  The post norm and the next pre norm then share their
-    eps; without a post norm the next one's holds."""
+    next_normed gets the next block's pre norm in the same pass: hand it to that
+    block as its `normed`, with normed_ready, and its first norm is not done
+    again.  The post norm and the next pre norm share their eps; without a post
+    norm the next one's holds."""
     eps = norms.eps
     if next_norms is not None and next_norms.eps != eps:
         if norms.w_post is not None:
             raise ValueError(f"run_block: a post norm with eps {eps} and a next pre norm with "
                              f"{next_norms.eps} are not one pass")
         eps = next_norms.eps
-    B.moe_block_norm(None, res, None, normed, w_pre=norms.w_pre, eps=norms.eps, stream=stream)
+    if not normed_ready:
+        B.moe_block_norm(None, res, None, normed, w_pre=norms.w_pre, eps=norms.eps, stream=stream)
     side = _torch_stream(stream, res.device)
     with contextlib.nullcontext() if side is None else torch.cuda.stream(side):
         out = layer(normed)

@@ -187,3 +187,18 @@ def test_layer_runs_on_its_buffers_gpu(monkeypatch, current):
     by_address = [(n, d) for n, d in calls if n in ("moe_route_union", "moe_combine")]
     assert len(by_address) == 5 and all(d == 1 for _, d in by_address), by_address
     assert at == [current]
+
+
+def test_chained_blocks_do_each_norm_once(monkeypatch):
+    """Two blocks: the first's pre norm, its layer, one pass for its post norm with
+    the second's pre norm, the second's layer, its post norm."""
+    log = []
+    monkeypatch.setattr(B, "moe_block_norm", lambda y, res, out, normed, *a, **k: log.append(
+        ("norm", y is not None, normed is not None)))
+    t, n = bf(T, D), [bf(T, D), bf(T, D)]
+    norms = [L.BlockNorms(torch.ones(D), torch.ones(D)) for _ in range(2)]
+    inner = lambda v: (log.append(("layer", [v is x for x in n].index(True))), v)[1]  # noqa: E731
+    L.run_block(t, norms[0], inner, n[0], t, norms[1], n[1])
+    L.run_block(t, norms[1], inner, n[1], t, normed_ready=True)
+    assert log == [("norm", False, True), ("layer", 0), ("norm", True, True), ("layer", 1),
+                   ("norm", True, False)]

@@ -1,10 +1,11 @@
-"""Values and sizes at the edge of the calls in include/moe_int4_block.h: no rows
-beside weights that are not finite."""
+"""The norms of include/moe_int4_block.h at their edges: no rows beside weights that
+are not finite, operands that are absent, blocks in a chain."""
 import pytest
 import torch
 
 import int4_routed_expert_logits_amd as moe
-from test_gpu_block import BF16, F32, poison
+from int4_routed_expert_logits_amd import layer as L
+from test_gpu_block import BF16, F32, gen, poison, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,19 @@ def test_norm_gradient_of_bf16_rows_fetches_ahead(gpu_lib, y, res, pre, ahead):
         w if y and not res else None, w if pre else None))
     [name] = [n for n in names if "norm_grad_rows" in n]
     assert name.split("<")[1].split(",")[1].strip() == ("true" if ahead else "false"), name
+
+
+def test_chained_blocks_are_the_blocks_one_by_one(gpu_lib):
+    """The second block on the first's next_normed, against its norm done alone: the
+    same bits where the residual is float32, so that nothing is rounded in between."""
+    T, d, eps = 5, 136, 1e-5
+    g = gen(5)
+    res, w = rand(g, T, d, dt=F32), [1 + rand(g, d, dt=F32, scale=0.1) for _ in range(4)]
+    norms = [L.BlockNorms(w[0], w[1], eps=eps), L.BlockNorms(w[2], w[3], eps=eps)]
+    layer = lambda n: n * 0.5  # noqa: E731
+    new = lambda: torch.empty((T, d), device="cuda")  # noqa: E731
+    n, r = [new(), new()], [new(), new(), new()]
+    L.run_block(res, norms[0], layer, n[0], r[0], norms[1], n[1])
+    L.run_block(r[0], norms[1], layer, n[1], r[1], normed_ready=True)
+    L.run_block(r[0], norms[1], layer, new(), r[2])
+    assert torch.equal(r[1], r[2])
