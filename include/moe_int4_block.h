@@ -22,9 +22,10 @@
  * enqueued on `stream`, nothing allocated, no state, arguments checked before
  * anything is enqueued.  Results do not depend on the order in which
  * workgroups run (no atomics), so a call repeated on the same inputs gives the
- * same bits.  Tensors are row-major without gaps; bf16 and f32 arrays are
- * 16-byte aligned, e4m3 codes and the norms' weights too, int32 arrays, scales
- * and the weights' gradients of the norms 4-byte.
+ * same bits (a product's last bits may differ between calls of other sizes, which
+ * other kernels add up in another order).  Tensors are row-major without gaps;
+ * bf16 and f32 arrays are 16-byte aligned, e4m3 codes and the norms' weights too,
+ * int32 arrays, scales and the weights' gradients of the norms 4-byte.
  *
  * Rows grouped by expert: position p belongs to expert e when
  *   offsets[e] <= p < offsets[e + 1],

@@ -5,9 +5,10 @@
 // and its gradient.  All of it is bound by memory: a row is read once into
 // registers (8 columns per thread, d <= 8192), both statistics come from
 // them in float32, and n is taken from r before r is rounded to its own type.
-// One row of 6144 takes 3.5 us (launch and two meetings of the workgroup); the
-// gradient of 2048 rows (151 MB) 38 us for the rows, 4.0 TB/s, and 5 for the
-// columns' sums.
+// One row of 6144 takes 4.2 us (launch and two meetings of the workgroup), 2048
+// of bf16 (101 MB) 29 us, of float32 46; the gradient of 2048 rows of bf16 (151
+// MB) 38 us for the rows, 4.0 TB/s, and 5 for the columns' sums, of float32 75 in
+// all.
 #include "common.h"
 #include "launch.h"
 
@@ -193,7 +194,11 @@ __device__ __forceinline__ void values(const Raw& r, bool bf16, float (&v)[kV]) 
 // workgroup.  With all-bf16 rows the next row is fetched before this row's
 // sums (a row of float32 would not fit the registers twice).
 // THREADS, the most of a launch, sets the registers a thread may hold (256, 168,
-// 128): the widest rows have the fewest.  PER_TOKEN: a gate of T rows.
+// 128): the widest rows have the fewest, and past 6144 columns some of a row goes
+// through scratch (bf16 with a gate per token 20 bytes a lane, other types 44, 128
+// with a gate per token; bf16 rows of 8192 none): 2048 x 8192 takes 48-58 us of
+// bf16 (201 MB), 102 with a float32 residual (302 MB), 120 of float32 (403 MB).
+// PER_TOKEN: a gate of T rows.
 template <int THREADS, bool ALL_BF16, bool PER_TOKEN>
 __global__ __launch_bounds__(THREADS) void norm_grad_rows(BlockNorm g) {
   __shared__ float sh[2][6][kMaxWaves];  // by the row's parity

@@ -20,12 +20,13 @@
 // a lane then holds four consecutive columns of one output row.
 //
 // What bounds it (measured): with few rows a group, the weights' bytes (8 rows
-// over 8 of 256 experts, 403 MB: 73 us, 5.5 TB/s; the skewed 2048-token prompt,
-// 13.0 GB: 2.41 ms, 5.4 TB/s).  With many, LDS: a 32-deep stage of a 256 x 256
+// over 8 of 256 experts, 403 MB: 75 us, 5.4 TB/s; the skewed 2048-token prompt,
+// 13.0 GB: 2.45 ms, 5.3 TB/s).  With many, LDS: a 32-deep stage of a 256 x 256
 // tile takes 1024 cycles of the matrix cores and as many of LDS (96 KB of
 // fragment reads, 32 KB of fetches at 128 bytes a cycle), one half's reads
 // against the other's products; 8192 rows over one 4096 x 4096 matrix run at
-// 1190 TFLOP/s in all, over 8192 x 8192 at 1310.
+// 1150-1190 TFLOP/s in all, over 8192 x 8192 at 1310.  Codes run their products
+// at the same rate with the widening beside them: 930 TFLOP/s (297 us) there.
 #include <type_traits>
 
 #include "common.h"
@@ -601,9 +602,10 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
 // or weights share an L2.  Long runs share more, short ones balance groups of
 // unequal size: 16 where the products bound the call (64 groups of 512 rows,
 // 2048 x 2048: 322 us against 336 with 4), 4 elsewhere (the skewed prompt of
-// 256 groups over 4096 x 6144: 2437 us against 2529; weight gradients within 8%
-// either way: 64 even groups of 2048 x 1024 260 us against 236, skewed 271 and
-// 268, 256 skewed ones 335 and 351).
+// 256 groups over 4096 x 6144: 2437 us against 2529; weight gradients, whose
+// groups are seldom even, with runs of 4 / 16: 64 skewed groups of 2048 x 1024
+// 268 / 286, gathered 378 / 427, of 2048 x 2048 494 / 510, gathered 677 / 745; 64
+// even ones of 2048 x 1024 235 / 223).
 constexpr int kXcds = 8, kLongRun = 16, kShortRun = 4;
 __device__ __forceinline__ int64_t my_tile(int run) {
   const int xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
@@ -632,13 +634,13 @@ __device__ __forceinline__ Place place(const Group& gr, int col, int nt) {
 // Row tiles are 256 high (codes: 128, as both the codes and their bf16 values
 // sit in registers; 256 x 128 tiles, two after the other, took 1671 us for the
 // skewed prompt and 364 for 64 skewed groups over 2048 x 2048, where these take
-// 1612 and 331); a group's last one takes the smallest
-// height that holds its rows.  Where bf16 rows left over are at most 64 for
-// each full tile, as many of those as it takes are 320 high instead (160
-// accumulators a lane, 247 registers): a tile of few rows would read all of the
-// weights once more (64 groups of about 512 rows over 2048 x 2048 341 us without,
-// 318 with; one of 4200 rows over 4096 x 4096 161 and 121; the skewed prompt
-// 2440 and 2410).  Codes have no registers left for it.  The short ones are bound by their fetches and
+// 1612 and 331); a group's last one takes the smallest height that holds its
+// rows.  Where bf16 rows left over are at most 64 for each full tile, as many of
+// those as it takes are 320 high instead (160 accumulators a lane, 247
+// registers): a tile of few rows would read all of the weights once more (64
+// groups of about 512 rows over 2048 x 2048 341 us without, 318 with; one of 4200
+// rows over 4096 x 4096 161 and 121; the skewed prompt 2440 and 2410).  Codes
+// have no registers left for it.  The short ones are bound by their fetches and
 // keep three or four stages in LDS.
 constexpr int kBN = 256, kThreads = 512, kCus = 256;
 template <int KIND>
@@ -791,7 +793,9 @@ struct WeightPlan {
 // rows, 1024 x 1024 27 / 38, 2048 x 2048 54 / 62; 16384 rows, 2560 x 2560 327 /
 // 242, 4096 x 3840 653 / 456; 8 groups of 1024 rows, 1024 x 1280 51 / 43, skewed
 // 55 / 79; 32 of 512, 512 x 768 35 / 27, skewed 47 / 84; 16 of 2048, skewed,
-// 2048 x 1024 231 / 181.
+// 2048 x 1024 231 / 181.  The terms are for ranking the two: what they leave out
+// (operands read several times, stores) is alike in both, and adds up to half as
+// much again (64 skewed groups of 2048 x 1024: 186 us here, 270 measured).
 WeightPlan weight_plan(int E, int P, int N, int K, bool small) {
   using T = Tall<kWeights>;
   using S = SmallDw<kWeights>;
@@ -850,14 +854,19 @@ int64_t most_row_tiles(const GroupedMm& g, int bm) {
 // wavefronts (eight loads at once and half as many wavefronts: 82 us against
 // 74 for one token; non-temporal loads: 90).  e4m3 codes are widened to bf16
 // (exact); two fragments of columns share the widening of
-// x (8 tokens over 256 experts of 4096 x 6144: 258 us, 5.6 TB/s; one: 333).
+// x (8 tokens over 256 experts of 4096 x 6144: 260-277 us, 5.2-5.5 TB/s; one: 333).
 // ---------------------------------------------------------------------------
 
-// Against the tiles, us per call (one N = 4096, K = 6144 bf16 expert; 64 of
-// N = K = 2048; 256 of 4096 x 6144, codes): 68 rows 50 / 60, 16 rows 15 / 45;
-// 256 rows 105 / 130; 512 rows 1013 / 1138, 2048 rows 1400 / 1318.  Past about
-// 3 rows a group (64 in one) a group's second pass over its weights costs more
-// than the tiles' staging.
+// Against the tiles, us per call, bf16 and codes.  One expert of N = 4096,
+// K = 6144: 1 row 17 / 46 and 18 / 46, 32 rows 28 / 48 and 33 / 46, 64 rows
+// 51 / 52 and 58 / 47.  64 of N = K = 2048: 32 rows 45 / 58 and 31 / 28, 240 rows
+// 108 / 143 and 58 / 59, skewed 93 / 117 and 54 / 53.  256 of 4096 x 6144: 8 rows
+// 77 / 76 and 46 / 50, 512 rows 1909 / 1865 and 1012 / 921, skewed 1400 / 1241 and
+// 732 / 628.  Drawn sizes (1 to 250 experts, N and K of 64 to 6144, 90 cases): up
+// to three times as fast, 10% slower at worst.  Each 16 rows of a group are a pass
+// over its weights: where the experts are large and rows crowd, that costs more
+// than the tiles' staging, and past about 3 rows a group (64 in one) everywhere
+// (256 of 4096 x 6144, 2048 skewed rows of codes 1525 / 993).
 bool few_rows(const GroupedMm& g) { return g.P <= 64 + 3 * g.E; }
 
 constexpr int kSkinnyThreads = 256;
