@@ -261,10 +261,10 @@ def _few_out(s, c, out, idx, w):
 
 
 def _row_codes(v):
-    """(codes, scales) of float32 rows: scale = absmax / 127, the code the integer
-    nearest to v / scale, decided in 64 bits."""
+    """(codes, scales) of float32 rows: scale = absmax times float32's 1 / 127, the
+    code the integer nearest to v / scale, decided in 64 bits."""
     top = v.abs().amax(1, keepdim=True)
-    scale = torch.where(top == 0, 1.0, (top / 127).clamp(min=2.0 ** -126))
+    scale = torch.where(top == 0, 1.0, (top * (1 / 127)).clamp(min=2.0 ** -126))
     return (v.double() / scale.double()).round().float(), scale
 
 
@@ -422,7 +422,7 @@ def exact(case, seed):
         for i in range(0, x.shape[0], 1024):
             v = x[i:i + 1024]
             top = v.abs().max(1).values
-            sc = (top.float() / 127.0).to(f64)  # the scale is a float32
+            sc = (top.float() * (1 / 127)).to(f64)  # the scale is a float32
             sc[top == 0] = 1.0
             scale[i:i + 1024] = sc
             codes[i:i + 1024] = torch.round(v / sc[:, None])
