@@ -4,15 +4,17 @@
  *
  * moe_int4.h serves the layer from int4 / MXFP4 expert blocks.  The calls here
  * compute the same layer from the weights a checkpoint has before that
- * conversion (bfloat16, or e4m3 codes with a float32 scale per 128 x 128), and
- * train it:
+ * conversion (bfloat16, or e4m3 codes with a float32 scale per 128 x 128) or as
+ * 8-bit integers (with a float32 scale per output channel), and train it:
  *
  *   moe_grouped_mm        y[p] = W_e x[row(p)] over rows grouped by expert
  *   moe_grouped_mm_dx     its input's gradient
  *   moe_grouped_mm_dw     its weights' gradient
  *   moe_blockscale_quantize  bf16 / f32 -> e4m3 codes and block scales
  *   moe_blockscale_mm     moe_grouped_mm over e4m3 codes
- *   moe_swiglu[_quantize] silu(gate) * up between the two products
+ *   moe_rowscale_quantize bf16 / f32 -> 8-bit integers and a scale per row
+ *   moe_rowscale_mm       moe_grouped_mm over 8-bit integers
+ *   moe_swiglu[_quantize, _rowscale] silu(gate) * up between the two products
  *   moe_swiglu_grad       its gradient
  *   moe_combine_grad      moe_combine's gradient
  *   moe_block_norm        post norm, gate, residual and next pre norm in one pass
@@ -24,8 +26,8 @@
  * workgroups run (no atomics), so a call repeated on the same inputs gives the
  * same bits (a product's last bits may differ between calls of other sizes, which
  * other kernels add up in another order).  Tensors are row-major without gaps;
- * bf16 and f32 arrays are 16-byte aligned, e4m3 codes and the norms' weights too,
- * int32 arrays, scales and the weights' gradients of the norms 4-byte.
+ * bf16 and f32 arrays are 16-byte aligned, codes, the norms' weights and the
+ * scales of a matrix's output channels too, int32 arrays, other scales and the weights' gradients of the norms 4-byte.
  *
  * Rows grouped by expert: position p belongs to expert e when
  *   offsets[e] <= p < offsets[e + 1],
@@ -118,6 +120,29 @@ moe_status moe_blockscale_mm(int32_t E, int32_t P, int32_t N, int32_t K, const u
                              int32_t rows_div, const uint8_t* wq, const float* ws,
                              const int32_t* offsets, void* y, moe_dtype y_dt, void* stream);
 
+/* 8-bit integers with a float32 scale per row (a token, or an output channel of a
+ * weight matrix): value = code * scale.
+ *   scale = max(absmax * c, 2^-126), c = 1 / 127 and the product rounded to float32;
+ *           1 for a row of zeros, NaN for one that holds a value that is not finite
+ *   code  = the integer nearest to x / scale, ties to even, -127..127, decided
+ *           exactly; 0 where the scale is NaN
+ *  rows    0..2^31 - 1 (n matrices of R rows: n * R); K a multiple of 16, 16..65536
+ *  x       [rows][K] bf16 or f32; codes [rows][K], scales [rows] */
+moe_status moe_rowscale_quantize(int32_t rows, int32_t K, const void* x, moe_dtype x_dt,
+                                 int8_t* codes, float* scales, void* stream);
+
+/* moe_grouped_mm over 8-bit integers:
+ *   y[p][n] = (sum_k wq[e][n][k] * xq[row(p)][k]) * xs[row(p)] * ws[e][n]
+ * with any codes and float32 scales; the sum is exact (int32), then rounded to
+ * float32, as is each product with a scale, and the result to y's type.
+ *  N a multiple of 8 and K of 16, 16..65536
+ *  xq [x_rows][K], xs [x_rows], wq [E][N][K], ws [E][N] (16-byte aligned); rows as in
+ *  moe_grouped_mm, a row of zeros having a scale of 0;  y out [P][N] */
+moe_status moe_rowscale_mm(int32_t E, int32_t P, int32_t N, int32_t K, const int8_t* xq,
+                           const float* xs, int32_t x_rows, const int32_t* rows, int32_t rows_div,
+                           const int8_t* wq, const float* ws, const int32_t* offsets, void* y,
+                           moe_dtype y_dt, void* stream);
+
 /* h[p][c] = silu(gu[p][c]) * gu[p][f + c] for p < P, silu(z) = z / (1 + e^-z).
  *  f       a multiple of 8, 8..32768
  *  gu, h   [P][2 f] and [P][f], both dt (bf16 or f32)
@@ -129,6 +154,11 @@ moe_status moe_swiglu(int32_t P, int32_t f, const void* gu, void* h, moe_dtype d
 /* moe_swiglu, then moe_blockscale_quantize's 1 x 128 blocks of the float32
  * result: codes [P][f], scales [P][ceil(f/128)]; f a multiple of 16. */
 moe_status moe_swiglu_quantize(int32_t P, int32_t f, const void* gu, moe_dtype dt, uint8_t* codes,
+                               float* scales, const int32_t* n_rows, void* stream);
+
+/* moe_swiglu, then moe_rowscale_quantize of the float32 result: codes [P][f],
+ * scales [P]; f a multiple of 16. */
+moe_status moe_swiglu_rowscale(int32_t P, int32_t f, const void* gu, moe_dtype dt, int8_t* codes,
                                float* scales, const int32_t* n_rows, void* stream);
 
 /* With s = 1 / (1 + e^-g): dgu[p][c] = dh u s (1 + g (1 - s)) and

@@ -14,6 +14,9 @@ from ._binding import (  # noqa: F401
     moe_cache_create, moe_cache_destroy, moe_cache_layer_decode, moe_cache_pin, moe_cache_plan,
     moe_cache_stats, moe_cache_last_fetch, moe_cache_unplan_last, moe_cache_workspace_bytes, moe_measure_stream_read,
     moe_grouped_mm, moe_grouped_mm_dx, moe_grouped_mm_dw, moe_grouped_mm_dw_workspace_bytes,
+    moe_rowscale_quantize, moe_rowscale_mm, moe_swiglu_rowscale,
+    MOE_WEIGHTS_BF16, MOE_WEIGHTS_E4M3, MOE_WEIGHTS_INT8, moe_layer_few,
+    moe_layer_few_workspace_bytes, AdamWTensors, moe_adamw,
     moe_blockscale_quantize, moe_blockscale_mm, moe_swiglu, moe_swiglu_quantize, moe_swiglu_grad,
     moe_combine_grad, moe_block_norm, moe_block_norm_grad, moe_block_norm_grad_workspace_bytes,
 )

@@ -23,6 +23,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_
 MOE_F32, MOE_BF16 = 0, 1
 MOE_PATH_DECODE_F32, MOE_PATH_PREFILL_BF16 = 0, 1
 MOE_QUANT_GS64, MOE_QUANT_ROW = 0, 1
+MOE_WEIGHTS_BF16, MOE_WEIGHTS_E4M3, MOE_WEIGHTS_INT8 = 0, 1, 2
 
 # every function include/moe_int4.h declares
 EXPORTS = ("moe_expert_bytes", "moe_pack_experts", "moe_quantize", "moe_route_workspace_bytes",
@@ -35,6 +36,8 @@ EXPORTS = ("moe_expert_bytes", "moe_pack_experts", "moe_quantize", "moe_route_wo
            "moe_cache_layer_decode", "moe_status_str", "moe_measure_stream_read",
            "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
            "moe_grouped_mm_dw_workspace_bytes", "moe_blockscale_quantize", "moe_blockscale_mm",
+           "moe_rowscale_quantize", "moe_rowscale_mm", "moe_swiglu_rowscale",
+           "moe_layer_few", "moe_layer_few_workspace_bytes", "moe_adamw",
            "moe_swiglu", "moe_swiglu_quantize", "moe_swiglu_grad", "moe_combine_grad",
            "moe_block_norm", "moe_block_norm_grad", "moe_block_norm_grad_workspace_bytes")
 
@@ -47,6 +50,19 @@ class Shape(ctypes.Structure):
     def __repr__(self):
         return (f"Shape(d={self.d}, f={self.f}, n_experts={self.n_experts}, top_k={self.top_k}, "
                 f"group={self.group}, f_shared={self.f_shared})")
+
+
+class ExpertWeights(ctypes.Structure):
+    """moe_expert_weights: device addresses."""
+    _fields_ = [(name, c_void_p) for name in ("gate_up", "down", "gate_up_scales", "down_scales")]
+
+
+class AdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor: an element count, device addresses, two moe_dtypes."""
+    _fields_ = ([("n", ctypes.c_int64)] +
+                [(name, c_void_p) for name in ("p", "master", "g", "m", "v", "m_scales",
+                                               "v_scales")] +
+                [("p_dt", c_int32), ("g_dt", c_int32)])
 
 
 class MoeError(RuntimeError):
@@ -141,6 +157,13 @@ def load():
              [i32] * 4 + [vp, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp], i32),
             ("moe_swiglu", [i32, i32, vp, vp, i32, vp, vp], i32),
             ("moe_swiglu_quantize", [i32, i32, vp, i32, vp, vp, vp, vp], i32),
+            ("moe_rowscale_quantize", [i32, i32, vp, i32, vp, vp, vp], i32),
+            ("moe_rowscale_mm", [i32] * 4 + [vp, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp], i32),
+            ("moe_swiglu_rowscale", [i32, i32, vp, i32, vp, vp, vp, vp], i32),
+            ("moe_layer_few_workspace_bytes", [sp, i32], sz),
+            ("moe_layer_few", [sp, i32, vp, vp, vp, i32, POINTER(ExpertWeights),
+                               POINTER(ExpertWeights), vp, vp, vp, i32, vp, sz, vp], i32),
+            ("moe_adamw", [POINTER(AdamWTensor), i32, vp] + [ctypes.c_double] * 5 + [vp, vp], i32),
             ("moe_swiglu_grad", [i32, i32, vp, vp, vp, i32, vp, vp], i32),
             ("moe_combine_grad", [sp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp], i32),
             ("moe_block_norm", [i32, i32, vp, i32, vp, vp, i32, f32, vp, i32, vp, vp, f32, vp, i32,
@@ -416,19 +439,20 @@ def moe_cache_layer_decode(cache: int, x, w_router, bias, shared, topk_idx, topk
 # ----------------------------------------------------------------------------
 
 # set by _types(), which every call below makes first (once: `_T or _types()`)
-_T = _raw_stream = _current_device = None
+_T = _raw_stream = _current_device = _INT8 = None
 _CODES = {}  # torch type -> moe_dtype
 
 
 def _types():
     """(bf16, f32, either, int32, e4m3 code) as tuples of torch types."""
-    global _T, _raw_stream, _current_device
+    global _T, _raw_stream, _current_device, _INT8
     if _T is None:
         import torch
         # the stream's handle and the device's index themselves: building a torch
         # Stream takes as long as a launch
         _raw_stream = torch._C._cuda_getCurrentRawStream
         _current_device = torch._C._cuda_getDevice
+        _INT8 = (torch.int8,)
         _CODES.update({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
         _T = ((torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32), (torch.int32,),
               (torch.float8_e4m3fn, torch.uint8))
@@ -578,6 +602,47 @@ def moe_blockscale_mm(xq, xs, wq, ws, offsets, y, rows=None, rows_div: int = 1, 
          _take(fn, dev, "y", y, floats, (P, N)), _code(y.dtype))
 
 
+def moe_rowscale_quantize(x, codes, scales, stream=None):
+    """x [R, K] or [n, R, K] bf16/f32 -> int8 codes of x's shape and a float32
+    scale per row ([R] or [n, R])."""
+    fn, dev = "moe_rowscale_quantize", x.get_device()
+    _, f32, floats, _, _ = _T or _types()
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{fn}: x has {x.dim()} dimensions, not 2 or 3")
+    shape = _dim(fn, "x", x, x.dim())
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    _run(fn, dev, stream, _int32(fn, rows), shape[-1], _take(fn, dev, "x", x, floats, shape),
+         _code(x.dtype), _take(fn, dev, "codes", codes, _INT8, shape),
+         _take(fn, dev, "scales", scales, f32, shape[:-1]))
+
+
+def moe_rowscale_mm(xq, xs, wq, ws, offsets, y, rows=None, rows_div: int = 1, stream=None):
+    """moe_grouped_mm over 8-bit integers: xq [X, K] int8 with xs [X], wq [E, N, K]
+    int8 with ws [E, N], y [P, N] bf16/f32."""
+    fn, dev = "moe_rowscale_mm", xq.get_device()
+    _, f32, floats, i32, _ = _T or _types()
+    E, N, K = _dim(fn, "wq", wq, 3)
+    P, X = _dim(fn, "y", y, 2)[0], _dim(fn, "xq", xq, 2)[0]
+    _run(fn, dev, stream, E, P, N, K, _take(fn, dev, "xq", xq, _INT8, (X, K)),
+         _take(fn, dev, "xs", xs, f32, (X,)), X,
+         _rows_args(fn, dev, P, rows), _int32(fn, rows_div),
+         _take(fn, dev, "wq", wq, _INT8, (E, N, K)), _take(fn, dev, "ws", ws, f32, (E, N)),
+         _take(fn, dev, "offsets", offsets, i32, (E + 1,)),
+         _take(fn, dev, "y", y, floats, (P, N)), _code(y.dtype))
+
+
+def moe_swiglu_rowscale(gu, codes, scales, n_rows=None, stream=None):
+    """moe_swiglu's result as int8 codes [P, f] and a scale per row [P]."""
+    fn, dev = "moe_swiglu_rowscale", gu.get_device()
+    _, f32, floats, _, _ = _T or _types()
+    P, f = _dim(fn, "codes", codes, 2)
+    _run(fn, dev, stream, P, f, _take(fn, dev, "gu", gu, floats, (P, 2 * f)), _code(gu.dtype),
+         _take(fn, dev, "codes", codes, _INT8, (P, f)),
+         _take(fn, dev, "scales", scales, f32, (P,)), _n_rows(fn, dev, n_rows))
+
+
 def _n_rows(fn, dev, n_rows):
     return None if n_rows is None else _take(fn, dev, "n_rows", n_rows, (_T or _types())[3], (1,))
 
@@ -690,3 +755,143 @@ def moe_block_norm_grad(y, res, dr, dn, dy, dres, dw_post, dw_pre, dgate, w_post
          _take(fn, dev, "dgate", dgate, (ydt,), (head[6], d)),
          _take(fn, dev, "dw_post", dw_post, f32, (d,)),
          _take(fn, dev, "dw_pre", dw_pre, f32, (d,)), ws, nws)
+
+
+# ----------------------------------------------------------------------------
+# the layer for a few tokens (include/moe_int4_few.h)
+# ----------------------------------------------------------------------------
+
+def moe_layer_few_workspace_bytes(shape, T: int) -> int:
+    if not 0 <= T <= _INT32_MAX:
+        return 0
+    return load().moe_layer_few_workspace_bytes(ctypes.byref(_shape(shape)), T)
+
+
+def _expert_weights(fn, dev, who, w, n, d, f):
+    """(kind, moe_expert_weights) of a tuple (gate_up, down[, gate_up_scales,
+    down_scales]) for n experts."""
+    bf16, f32, _, _, codes = _T or _types()
+    gu, dn, gus, dns = w if len(w) == 4 else (*w, None, None)
+    if gu.dtype == bf16[0]:
+        kind, dt, sizes = MOE_WEIGHTS_BF16, bf16, None
+        if gus is not None or dns is not None:
+            raise ValueError(f"{fn}: bfloat16 {who} weights have no scales")
+    elif gu.dtype == _INT8[0]:
+        kind, dt, sizes = MOE_WEIGHTS_INT8, _INT8, ((n, 2 * f), (n, d))
+    elif gu.dtype in codes:
+        b = lambda v: -(-v // 128)  # noqa: E731
+        kind, dt, sizes = MOE_WEIGHTS_E4M3, codes, ((n, b(2 * f), b(d)), (n, b(d), b(f)))
+    else:
+        raise TypeError(f"{fn}: {who} gate_up is {gu.dtype}, not bfloat16, int8 or e4m3 codes")
+    s = ExpertWeights(_take(fn, dev, f"{who} gate_up", gu, dt, (n, 2 * f, d)),
+                      _take(fn, dev, f"{who} down", dn, dt, (n, d, f)))
+    if sizes is not None:
+        if gus is None or dns is None:
+            raise ValueError(f"{fn}: {who} codes have no scales")
+        s.gate_up_scales = _take(fn, dev, f"{who} gate_up scales", gus, f32, sizes[0])
+        s.down_scales = _take(fn, dev, f"{who} down scales", dns, f32, sizes[1])
+    return kind, s
+
+
+def moe_layer_few(shape, x, w_router, bias, experts, shared, topk_idx, topk_w, out, workspace,
+                  stream=None):
+    """The whole layer for x [T, d] bf16, T <= 32 and T * top_k <= 256.  experts:
+    (gate_up [E, 2 f, d], down [E, d, f]) in bf16, or with their scales behind them
+    in e4m3 codes or int8; shared: one expert's the same way, or None.  w_router
+    [E, d] f32 (bias [E] or None): the routing goes to topk_idx and topk_w [T, k];
+    None: they are given.  out [T, d] bf16/f32."""
+    fn, dev = "moe_layer_few", x.get_device()
+    bf16, f32, floats, i32, _ = _T or _types()
+    sh = _shape(shape)
+    T, d, f, E, k = _dim(fn, "x", x, 2)[0], sh.d, sh.f, sh.n_experts, sh.top_k
+    kind, w = _expert_weights(fn, dev, "expert", experts, E, d, f)
+    ws = None
+    if shared is not None:
+        other, ws = _expert_weights(fn, dev, "shared", shared, 1, d, f)
+        if other != kind:
+            raise TypeError(f"{fn}: the shared expert's weights are held another way")
+        ws = ctypes.byref(ws)
+    scratch, n_scratch = _workspace(fn, dev, workspace)
+    _run(fn, dev, stream, ctypes.byref(sh), T, _take(fn, dev, "x", x, bf16, (T, d)),
+         _take(fn, dev, "w_router", w_router, f32, (E, d)), _take(fn, dev, "bias", bias, f32, (E,)),
+         kind, ctypes.byref(w), ws, _take(fn, dev, "topk_idx", topk_idx, i32, (T, k)),
+         _take(fn, dev, "topk_w", topk_w, f32, (T, k)), _take(fn, dev, "out", out, floats, (T, d)),
+         _code(out.dtype), scratch, n_scratch)
+
+
+# ----------------------------------------------------------------------------
+# one AdamW step over many tensors (include/moe_int4_adamw.h)
+# ----------------------------------------------------------------------------
+
+class AdamWTensors:
+    """The tensors of moe_adamw, checked once and held: lists, entry by entry, of
+    the parameters (bf16/f32), their gradients (bf16/f32, of the same shape) and
+    the moments: float32 of the same shape, or with m_scales and v_scales 8-bit
+    codes (m float8_e4m3fn or uint8, v uint8) and a float32 scale per 256 elements.
+    masters: a float32 copy of each bf16 parameter, or None for all or for one.
+    All on one GPU, without gaps, none overlapping one that the step writes."""
+
+    def __init__(self, params, grads, m, v, masters=None, m_scales=None, v_scales=None):
+        fn = "AdamWTensors"
+        _, f32, floats, _, codes = _T or _types()
+        n = len(params)
+        lists = [params, masters, grads, m, v, m_scales, v_scales]
+        names = ("params", "masters", "grads", "m", "v", "m_scales", "v_scales")
+        for i, (name, q) in enumerate(zip(names, lists)):
+            if q is None:
+                if name in ("grads", "m", "v"):
+                    raise ValueError(f"{fn}: {name} is missing")
+                lists[i] = [None] * n
+            elif len(q) != n:
+                raise ValueError(f"{fn}: {len(q)} {name} for {n} params")
+        self.tensors = lists = [list(q) for q in lists]  # held: the step goes by address
+        self.device = params[0].get_device() if n else -1
+        self.array = (AdamWTensor * n)()
+        self.n = n
+        spans = []
+        for i, (p, w, g, a, b, sa, sb) in enumerate(zip(*lists)):
+            for name, t in (("params", p), ("grads", g), ("m", a), ("v", b)):
+                if t is None:
+                    raise ValueError(f"{fn}: {name}[{i}] is missing")
+            if (sa is None) != (sb is None):
+                raise ValueError(f"{fn}: only one of m_scales[{i}] and v_scales[{i}] is given")
+            if w is not None and p.dtype != (_T or _types())[0][0]:
+                raise TypeError(f"{fn}: masters[{i}] stands beside a parameter of {p.dtype}")
+            s = self.array[i]
+            take = lambda name, t, dt, size: _take(fn, self.device, f"{name}[{i}]", t, dt,  # noqa: E731
+                                                   size)
+            s.n = p.numel()
+            blocks = (-(-s.n // 256),)
+            s.p, s.p_dt = take("params", p, floats, p.shape), _code(p.dtype)
+            s.master = take("masters", w, f32, p.shape)
+            s.g, s.g_dt = take("grads", g, floats, p.shape), _code(g.dtype)
+            s.m = take("m", a, f32 if sa is None else codes, p.shape)
+            s.v = take("v", b, f32 if sa is None else codes[1:], p.shape)
+            s.m_scales = take("m_scales", sa, f32, blocks)
+            s.v_scales = take("v_scales", sb, f32, blocks)
+            for t, written in ((p, 1), (w, 1), (g, 0), (a, 1), (b, 1), (sa, 1), (sb, 1)):
+                if t is not None and t.numel():
+                    spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), written, i))
+        # two spans overlap only if one of them does with the one that reaches
+        # furthest among those that begin before it: of the written and of all
+        end = [(0, -1), (0, -1)]
+        for lo, hi, written, i in sorted(spans):
+            for reach, j in (end if written else end[:1]):
+                if lo < reach:
+                    raise ValueError(f"{fn}: tensors {j} and {i} overlap")
+            if written:
+                end[0] = max(end[0], (hi, i))
+            end[1] = max(end[1], (hi, i))
+
+
+def moe_adamw(tensors: AdamWTensors, step, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+              eps: float = 1e-8, weight_decay: float = 0.0, grad_scale=None, stream=None):
+    """One step, in place.  step: device int64 [1], 1 for the first (the caller
+    advances it); grad_scale: device f32 [1] that gradients are multiplied by."""
+    fn = "moe_adamw"
+    import torch
+    dev = tensors.device if tensors.n else step.get_device()
+    _, f32, _, _, _ = _T or _types()
+    _run(fn, dev, stream, tensors.array, tensors.n,
+         _take(fn, dev, "step", step, (torch.int64,), (1,)), lr, beta1, beta2, eps, weight_decay,
+         _take(fn, dev, "grad_scale", grad_scale, f32, (1,)))

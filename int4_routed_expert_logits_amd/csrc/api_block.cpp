@@ -224,6 +224,49 @@ moe_status moe_blockscale_mm(int32_t E, int32_t P, int32_t N, int32_t K, const u
       moe::launch_grouped_mm(g, moe::kGroupedCodes, static_cast<hipStream_t>(stream)));
 }
 
+moe_status moe_rowscale_quantize(int32_t rows, int32_t K, const void* x, moe_dtype x_dt,
+                                 int8_t* codes, float* scales, void* stream) {
+  if (rows < 0 || K <= 0 || K % 16 != 0) return MOE_ERR_SHAPE;
+  if (K > kMaxCols) return MOE_ERR_UNSUPPORTED;
+  if (!float_dtype(x_dt)) return MOE_ERR_DTYPE;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
+  return hip_status(moe::launch_rowscale_quantize(rows, K, x, x_dt == MOE_F32,
+                                                  reinterpret_cast<uint8_t*>(codes), scales,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_rowscale_mm(int32_t E, int32_t P, int32_t N, int32_t K, const int8_t* xq,
+                           const float* xs, int32_t x_rows, const int32_t* rows, int32_t rows_div,
+                           const int8_t* wq, const float* ws, const int32_t* offsets, void* y,
+                           moe_dtype y_dt, void* stream) {
+  moe_status st = check_sizes(E, P, N, K, 16);
+  if (st != MOE_OK) return st;
+  if (!float_dtype(y_dt)) return MOE_ERR_DTYPE;
+  if ((st = check_rows(P, x_rows, rows, rows_div)) != MOE_OK) return st;
+  if (P == 0) return MOE_OK;
+  if (((!xq || !xs) && x_rows > 0) || !wq || !ws || !offsets || !y) return MOE_ERR_NULL;
+  if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(y, 16) || !aligned(xs, 4) ||
+      !aligned(ws, 16) || !aligned(offsets, 4))
+    return MOE_ERR_ALIGN;
+  moe::GroupedMm g{};
+  g.r = reinterpret_cast<const uint8_t*>(xq);
+  g.f = reinterpret_cast<const uint8_t*>(wq);
+  g.r_scale = xs;
+  g.f_scale = ws;
+  g.offsets = offsets;
+  set_rows(g, x_rows, rows, rows_div);
+  g.out = y;
+  g.E = E;
+  g.P = P;
+  g.N = N;
+  g.K = K;
+  g.out_f32 = y_dt == MOE_F32;
+  return hip_status(
+      moe::launch_grouped_mm(g, moe::kGroupedInts, static_cast<hipStream_t>(stream)));
+}
+
 namespace {
 moe_status check_swiglu(int32_t P, int32_t f, moe_dtype dt, const int32_t* n_rows, int f_step) {
   if (P < 0 || f <= 0 || f % f_step != 0) return MOE_ERR_SHAPE;
@@ -251,6 +294,17 @@ moe_status moe_swiglu_quantize(int32_t P, int32_t f, const void* gu, moe_dtype d
   if (!aligned(gu, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
   return hip_status(moe::launch_swiglu(P, f, gu, dt == MOE_F32, codes, scales, n_rows,
                                        static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_swiglu_rowscale(int32_t P, int32_t f, const void* gu, moe_dtype dt, int8_t* codes,
+                               float* scales, const int32_t* n_rows, void* stream) {
+  const moe_status st = check_swiglu(P, f, dt, n_rows, 16);
+  if (st != MOE_OK || P == 0) return st;
+  if (!gu || !codes || !scales) return MOE_ERR_NULL;
+  if (!aligned(gu, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
+  return hip_status(moe::launch_swiglu_rowscale(P, f, gu, dt == MOE_F32,
+                                                reinterpret_cast<uint8_t*>(codes), scales, n_rows,
+                                                static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_swiglu_grad(int32_t P, int32_t f, const void* gu, const void* dh, void* dgu,

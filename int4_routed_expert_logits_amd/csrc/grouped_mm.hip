@@ -3,9 +3,10 @@
 //   input    dx[p] = W_e^T dy[p]
 //   weights  dW_e  = sum over the group's p of dy[p] x[row(p)]^T
 // and the first of them over e4m3 codes with a float32 scale per 128 columns
-// of a row and per 128 x 128 weights.
+// of a row and per 128 x 128 weights, and over 8-bit integers with a float32
+// scale per row of x and per row of W_e.
 //
-// All four are one loop: D[m][n] = sum_k R[m][k] F[n][k] over a tile of one
+// All five are one loop: D[m][n] = sum_k R[m][k] F[n][k] over a tile of one
 // group (256 x 256 where it has the rows), R being the operand whose index is
 // the output's row and F the one whose index is its column.  A stage of the
 // loop is 64 or 128 bytes of the contraction of every row of R and F in LDS,
@@ -41,6 +42,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 // read by scalar loads: a vector load's wait would drain the fetches into LDS
@@ -53,7 +55,7 @@ constexpr int kBlock = 128;       // columns (and weight rows) per scale
 __device__ const uint4 g_zero[8] = {};
 
 // kWeightsBy: kWeights with x gathered through rows.
-enum Kind { kRows, kInput, kWeights, kWeightsBy, kCodes };
+enum Kind { kRows, kInput, kWeights, kWeightsBy, kCodes, kInts };
 
 // This wavefront's fetches but the newest N done and its LDS reads back, then
 // every wavefront of the workgroup here.
@@ -110,6 +112,17 @@ __device__ __forceinline__ f32x4_t codes_product(const u32x4_t (&f)[2], const u3
       p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(f[h][v], f[h][v + 1]),
                                                   codes_to_bf16(r[h][v], r[h][v + 1]), p, 0, 0, 0);
   return p;
+}
+
+// One matrix instruction over 64 bytes of the contraction: 32 bf16 values, or
+// 64 integers, whose int32 sums are exact (K <= 65536 products of at most 2^14).
+__device__ __forceinline__ f32x4_t mma(u32x4_t f, u32x4_t r, f32x4_t acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f),
+                                                 __builtin_bit_cast(bf16x8_t, r), acc, 0, 0, 0);
+}
+__device__ __forceinline__ i32x4_t mma(u32x4_t f, u32x4_t r, i32x4_t acc) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, f),
+                                               __builtin_bit_cast(i32x4_t, r), acc, 0, 0, 0);
 }
 
 struct Group {
@@ -217,7 +230,8 @@ struct Cfg {
   static constexpr bool DW = KIND == kWeights || KIND == kWeightsBy;
   static constexpr bool RT = DW;                    // R contiguous along m
   static constexpr bool FT = DW || KIND == kInput;  // F contiguous along n
-  static constexpr bool F8 = KIND == kCodes;
+  static constexpr bool F8 = KIND == kCodes, I8 = KIND == kInts;
+  using Acc = std::conditional_t<I8, i32x4_t, f32x4_t>;
   static constexpr int RBytes = BM * SB, FBytes = BN * SB;
   static constexpr int SBytes = F8 ? Threads * 4 : 0;  // a stage's row scales
   static constexpr int Stage = RBytes + FBytes + SBytes;
@@ -298,7 +312,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   const int t = threadIdx.x, lane = t & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(t / kWave);
   const int wm = wv % C::WM, wn = wv / C::WM;
-  const int elem = C::F8 ? 1 : 2;
+  const int elem = C::F8 || C::I8 ? 1 : 2;
   const int64_t wsz = static_cast<int64_t>(g.N) * g.K * elem;
   const int red = C::DW ? gb - ga : C::K == kInput ? g.N : g.K;
   const int red_bytes = C::RT ? 0 : red * elem;
@@ -425,11 +439,11 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   };
   if constexpr (C::K == kWeightsBy) load_rows(0);
 
-  f32x4_t acc[C::RF][C::FF];
+  typename C::Acc acc[C::RF][C::FF];
 #pragma unroll
   for (int i = 0; i < C::RF; ++i)
 #pragma unroll
-    for (int j = 0; j < C::FF; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < C::FF; ++j) acc[i][j] = typename C::Acc{0, 0, 0, 0};
   const int mw = wm * C::RF * 16, nw = wn * C::FF * 16;
   const_f32* fsc = nullptr;  // this wavefront's row of weight scales
   float ws_next = 0.0f;      // ... of the next stage
@@ -481,24 +495,23 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     } else {
 #pragma unroll
       for (int kk = 0; kk < C::KK; ++kk) {
-        bf16x8_t fa[C::FF];
+        u32x4_t fa[C::FF];
 #pragma unroll
         for (int j = 0; j < C::FF; ++j) {
           if constexpr (C::FT)
-            fa[j] = __builtin_bit_cast(bf16x8_t, frag_mn<C::BN>(sf, nw + j * 16, kk, lane));
+            fa[j] = frag_mn<C::BN>(sf, nw + j * 16, kk, lane);
           else
-            fa[j] = __builtin_bit_cast(bf16x8_t, frag_k<C::SB>(sf, nw + j * 16, kk, lane));
+            fa[j] = frag_k<C::SB>(sf, nw + j * 16, kk, lane);
         }
 #pragma unroll
         for (int i = 0; i < C::RF; ++i) {
-          bf16x8_t rb;
+          u32x4_t rb;
           if constexpr (C::RT)
-            rb = __builtin_bit_cast(bf16x8_t, frag_mn<C::BM>(sr, mw + i * 16, kk, lane));
+            rb = frag_mn<C::BM>(sr, mw + i * 16, kk, lane);
           else
-            rb = __builtin_bit_cast(bf16x8_t, frag_k<C::SB>(sr, mw + i * 16, kk, lane));
+            rb = frag_k<C::SB>(sr, mw + i * 16, kk, lane);
 #pragma unroll
-          for (int j = 0; j < C::FF; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[j], rb, acc[i][j], 0, 0, 0);
+          for (int j = 0; j < C::FF; ++j) acc[i][j] = mma(fa[j], rb, acc[i][j]);
         }
       }
     }
@@ -519,16 +532,15 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
     int buf = 0;
     for (int s = 0; s < stages; ++s) {
       const uint8_t* st = smem + buf * C::Stage;
-      bf16x8_t fa[C::FF], rb[C::RF];
+      u32x4_t fa[C::FF], rb[C::RF];
 #pragma unroll
       for (int j = 0; j < C::FF; ++j)
-        fa[j] = __builtin_bit_cast(
-            bf16x8_t, C::FT ? frag_mn<C::BN>(st + C::RBytes + C::SBytes, nw + j * 16, 0, lane)
-                            : frag_k<C::SB>(st + C::RBytes + C::SBytes, nw + j * 16, 0, lane));
+        fa[j] = C::FT ? frag_mn<C::BN>(st + C::RBytes + C::SBytes, nw + j * 16, 0, lane)
+                      : frag_k<C::SB>(st + C::RBytes + C::SBytes, nw + j * 16, 0, lane);
 #pragma unroll
       for (int i = 0; i < C::RF; ++i)
-        rb[i] = __builtin_bit_cast(bf16x8_t, C::RT ? frag_mn<C::BM>(st, mw + i * 16, 0, lane)
-                                                   : frag_k<C::SB>(st, mw + i * 16, 0, lane));
+        rb[i] = C::RT ? frag_mn<C::BM>(st, mw + i * 16, 0, lane)
+                      : frag_k<C::SB>(st, mw + i * 16, 0, lane);
       issue(s + C::NST - 1, buf == 0 ? C::NST - 1 : buf - 1);
       wait_fetches<(C::NST - 2) * C::Fetches>();  // this wavefront's part of stage s + 1
       reads_and_meet();
@@ -536,8 +548,7 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
 #pragma unroll
       for (int i = 0; i < C::RF; ++i)
 #pragma unroll
-        for (int j = 0; j < C::FF; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[j], rb[i], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < C::FF; ++j) acc[i][j] = mma(fa[j], rb[i], acc[i][j]);
       __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
       asm volatile("s_barrier" ::: "memory");
@@ -569,21 +580,42 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   // row again (stores of 8 bytes per lane, 32 in a row, took twice the time).
   const int cols = C::FT ? g.K : g.N;
   const int q = lane >> 4;
+  f32x4_t wsc[C::FF];  // integers: the columns' scales
+  if constexpr (C::I8) {
+#pragma unroll
+    for (int j = 0; j < C::FF; ++j) {
+      const int n = n0 + nw + j * 16 + q * 4;
+      wsc[j] = n < cols ? *reinterpret_cast<const f32x4_t*>(g.f_scale +
+                                                            static_cast<int64_t>(e) * g.N + n)
+                        : f32x4_t{0, 0, 0, 0};
+    }
+  }
 #pragma unroll
   for (int i = 0; i < C::RF; ++i) {
     const int m = m0 + mw + i * 16 + (lane & 15);
+    float xsc = 0.0f;
+    if constexpr (C::I8) {
+      const int64_t src = m < mend ? source_row(g, m) : -1;
+      if (src >= 0) xsc = g.r_scale[src];
+    }
+    auto value = [&](int j) -> f32x4_t {
+      if constexpr (C::I8)
+        return __builtin_convertvector(acc[i][j], f32x4_t) * xsc * wsc[j];
+      else
+        return acc[i][j];
+    };
     const int64_t row = (C::DW ? static_cast<int64_t>(e) * g.N + m : m) * cols;
     if (out_f32) {
 #pragma unroll
       for (int j = 0; j < C::FF; ++j) {
         const int n = n0 + nw + j * 16 + q * 4;
         if (m < mend && n < cols)
-          *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + row + n) = acc[i][j];
+          *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + row + n) = value(j);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < C::FF; j += 2) {
-        const f32x4_t u = acc[i][j], v = acc[i][j + 1];
+        const f32x4_t u = value(j), v = value(j + 1);
         const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(u[0], u[1]),
                                                         pack_bf16(v[0], v[1]), false, false);
         const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16(u[2], u[3]),
@@ -669,7 +701,8 @@ constexpr int lds_of() {
 
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void grouped_tiles(GroupedMm g) {
-  constexpr int kBM = Tall<KIND>::BM, kExtra = KIND <= kInput ? High<KIND>::BM - kBM : 0;
+  constexpr int kBM = Tall<KIND>::BM;
+  constexpr int kExtra = KIND <= kInput || KIND == kInts ? High<KIND>::BM - kBM : 0;
   __shared__ __align__(1024)
       uint8_t smem[lds_of<std::conditional_t<(kExtra > 0), High<KIND>, Tall<KIND>>, T128<KIND>,
                           T64<KIND>, T32<KIND>>()];
@@ -891,10 +924,10 @@ __device__ __forceinline__ int find_slot(const GroupedMm& g, int slot, int lane)
 
 template <int KIND>
 struct Skinny {
-  static constexpr bool F8 = KIND != kRows;
+  static constexpr bool F8 = KIND == kCodes, I8 = KIND == kInts;
   static constexpr int kFrags = F8 ? 2 : 1;  // fragments of 16 columns per wavefront
   static constexpr int kCols = 16 * kFrags;
-  static constexpr int kChunk = F8 ? 16 : 8;  // contraction elements per lane and load
+  static constexpr int kChunk = F8 || I8 ? 16 : 8;  // contraction elements per lane and load
   static constexpr int kLoads = 4;            // loads per turn and fragment
   static constexpr int kOcc = F8 ? 4 : 8;     // wavefronts per SIMD: 64 registers for bf16
   static constexpr int kSpan = kLoads * kChunk * 4;  // contraction elements of a turn
@@ -905,13 +938,15 @@ __global__ __launch_bounds__(kSkinnyThreads, Skinny<KIND>::kOcc) void grouped_sk
                                                                                    int nb) {
   using C = Skinny<KIND>;
   constexpr bool F8 = C::F8;
-  __shared__ float part[kSkinnyWaves][16][C::kCols + 1];
+  using Acc = std::conditional_t<C::I8, i32x4_t, f32x4_t>;
+  using Sum = std::conditional_t<C::I8, int, float>;
+  __shared__ Sum part[kSkinnyWaves][16][C::kCols + 1];
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave;
   const int e = __builtin_amdgcn_readfirstlane(find_slot(g, blockIdx.x / nb, lane));
   if (e < 0) return;
   int a, b;
   group_bounds(g, e, a, b);
-  const int n0 = (blockIdx.x % nb) * C::kCols, elem = F8 ? 1 : 2;
+  const int n0 = (blockIdx.x % nb) * C::kCols, elem = F8 || C::I8 ? 1 : 2;
   const int i16 = lane & 15, q = lane >> 4;
   const int64_t ld = static_cast<int64_t>(g.K) * elem;
   const uint8_t* wp[C::kFrags];
@@ -926,9 +961,9 @@ __global__ __launch_bounds__(kSkinnyThreads, Skinny<KIND>::kOcc) void grouped_sk
     int64_t src = -1;
     if (m0 + i16 < b) src = source_row(g, m0 + i16);
     const uint8_t* xp = g.r + (src < 0 ? 0 : src) * ld + q * 16;
-    f32x4_t acc[C::kFrags];
+    Acc acc[C::kFrags];
 #pragma unroll
-    for (int f = 0; f < C::kFrags; ++f) acc[f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int f = 0; f < C::kFrags; ++f) acc[f] = Acc{0, 0, 0, 0};
     for (int k0 = wv * C::kSpan; k0 < g.K; k0 += kSkinnyWaves * C::kSpan) {
       u32x4_t w[C::kFrags][C::kLoads], x[C::kLoads];
 #pragma unroll
@@ -973,10 +1008,7 @@ __global__ __launch_bounds__(kSkinnyThreads, Skinny<KIND>::kOcc) void grouped_sk
 #pragma unroll
         for (int u = 0; u < C::kLoads; ++u)
 #pragma unroll
-          for (int f = 0; f < C::kFrags; ++f)
-            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8_t, w[f][u]), __builtin_bit_cast(bf16x8_t, x[u]), acc[f],
-                0, 0, 0);
+          for (int f = 0; f < C::kFrags; ++f) acc[f] = mma(w[f][u], x[u], acc[f]);
       }
     }
 #pragma unroll
@@ -988,9 +1020,15 @@ __global__ __launch_bounds__(kSkinnyThreads, Skinny<KIND>::kOcc) void grouped_sk
     for (int o = t; o < 16 * C::kCols; o += kSkinnyThreads) {
       const int m = m0 + o / C::kCols, n = n0 + o % C::kCols;
       if (m >= b || n >= g.N) continue;
-      float v = 0.0f;
+      Sum sum = 0;
 #pragma unroll
-      for (int w = 0; w < kSkinnyWaves; ++w) v += part[w][o / C::kCols][o % C::kCols];
+      for (int w = 0; w < kSkinnyWaves; ++w) sum += part[w][o / C::kCols][o % C::kCols];
+      float v = static_cast<float>(sum);
+      if constexpr (C::I8) {
+        const int64_t from = source_row(g, m);
+        v = v * (from >= 0 ? g.r_scale[from] : 0.0f) *
+            g.f_scale[static_cast<int64_t>(e) * g.N + n];
+      }
       const int64_t at = static_cast<int64_t>(m) * g.N + n;
       if (g.out_f32)
         static_cast<float*>(g.out)[at] = v;
@@ -1028,12 +1066,16 @@ hipError_t launch_grouped_mm(const GroupedMm& args, GroupedKind kind, hipStream_
                   g);
   }
   if (kind != kGroupedInput && few_rows(g)) {
-    const int cols = kind == kGroupedRows ? Skinny<kRows>::kCols : Skinny<kCodes>::kCols;
-    const int nb = (g.N + cols - 1) / cols;
-    const dim3 grid(static_cast<uint32_t>(nb * (g.E < g.P ? g.E : g.P))), block(kSkinnyThreads);
-    return kind == kGroupedRows
-               ? launch(grouped_skinny<kRows>, grid, block, 0, stream, g, nb)
-               : launch(grouped_skinny<kCodes>, grid, block, 0, stream, g, nb);
+    auto skinny = [&](auto kernel, int cols) {
+      const int nb = (g.N + cols - 1) / cols;
+      return launch(kernel, dim3(static_cast<uint32_t>(nb * (g.E < g.P ? g.E : g.P))),
+                    dim3(kSkinnyThreads), 0, stream, g, nb);
+    };
+    switch (kind) {
+      case kGroupedRows: return skinny(grouped_skinny<kRows>, Skinny<kRows>::kCols);
+      case kGroupedInts: return skinny(grouped_skinny<kInts>, Skinny<kInts>::kCols);
+      default: return skinny(grouped_skinny<kCodes>, Skinny<kCodes>::kCols);
+    }
   }
   const int cols = kind == kGroupedInput ? g.K : g.N;
   const int bm = kind == kGroupedCodes ? Tall<kCodes>::BM : Tall<kRows>::BM;
@@ -1044,12 +1086,14 @@ hipError_t launch_grouped_mm(const GroupedMm& args, GroupedKind kind, hipStream_
     switch (kind) {
       case kGroupedRows: return go(grouped_small<kRows>, small, S::Threads);
       case kGroupedInput: return go(grouped_small<kInput>, small, S::Threads);
+      case kGroupedInts: return go(grouped_small<kInts>, small, S::Threads);
       default: return go(grouped_small<kCodes>, small, S::Threads);
     }
   }
   switch (kind) {
     case kGroupedRows: return go(grouped_tiles<kRows>, tiles, kThreads);
     case kGroupedInput: return go(grouped_tiles<kInput>, tiles, kThreads);
+    case kGroupedInts: return go(grouped_tiles<kInts>, tiles, kThreads);
     default: return go(grouped_tiles<kCodes>, tiles, kThreads);
   }
 }

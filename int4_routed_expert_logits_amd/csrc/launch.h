@@ -122,7 +122,8 @@ hipError_t launch_combine(int T, int d, int k, const void* y, const void* y_shar
 struct GroupedMm {
   const uint8_t* r;  // operand indexed by the output's row: x or its codes, dy
   const uint8_t* f;  // ... by the output's column: w or its codes, x
-  const float *r_scale, *f_scale;  // kGroupedCodes: per (row, 128 columns), per 128 x 128
+  // kGroupedCodes: per (row, 128 columns), per 128 x 128; kGroupedInts: per row of each
+  const float *r_scale, *f_scale;
   const int32_t* offsets;          // [E + 1]
   const int32_t* rows;             // [P] source rows of x times div, or NULL
   uint32_t row_limit, div_magic;   // rows entries below row_limit are valid
@@ -133,7 +134,7 @@ struct GroupedMm {
   bool out_f32;
 };
 size_t grouped_dw_workspace(int E, int P, int N, int K);
-enum GroupedKind { kGroupedRows, kGroupedInput, kGroupedWeights, kGroupedCodes };
+enum GroupedKind { kGroupedRows, kGroupedInput, kGroupedWeights, kGroupedCodes, kGroupedInts };
 hipError_t launch_grouped_mm(const GroupedMm& g, GroupedKind kind, hipStream_t stream);
 
 // blockscale.hip: e4m3 codes with a float32 scale per 128 columns (or per 128
@@ -145,6 +146,56 @@ hipError_t launch_swiglu(int P, int f, const void* gu, bool f32, void* h, float*
                          const int32_t* n_rows, hipStream_t stream);
 hipError_t launch_swiglu_grad(int P, int f, const void* gu, const void* dh, bool f32, void* dgu,
                               const int32_t* n_rows, hipStream_t stream);
+
+// rowscale.hip: 8-bit integers with a float32 scale per row, and SwiGLU's
+// result as such.
+hipError_t launch_rowscale_quantize(int64_t rows, int K, const void* x, bool f32, uint8_t* codes,
+                                    float* scales, hipStream_t stream);
+hipError_t launch_swiglu_rowscale(int P, int f, const void* gu, bool f32, uint8_t* codes,
+                                  float* scales, const int32_t* n_rows, hipStream_t stream);
+
+// layer_few.hip: experts, SwiGLU and combine for at most kFewTokens tokens and
+// kFewPairs (token, expert) pairs, given the routing.
+constexpr int kFewTokens = 32, kFewPairs = 256;
+enum FewKind { kFewBf16, kFewE4m3, kFewInt8 };
+struct FewLayer {
+  int T, k, d, f, E;
+  int shared;  // 1: with a shared expert
+  const void* x;
+  const int32_t* topk_idx;
+  const float* topk_w;
+  const void *gate_up, *down, *shared_gate_up, *shared_down;
+  const float *gate_up_scales, *down_scales, *shared_gate_up_scales, *shared_down_scales;
+  uint16_t *h_hi, *h_lo;  // [T * k (+ T)][f]
+  void* out;
+  bool out_f32;
+};
+size_t few_workspace(int T, int k, int f, bool shared);
+hipError_t launch_layer_few(const FewLayer& g, FewKind kind, hipStream_t stream);
+
+// adamw.hip: one optimiser step over many tensors.
+constexpr int kAdamWBatch = 40;   // tensors a launch
+constexpr int kAdamWBlock = 256;  // elements per scale of 8-bit moments
+struct AdamWTensor {
+  int64_t n;
+  void *p, *master;
+  const void* g;
+  void *m, *v;
+  float *m_scales, *v_scales;  // NULL: float32 moments
+  bool p_bf16, g_bf16;
+  bool wide;  // every array is aligned for four elements at once
+};
+struct AdamWStep {
+  const int64_t* step;
+  const float* grad_scale;
+  double lr, log_beta1, log_beta2;
+  float beta1, rest1, beta2, rest2, eps, keep;  // rest = 1 - beta, keep = 1 - lr * decay
+};
+struct AdamWSource {
+  const void* tensors;
+  AdamWTensor (*get)(const void* tensors, int i);
+};
+hipError_t launch_adamw(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t stream);
 
 // block_norm.hip: the norms and the residual around a block, and the gradient.
 struct BlockNorm {
