@@ -84,9 +84,10 @@ moe_status moe_layer_few(const moe_shape* shape, int32_t T, const void* x, const
     g.shared_gate_up_scales = shared->gate_up_scales;
     g.shared_down_scales = shared->down_scales;
   }
-  g.h_hi = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) +
-                                       moe_route_workspace_bytes(shape, T));
-  g.h_lo = g.h_hi + static_cast<size_t>(T) * (g.k + g.shared) * g.f;
+  uint8_t* scratch = static_cast<uint8_t*>(workspace) + moe_route_workspace_bytes(shape, T);
+  g.table = scratch;
+  g.h = reinterpret_cast<uint16_t*>(scratch + moe::kFewTableBytes);
+  g.h_apart = static_cast<int64_t>(T) * (g.k + g.shared) * g.f;
   g.out = out;
   g.out_f32 = out_dt == MOE_F32;
   if (w_router) {

@@ -157,6 +157,7 @@ hipError_t launch_swiglu_rowscale(int P, int f, const void* gu, bool f32, uint8_
 // layer_few.hip: experts, SwiGLU and combine for at most kFewTokens tokens and
 // kFewPairs (token, expert) pairs, given the routing.
 constexpr int kFewTokens = 32, kFewPairs = 256;
+constexpr size_t kFewTableBytes = 2080;  // of the grouping between its kernels
 enum FewKind { kFewBf16, kFewE4m3, kFewInt8 };
 struct FewLayer {
   int T, k, d, f, E;
@@ -166,7 +167,9 @@ struct FewLayer {
   const float* topk_w;
   const void *gate_up, *down, *shared_gate_up, *shared_down;
   const float *gate_up_scales, *down_scales, *shared_gate_up_scales, *shared_down_scales;
-  uint16_t *h_hi, *h_lo;  // [T * k (+ T)][f]
+  void* table;      // kFewTableBytes, 16-byte aligned
+  uint16_t* h;      // h as a sum of two or three bf16 parts, each [T * k (+ T)][f]
+  int64_t h_apart;  // from one part to the next
   void* out;
   bool out_f32;
 };

@@ -34,19 +34,21 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kCols = 16;     // weight rows (output columns) of a fragment
+constexpr int kCols = 8;      // weight rows (output columns) of a fragment
 constexpr int kBlock = 128;   // rows and columns per scale of e4m3 codes
-constexpr int kMaxPairs = 256, kMaxIds = 1024;
+constexpr int kMaxPairs = 256, kMaxIds = 1024, kCus = 256;
 constexpr int kIds = kMaxPairs / kWave;  // ids a lane holds
-constexpr int kChunkRows = 32;           // tokens per pass over an expert's weights
 
+// A load of a wavefront: 8 weight rows x 128 bytes.  The matrix instruction's 16
+// rows are those 8 with the first 64 bytes and again with the other 64, its 16
+// columns 8 tokens with the one and with the other half of x, so that of its
+// result the two 8 x 8 blocks on the diagonal are the two halves' sums.
 template <int KIND>
 struct Fmt {
   static constexpr int kElem = KIND == kFewBf16 ? 2 : 1;
-  static constexpr int kChunk = 16 / kElem;       // values a lane loads at once
-  static constexpr int kStep = 4 * kChunk;        // contraction of one load
-  static constexpr int kLoads = 4;                // loads of a turn
-  static constexpr int kTurn = kLoads * kStep;    // contraction of a turn
+  static constexpr int kChunk = 16 / kElem;  // values a lane loads at once
+  static constexpr int kHalf = 4 * kChunk;   // contraction of half a load
+  static constexpr int kStep = 2 * kHalf;    // ... of a load
 };
 
 // The pairs' ids, a few per lane; -1 where there is none or it names no expert.
@@ -118,6 +120,84 @@ __device__ __forceinline__ int pairs_of(const Ids& ids, int e, int lane, uint8_t
   return n;
 }
 
+// The grouping as few_gate_up leaves it for few_down: the experts hit, ascending,
+// and each one's pairs, ascending.
+struct alignas(16) FewTable {
+  int32_t n;                           // experts hit
+  int32_t most;                        // pairs of the one that has most
+  uint16_t active[kMaxPairs];          // the experts
+  uint16_t start[kMaxPairs + 8];       // where an expert's pairs begin in `pair`; the end
+  uint8_t pair[kMaxPairs];
+  uint8_t group[kMaxPairs];            // of a pair: which of `active`,
+  uint8_t rank[kMaxPairs];             // the how many-th of its pairs,
+  uint8_t valid[kMaxPairs];            // whether its id names an expert (else no more is said)
+};
+static_assert(sizeof(FewTable) == kFewTableBytes, "workspace");
+
+// ... made by one workgroup of WAVES wavefronts, with scratch in LDS.
+template <int WAVES>
+__device__ void make_table(const Ids& ids, FewTable* out, uint32_t* bits, uint8_t (*lists)[kMaxPairs],
+                           FewTable& tb) {
+  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
+  mark_experts(ids, bits);
+  if (wv == 0) {
+    uint32_t m = lane < 32 ? bits[lane] : 0u;
+    const int c = __popc(m), inc = scan32(c, lane);
+    for (int at = inc - c; m; m &= m - 1)
+      tb.active[at++] = static_cast<uint16_t>(lane * 32 + __ffs(m) - 1);
+    if (lane == 31) tb.n = inc;
+#pragma unroll
+    for (int i = 0; i < kIds; ++i) tb.valid[lane + i * kWave] = ids.id[i] >= 0;
+  }
+  __syncthreads();
+  for (int g = wv; g < tb.n; g += WAVES) {
+    const int n = pairs_of(ids, tb.active[g], lane, lists[wv]);
+    if (lane == 0) tb.start[g] = static_cast<uint16_t>(n);
+  }
+  __syncthreads();
+  if (wv == 0) {
+    int v[kIds], sum = 0, most = 0;
+#pragma unroll
+    for (int i = 0; i < kIds; ++i) {
+      const int g = lane * kIds + i;
+      v[i] = g < tb.n ? tb.start[g] : 0;
+      sum += v[i];
+      most = max(most, v[i]);
+    }
+    int at = sum;
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int u = __shfl_up(at, off, kWave);
+      if (lane >= off) at += u;
+      most = max(most, __shfl_xor(most, off, kWave));
+    }
+    const int end = at;
+    at -= sum;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < kIds; ++i) {
+      if (lane * kIds + i <= tb.n) tb.start[lane * kIds + i] = static_cast<uint16_t>(at);
+      at += v[i];
+    }
+    if (lane == kWave - 1) {
+      tb.start[kMaxPairs] = static_cast<uint16_t>(end);  // where all 256 are groups
+      tb.most = most;
+    }
+  }
+  __syncthreads();
+  for (int g = wv; g < tb.n; g += WAVES) {
+    const int n = pairs_of(ids, tb.active[g], lane, lists[wv]), at = tb.start[g];
+    for (int i = lane; i < n; i += kWave) {
+      const int s = lists[wv][i];
+      tb.pair[at + i] = static_cast<uint8_t>(s);
+      tb.group[s] = static_cast<uint8_t>(g);
+      tb.rank[s] = static_cast<uint8_t>(i);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(FewTable) / 16); i += WAVES * kWave)
+    reinterpret_cast<u32x4_t*>(out)[i] = reinterpret_cast<const u32x4_t*>(&tb)[i];
+}
+
 // Eight codes as bf16, exactly.
 template <int KIND>
 __device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi) {
@@ -139,103 +219,147 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi) {
   }
 }
 
-__device__ __forceinline__ u32x4_t load16(const void* p, int64_t byte) {
-  return *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(p) + byte);
+// 16 bytes at a uniform address and a lane's offset.
+__device__ __forceinline__ u32x4_t load16(const uint8_t* base, uint32_t off) {
+  return *reinterpret_cast<const u32x4_t*>(base + off);
 }
 
 __device__ __forceinline__ f32x4_t mma(bf16x8_t w, u32x4_t x, f32x4_t acc) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8_t, x), acc, 0, 0, 0);
 }
 
-// The B side: this lane's row of x (or of h's two parts) in each fragment.
-template <int NB, bool SPLIT>
-struct Rows {
-  const uint16_t* hi[NB];
-  const uint16_t* lo[NB];
-  bool on[NB];
-  __device__ __forceinline__ f32x4_t product(bf16x8_t w, int b, int k, f32x4_t acc) const {
-    u32x4_t v{0, 0, 0, 0}, u{0, 0, 0, 0};
-    if (on[b]) {
-      v = load16(hi[b] + k, 0);
-      if constexpr (SPLIT) u = load16(lo[b] + k, 0);
-    }
-    acc = mma(w, v, acc);
-    if constexpr (SPLIT) acc = mma(w, u, acc);
-    return acc;
+// One wavefront's loads of weights: step s of its two fragments.
+template <int FR>
+struct Weights {
+  const uint8_t* p[FR];  // the fragments' first rows
+  const float* scales[FR];  // e4m3: of the fragments' block rows
+};
+template <int KIND, int FR>
+struct Loaded {
+  u32x4_t w[FR];
+  // `last`: the step whose second half lies past the contraction's end; there the
+  // lanes of that half read the first
+  __device__ __forceinline__ void load(const Weights<FR>& at, uint32_t off, int s, int last, int half) {
+    if (KIND != kFewBf16 && s == last) off -= half * 64;
+#pragma unroll
+    for (int f = 0; f < FR; ++f) w[f] = load16(at.p[f] + static_cast<int64_t>(s) * 128, off);
   }
 };
 
-// One turn of the contraction, [k0, k0 + kTurn): this wavefront's 16 weight rows
-// (wp: the lane's row, its part of a load) times the tokens.  scales: of the
-// turn's blocks of 128 (e4m3).
-template <int KIND, int NB, bool SPLIT>
-__device__ __forceinline__ void turn(const uint8_t* wp, const float* scales, int k0, int K, int q,
-                                     const Rows<NB, SPLIT>& rows, f32x4_t (&acc)[NB]) {
+// Steps [from, to) of a contraction of K, into acc.  `first` holds step `from`
+// already and is left with step next_from of `next`: the loads of what comes next
+// are under way while a step is worked on, the tokens' ahead of them, since loads
+// come back in the order of their issue.
+//  off  this lane's place in a fragment's load
+//  x    the tokens (NB of them a lane, at xo), or the PARTS of h, `apart` bytes from
+//       one another.  Lanes without a token read another one's: no one reads their
+//       sums.
+template <int KIND, int FR, int NB, int PARTS>
+__device__ __forceinline__ void steps(const Weights<FR>& at, uint32_t off, Loaded<KIND, FR>& first,
+                                      int from, int to, int K, const Weights<FR>& next, int next_from,
+                                      const uint8_t* x, const uint32_t (&xo)[NB], int64_t apart,
+                                      int half, f32x4_t (&acc)[FR][NB]) {
   using F = Fmt<KIND>;
-  u32x4_t w[F::kLoads];
+  constexpr int kPer = KIND == kFewBf16 ? 1 : 2;  // matrix instructions per load and token
+  const int last = K % F::kStep ? K / F::kStep : -1;
+  u32x4_t v[kPer][NB][PARTS];
+  auto tokens = [&](int s) {
 #pragma unroll
-  for (int u = 0; u < F::kLoads; ++u)
-    w[u] = k0 + u * F::kStep < K ? load16(wp, static_cast<int64_t>(k0 + u * F::kStep) * F::kElem)
-                                 : u32x4_t{0, 0, 0, 0};
-  if constexpr (KIND == kFewBf16) {
-#pragma unroll
-    for (int u = 0; u < F::kLoads; ++u) {
-      const int k = k0 + u * F::kStep;
-      if (k >= K) break;
+    for (int i = 0; i < kPer; ++i)
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        acc[b] = rows.product(__builtin_bit_cast(bf16x8_t, w[u]), b, k + q * F::kChunk, acc[b]);
-    }
-  } else {
-    constexpr int kPer = kBlock / F::kStep;  // loads per block
 #pragma unroll
-    for (int h = 0; h < F::kLoads; h += kPer) {
-      if (k0 + h * F::kStep >= K) break;
-      f32x4_t p[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) p[b] = KIND == kFewE4m3 ? f32x4_t{0, 0, 0, 0} : acc[b];
-#pragma unroll
-      for (int u = h; u < h + kPer; ++u) {
-        const int k = k0 + u * F::kStep;
-        if (k >= K) break;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const bf16x8_t c = widen<KIND>(w[u][2 * v], w[u][2 * v + 1]);
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            p[b] = rows.product(c, b, k + q * F::kChunk + v * 8, p[b]);
+        for (int p = 0; p < PARTS; ++p) {
+          uint32_t o = xo[b] + i * 16;
+          if (KIND != kFewBf16 && s == last) o -= half * (F::kHalf * 2);
+          v[i][b][p] = load16(x + p * apart + static_cast<int64_t>(s) * (F::kStep * 2), o);
         }
-      }
+  };
+  auto work = [&](const Loaded<KIND, FR>& l, int s) {
+    if (KIND != kFewBf16 && s == last) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if constexpr (KIND == kFewE4m3) {
-          const float s = scales[(k0 + h * F::kStep) / kBlock];
+      for (int i = 0; i < kPer; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[b][j] = fmaf(s, p[b][j], acc[b][j]);
-        } else {
-          acc[b] = p[b];
-        }
-      }
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p)
+            if (half) v[i][b][p] = u32x4_t{0, 0, 0, 0};
     }
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+      f32x4_t sum[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) sum[b] = KIND == kFewE4m3 ? f32x4_t{0, 0, 0, 0} : acc[f][b];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        bf16x8_t c;
+        if constexpr (KIND == kFewBf16)
+          c = __builtin_bit_cast(bf16x8_t, l.w[f]);
+        else
+          c = widen<KIND>(l.w[f][2 * i], l.w[f][2 * i + 1]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) sum[b] = mma(c, v[i][b][p], sum[b]);
+      }
+      static_assert(KIND != kFewE4m3 || F::kStep == kBlock, "a load is a block of scales");
+      const float scale = KIND == kFewE4m3 ? at.scales[f][s] : 1.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[f][b][j] = KIND == kFewE4m3 ? fmaf(scale, sum[b][j], acc[f][b][j]) : sum[b][j];
+    }
+  };
+  Loaded<KIND, FR> second;
+  for (int s = from; s < to; s += 2) {
+    const bool two = s + 1 < to, more = s + 2 < to;
+    tokens(s);
+    second.load(at, off, min(s + 1, to - 1), last, half);
+    __builtin_amdgcn_sched_barrier(0);
+    work(first, s);
+    __builtin_amdgcn_sched_barrier(0);
+    if (two) tokens(s + 1);
+    first.load(more ? at : next, off, more ? s + 2 : next_from, last, half);
+    __builtin_amdgcn_sched_barrier(0);
+    if (two) work(second, s + 1);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// ---------------------------------------------------------------------------
-// gate and up: a workgroup takes 16 columns of one expert's h; four wavefronts
-// the gate's rows and four the up's, in turns along the contraction.
-// ---------------------------------------------------------------------------
-constexpr int kGuWaves = 8, kGuThreads = kGuWaves * kWave;
+// The sums of a fragment's two halves: column 4 (lane / 16) + j of token lane % 16
+// in lanes of the first 32 with a token below 8.
+__device__ __forceinline__ bool owns_sums(int lane) { return lane < 32 && !(lane & 8); }
+__device__ __forceinline__ f32x4_t both_halves(f32x4_t v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] += __shfl_down(v[j], 40, kWave);
+  return v;
+}
 
-template <int KIND>
+// ---------------------------------------------------------------------------
+// gate and up: a workgroup takes 8 columns of one expert's h: each wavefront the
+// gate's and the up's rows over an eighth of the contraction.
+// ---------------------------------------------------------------------------
+constexpr int kGuFrags = 2;  // the gate's and the up's
+constexpr int kGuWaves = 4, kGuThreads = kGuWaves * kWave;
+
+// MANY: up to 16 tokens in one pass over an expert's weights, else 8.
+template <int KIND, int PARTS, bool MANY>
 __global__ __launch_bounds__(kGuThreads) void few_gate_up(FewLayer g, int tiles) {
   using F = Fmt<KIND>;
-  __shared__ float part[kGuWaves][kChunkRows][kCols + 1];
+  constexpr int kPassRows = MANY ? 16 : 8;
+  __shared__ float part[kGuWaves][kGuFrags][kPassRows][kCols + 1];
   __shared__ uint32_t bits[kMaxIds / 32];
   __shared__ uint8_t lists[kGuWaves][kMaxPairs];
   const int t = threadIdx.x, lane = t & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(t / kWave);
-  const int n0 = static_cast<int>(blockIdx.x) % tiles * kCols;
-  int slot = static_cast<int>(blockIdx.x) / tiles;
+  if (blockIdx.x == 0) {  // one more workgroup: the grouping for the other kernel
+    __shared__ FewTable tb;
+    make_table<kGuWaves>(load_ids(g, lane), static_cast<FewTable*>(g.table), bits, lists, tb);
+    return;
+  }
+  const int id = static_cast<int>(blockIdx.x) - 1, n0 = id % tiles * kCols;
+  int slot = id / tiles;
   const bool shared = g.shared && slot == 0;
   slot -= g.shared;
   int e = 0, n = g.T;
@@ -247,170 +371,241 @@ __global__ __launch_bounds__(kGuThreads) void few_gate_up(FewLayer g, int tiles)
     if (e < 0) return;
     n = pairs_of(ids, e, lane, lists[wv]);
   }
-  const int i16 = lane & 15, q = lane >> 4;
-  const int row0 = (wv < kGuWaves / 2 ? 0 : g.f) + n0;  // of this wavefront's weight rows
+  const int i8 = lane & 7, half = (lane >> 3) & 1, q = lane >> 4;
   const uint8_t* wbase = static_cast<const uint8_t*>(shared ? g.shared_gate_up : g.gate_up);
   const float* sbase = shared ? g.shared_gate_up_scales : g.gate_up_scales;
-  const uint8_t* wp = wbase +
-                      (static_cast<int64_t>(e) * 2 * g.f + row0 + i16) * g.d * F::kElem + q * 16;
-  const float* ws = nullptr;
-  if (KIND == kFewE4m3)
-    ws = sbase + (static_cast<int64_t>(e) * ((2 * g.f + kBlock - 1) / kBlock) + row0 / kBlock) *
-                     ((g.d + kBlock - 1) / kBlock);
-  const uint16_t* x = static_cast<const uint16_t*>(g.x);
-  for (int m0 = 0; m0 < n; m0 += kChunkRows) {
+  Weights<kGuFrags> at;
+#pragma unroll
+  for (int f = 0; f < kGuFrags; ++f) {
+    const int row = f * g.f + n0;  // the gate's, the up's
+    at.p[f] = wbase + (static_cast<int64_t>(e) * 2 * g.f + row) * g.d * F::kElem;
+    at.scales[f] = KIND != kFewE4m3 ? nullptr
+                                    : sbase + (static_cast<int64_t>(e) * ((2 * g.f + kBlock - 1) / kBlock) +
+                                               row / kBlock) * ((g.d + kBlock - 1) / kBlock);
+  }
+  const uint32_t off = static_cast<uint32_t>(i8 * g.d * F::kElem + half * 64 + q * 16);
+  const int all = (g.d + F::kStep - 1) / F::kStep;
+  const int from = all * wv / kGuWaves, to = all * (wv + 1) / kGuWaves;
+  const int last = g.d % F::kStep ? g.d / F::kStep : -1;
+  Loaded<KIND, kGuFrags> w;
+  w.load(at, off, min(from, all - 1), last, half);
+  for (int m0 = 0; m0 < n; m0 += kPassRows) {
     auto pass = [&](auto nb) {
       constexpr int NB = decltype(nb)::value;
-      Rows<NB, false> rows;
-      f32x4_t acc[NB];
+      f32x4_t acc[kGuFrags][NB];
+      uint32_t xo[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int r = m0 + b * 16 + i16;
-        rows.on[b] = r < n;
-        const int token = r >= n ? 0 : shared ? r : list[r] / g.k;
-        rows.hi[b] = x + static_cast<int64_t>(token) * g.d;
-        acc[b] = f32x4_t{0, 0, 0, 0};
+        const int r = min(m0 + b * 8 + i8, n - 1);
+        const int token = shared ? r : list[r] / g.k;
+        xo[b] = static_cast<uint32_t>(token * g.d + half * F::kHalf + q * F::kChunk) * 2;
+        acc[0][b] = acc[1][b] = f32x4_t{0, 0, 0, 0};
       }
-      for (int k0 = (wv & 3) * F::kTurn; k0 < g.d; k0 += 4 * F::kTurn)
-        turn<KIND, NB, false>(wp, ws, k0, g.d, q, rows, acc);
+      steps<KIND, kGuFrags, NB, 1>(at, off, w, from, to, g.d, at, min(from, all - 1),
+                         static_cast<const uint8_t*>(g.x), xo, 0, half, acc);
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int f = 0; f < kGuFrags; ++f)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) part[wv][b * 16 + i16][q * 4 + j] = acc[b][j];
+        for (int b = 0; b < NB; ++b) {
+          const f32x4_t v = both_halves(acc[f][b]);
+          if (owns_sums(lane))
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part[wv][f][b * 8 + i8][q * 4 + j] = v[j];
+        }
     };
-    if (n - m0 > 16)
-      pass(std::integral_constant<int, 2>{});
-    else
+    if constexpr (MANY) {
+      if (n - m0 > 8)
+        pass(std::integral_constant<int, 2>{});
+      else
+        pass(std::integral_constant<int, 1>{});
+    } else {
       pass(std::integral_constant<int, 1>{});
+    }
     __syncthreads();
-    const int r = t / kCols, c = t % kCols;  // 512 threads: 32 rows of 16 columns
-    if (m0 + r < n) {
+    const int r = t / kCols, c = t % kCols;
+    if (r < kPassRows && m0 + r < n) {
       float gate = 0.0f, up = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kGuWaves / 2; ++w) {
-        gate += part[w][r][c];
-        up += part[w + kGuWaves / 2][r][c];
+      for (int w = 0; w < kGuWaves; ++w) {
+        gate += part[w][0][r][c];
+        up += part[w][1][r][c];
       }
       if (KIND == kFewInt8) {
         const float* s = sbase + static_cast<int64_t>(e) * 2 * g.f + n0 + c;
         gate *= s[0];
         up *= s[g.f];
       }
-      const float h = silu(gate) * up;
-      const uint16_t hi = f32_to_bf16(h);
-      const float rest = h - bf16_to_f32(hi);
-      // an infinity has no rest
-      const uint16_t lo = rest == rest ? f32_to_bf16(rest) : static_cast<uint16_t>(0);
+      float h = silu(gate) * up;
       const int row = shared ? g.T * g.k + m0 + r : list[m0 + r];
-      const int64_t at = static_cast<int64_t>(row) * g.f + n0 + c;
-      g.h_hi[at] = hi;
-      g.h_lo[at] = lo;
+      uint16_t* out = g.h + static_cast<int64_t>(row) * g.f + n0 + c;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        const uint16_t v = f32_to_bf16(h);
+        out[p * g.h_apart] = v;
+        h -= bf16_to_f32(v);
+        if (h != h) h = 0.0f;  // what is not finite has no rest
+      }
     }
     __syncthreads();
   }
 }
-static_assert(kGuThreads == kChunkRows * kCols, "a thread per element of h");
+static_assert(kGuThreads >= 16 * kCols, "a thread per element of h");
 
 // ---------------------------------------------------------------------------
-// down and combine: a workgroup takes 16 columns of out.  Its units of work are
-// (expert hit, part of the contraction), dealt to its wavefronts in turn; each
-// leaves its rows' sums in LDS, which one meeting later are weighted and added
-// up in the pairs' order.
+// down and combine: a workgroup takes 16 columns of out.  Its wavefronts share the
+// steps of all the experts hit evenly, each a contiguous range of them; an
+// expert's sums are left in LDS by the wavefront that begins it, those of a
+// wavefront that begins inside one beside them, and one meeting later they are
+// weighted and added up in the pairs' order.
 // ---------------------------------------------------------------------------
 constexpr int kDnWaves = 16, kDnThreads = kDnWaves * kWave;
-constexpr int kSumRows = 576;  // rows of sums in LDS: the pairs' and the tokens', per part
-constexpr int kUnits = 128;    // units to have, so that the wavefronts get about as many each
+constexpr int kEdgeRows = 32;  // rows of an expert that wavefronts may share
 
-template <int KIND>
+// Wavefront w's first step of `total`: a multiple of `grain`.
+__device__ __forceinline__ int first_step(int w, int waves, int total, int grain) {
+  return w * (total / grain) / waves * grain;
+}
+
+template <int KIND, int PARTS, bool MANY, int FR>
 __global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g) {
   using F = Fmt<KIND>;
-  __shared__ float sums[kSumRows][kCols + 4];
-  __shared__ uint32_t bits[kMaxIds / 32];
-  __shared__ uint16_t active[kMaxPairs];
-  __shared__ uint8_t lists[kDnWaves][kMaxPairs];
-  __shared__ int n_active;
+  constexpr int kDnCols = FR * kCols, kDnPitch = kDnCols + 4;
+  constexpr int kPassRows = MANY ? 16 : 8;
+  // sums by pair, then by token (the shared expert's)
+  __shared__ __align__(16) float sums[kMaxPairs + kFewTokens][kDnPitch];
+  __shared__ __align__(16) float edge[kDnWaves][kEdgeRows][kDnPitch];
+  __shared__ FewTable tb;
+  __shared__ float weight[kMaxPairs];
+  __shared__ int inside[kDnWaves];  // which of the experts a wavefront begins inside of, or -1
   const int t = threadIdx.x, lane = t & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(t / kWave);
-  const int n0 = static_cast<int>(blockIdx.x) * kCols;
-  const Ids ids = load_ids(g, lane);
-  mark_experts(ids, bits);
-  if (wv == 0) {
-    uint32_t m = lane < 32 ? bits[lane] : 0u;
-    const int c = __popc(m), inc = scan32(c, lane);
-    for (int at = inc - c; m; m &= m - 1)
-      active[at++] = static_cast<uint16_t>(lane * 32 + __ffs(m) - 1);
-    if (lane == 31) n_active = inc;
-  }
-  __syncthreads();
-  const int pairs = g.T * g.k, n_rows = pairs + (g.shared ? g.T : 0);
-  const int groups = n_active + g.shared;
-  const int turns = (g.f + F::kTurn - 1) / F::kTurn;
-  int parts = 1;
-  while (groups * parts < kUnits && 2 * parts <= turns && 2 * parts * n_rows <= kSumRows) parts *= 2;
-  const int i16 = lane & 15, q = lane >> 4;
-  for (int unit = wv; unit < groups * parts; unit += kDnWaves) {
-    const int grp = unit / parts, part = unit - grp * parts;
-    const bool shared = g.shared && grp == 0;
-    int e = 0, n = g.T;
-    if (!shared) {
-      e = active[grp - g.shared];
-      n = pairs_of(ids, e, lane, lists[wv]);
-    }
-    const int from = part * turns / parts * F::kTurn;
-    const int to = min(g.f, (part + 1) * turns / parts * F::kTurn);
+  const int n0 = static_cast<int>(blockIdx.x) * kDnCols;
+  const int pairs = g.T * g.k;
+  const FewTable* table = static_cast<const FewTable*>(g.table);
+  const int groups = __builtin_amdgcn_readfirstlane(table->n) + g.shared;
+  const int all = (g.f + F::kStep - 1) / F::kStep, total = groups * all;
+  // an expert with more rows than `edge` holds is one wavefront's
+  const int grain = __builtin_amdgcn_readfirstlane(table->most) > kEdgeRows ? all : 1;
+  const int begin = first_step(wv, kDnWaves, total, grain);
+  const int end = first_step(wv + 1, kDnWaves, total, grain);
+
+  const int i8 = lane & 7, half = (lane >> 3) & 1, q = lane >> 4;
+  const uint32_t off = static_cast<uint32_t>(i8 * g.f * F::kElem + half * 64 + q * 16);
+  const int last = g.f % F::kStep ? g.f / F::kStep : -1;
+  auto weights_of = [&](int grp, int e) {
+    const bool shared = grp < g.shared;
     const uint8_t* wbase = static_cast<const uint8_t*>(shared ? g.shared_down : g.down);
     const float* sbase = shared ? g.shared_down_scales : g.down_scales;
-    const uint8_t* wp =
-        wbase + (static_cast<int64_t>(e) * g.d + n0 + i16) * g.f * F::kElem + q * 16;
-    const float* ws = nullptr;
-    if (KIND == kFewE4m3)
-      ws = sbase + (static_cast<int64_t>(e) * ((g.d + kBlock - 1) / kBlock) + n0 / kBlock) *
-                       ((g.f + kBlock - 1) / kBlock);
-    for (int m0 = 0; m0 < n; m0 += kChunkRows) {
+    Weights<FR> r;
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+      const int col = min(n0 + f * kCols, g.d - kCols);  // fragments past out repeat the last
+      r.p[f] = wbase + (static_cast<int64_t>(e) * g.d + col) * g.f * F::kElem;
+      r.scales[f] = KIND != kFewE4m3
+                        ? nullptr
+                        : sbase + (static_cast<int64_t>(e) * ((g.d + kBlock - 1) / kBlock) +
+                                   col / kBlock) * ((g.f + kBlock - 1) / kBlock);
+    }
+    return r;
+  };
+  Loaded<KIND, FR> w;
+  Weights<FR> at;
+  int grp = begin / all, e = 0;
+  if (begin < end) {  // the first weights, ahead of the rest of the table
+    if (grp >= g.shared) e = __builtin_amdgcn_readfirstlane(table->active[grp - g.shared]);
+    at = weights_of(grp, e);
+    w.load(at, off, begin - grp * all, last, half);
+  }
+  for (int i = t; i < static_cast<int>(sizeof(FewTable) / 16); i += kDnThreads)
+    reinterpret_cast<u32x4_t*>(&tb)[i] = reinterpret_cast<const u32x4_t*>(table)[i];
+  if (t < pairs) weight[t] = g.topk_w[t];
+  if (lane == 0) inside[wv] = begin < end && begin > grp * all ? grp : -1;
+  __syncthreads();
+
+  for (int s = begin; s < end; ++grp) {
+    const int from = s - grp * all, to = min(all, from + end - s);
+    s += to - from;
+    const bool shared = grp < g.shared;
+    const int first = shared ? 0 : tb.start[grp - g.shared];
+    const int n = __builtin_amdgcn_readfirstlane(shared ? g.T : tb.start[grp - g.shared + 1] - first);
+    int next_e = e;
+    Weights<FR> next = at;
+    if (s < end) {
+      next_e = __builtin_amdgcn_readfirstlane(tb.active[grp + 1 - g.shared]);
+      next = weights_of(grp + 1, next_e);
+    }
+    const float* sbase = shared ? g.shared_down_scales : g.down_scales;
+    for (int m0 = 0; m0 < n; m0 += kPassRows) {
+      const bool again = m0 + kPassRows < n;  // these weights with other rows
       auto pass = [&](auto nb) {
         constexpr int NB = decltype(nb)::value;
-        Rows<NB, true> rows;
-        f32x4_t acc[NB];
+        f32x4_t acc[FR][NB];
         int row[NB];
+        uint32_t xo[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const int r = m0 + b * 16 + i16;
-          rows.on[b] = r < n;
-          row[b] = r >= n ? 0 : shared ? pairs + r : lists[wv][r];
-          rows.hi[b] = g.h_hi + static_cast<int64_t>(row[b]) * g.f;
-          rows.lo[b] = g.h_lo + static_cast<int64_t>(row[b]) * g.f;
-          acc[b] = f32x4_t{0, 0, 0, 0};
-        }
-        for (int k0 = from; k0 < to; k0 += F::kTurn)
-          turn<KIND, NB, true>(wp, ws, k0, to, q, rows, acc);
-        f32x4_t s{1, 1, 1, 1};
-        if constexpr (KIND == kFewInt8)
-          s = *reinterpret_cast<const f32x4_t*>(sbase + static_cast<int64_t>(e) * g.d + n0 + q * 4);
+          const int r = min(m0 + b * 8 + i8, n - 1);
+          row[b] = shared ? pairs + r : tb.pair[first + r];
+          xo[b] = static_cast<uint32_t>(row[b] * g.f + half * F::kHalf + q * F::kChunk) * 2;
+          
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          if (rows.on[b])
-            *reinterpret_cast<f32x4_t*>(&sums[part * n_rows + row[b]][q * 4]) = acc[b] * s;
+          for (int f = 0; f < FR; ++f) acc[f][b] = f32x4_t{0, 0, 0, 0};
+        }
+        steps<KIND, FR, NB, PARTS>(at, off, w, from, to, g.f, again ? at : next,
+                               again ? from : s < end ? 0 : from,
+                               reinterpret_cast<const uint8_t*>(g.h), xo, g.h_apart * 2, half, acc);
+#pragma unroll
+        for (int f = 0; f < FR; ++f) {
+          f32x4_t sc{1, 1, 1, 1};
+          if constexpr (KIND == kFewInt8)
+            sc = *reinterpret_cast<const f32x4_t*>(sbase + static_cast<int64_t>(e) * g.d +
+                                                   min(n0 + f * kCols, g.d - kCols) + (q & 1) * 4);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const f32x4_t v = both_halves(acc[f][b]) * sc;
+            const int r = m0 + b * 8 + i8;
+            if (owns_sums(lane) && r < n)
+              *reinterpret_cast<f32x4_t*>((from == 0 ? sums[row[b]] : edge[wv][r]) + f * kCols +
+                                          q * 4) = v;
+          }
+        }
       };
-      if (n - m0 > 16)
-        pass(std::integral_constant<int, 2>{});
-      else
+      if constexpr (MANY) {
+        if (n - m0 > 8)
+          pass(std::integral_constant<int, 2>{});
+        else
+          pass(std::integral_constant<int, 1>{});
+      } else {
         pass(std::integral_constant<int, 1>{});
+      }
     }
+    at = next;
+    e = next_e;
   }
   __syncthreads();
-  for (int o = t; o < g.T * kCols; o += kDnThreads) {
-    const int tok = o / kCols, c = o % kCols;
+  // what wavefronts that began inside an expert hold of it
+  for (int o = t; o < (pairs + (g.shared ? g.T : 0)) * kDnCols; o += kDnThreads) {
+    const int row = o / kDnCols, c = o % kDnCols;
+    if (row < pairs && !tb.valid[row]) continue;
+    const int grp = row < pairs ? tb.group[row] + g.shared : 0;
+    const int rank = row < pairs ? tb.rank[row] : row - pairs;
+    float y = sums[row][c];
+#pragma unroll
+    for (int w = 1; w < kDnWaves; ++w)
+      if (inside[w] == grp) y += edge[w][rank][c];
+    sums[row][c] = y;
+  }
+  __syncthreads();
+  for (int o = t; o < g.T * kDnCols; o += kDnThreads) {
+    const int tok = o / kDnCols, c = o % kDnCols;
+    if (n0 + c >= g.d) continue;
     float v = 0.0f;
-    auto whole = [&](int row) {
-      float y = sums[row][c];
-      for (int p = 1; p < parts; ++p) y += sums[p * n_rows + row][c];
-      return y;
-    };
+#pragma unroll 4
     for (int j = 0; j < g.k; ++j) {
-      const int s = tok * g.k + j, id = g.topk_idx[s];
-      if (id >= 0 && id < g.E) v = fmaf(g.topk_w[s], whole(s), v);
+      const int s = tok * g.k + j;
+      if (tb.valid[s]) v = fmaf(weight[s], sums[s][c], v);
     }
-    if (g.shared) v += whole(pairs + tok);
+    if (g.shared) v += sums[pairs + tok][c];
     const int64_t at = static_cast<int64_t>(tok) * g.d + n0 + c;
     if (g.out_f32)
       static_cast<float*>(g.out)[at] = v;
@@ -418,22 +613,41 @@ __global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g) {
       static_cast<uint16_t*>(g.out)[at] = f32_to_bf16(v);
   }
 }
+static_assert(kMaxPairs <= 8 * kWave, "a thread per pair");
 
-template <int KIND>
+// Fragments of a wavefront of few_down: as many workgroups as there are CUs.
+int down_frags(int d) { return (d / kCols + kCus - 1) / kCus; }
+
+template <int KIND, int PARTS, bool MANY>
 hipError_t go(const FewLayer& g, hipStream_t stream) {
   const int pairs = g.T * g.k, tiles = g.f / kCols;
   const int slots = (pairs < g.E ? pairs : g.E) + g.shared;
-  const hipError_t e = launch(few_gate_up<KIND>, dim3(static_cast<uint32_t>(slots * tiles)),
+  const hipError_t e = launch(few_gate_up<KIND, PARTS, MANY>, dim3(static_cast<uint32_t>(slots * tiles + 1)),
                               dim3(kGuThreads), 0, stream, g, tiles);
   if (e != hipSuccess) return e;
-  return launch(few_down<KIND>, dim3(static_cast<uint32_t>(g.d / kCols)), dim3(kDnThreads), 0,
-                stream, g);
+  auto down = [&](auto fr) {
+    constexpr int FR = decltype(fr)::value;
+    return launch(few_down<KIND, PARTS, MANY, FR>,
+                  dim3(static_cast<uint32_t>((g.d / kCols + FR - 1) / FR)), dim3(kDnThreads), 0,
+                  stream, g);
+  };
+  switch (down_frags(g.d)) {
+    case 1: return down(std::integral_constant<int, 1>{});
+    case 2: return down(std::integral_constant<int, 2>{});
+    case 3: return down(std::integral_constant<int, 3>{});
+    default: return down(std::integral_constant<int, 4>{});
+  }
+}
+template <int KIND>
+hipError_t go(const FewLayer& g, hipStream_t stream) {
+  if (g.T > 8) return g.out_f32 ? go<KIND, 3, true>(g, stream) : go<KIND, 2, true>(g, stream);
+  return g.out_f32 ? go<KIND, 3, false>(g, stream) : go<KIND, 2, false>(g, stream);
 }
 
 }  // namespace
 
 size_t few_workspace(int T, int k, int f, bool shared) {
-  return static_cast<size_t>(T) * (k + shared) * f * 2 * sizeof(uint16_t);
+  return kFewTableBytes + static_cast<size_t>(T) * (k + shared) * f * 3 * sizeof(uint16_t);
 }
 
 hipError_t launch_layer_few(const FewLayer& g, FewKind kind, hipStream_t stream) {
