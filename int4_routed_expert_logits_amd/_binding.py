@@ -848,30 +848,41 @@ class AdamWTensors:
         self.device = params[0].get_device() if n else -1
         self.array = (AdamWTensor * n)()
         self.n = n
-        spans = []
+        spans, dev = [], self.device
+        bf16, byte = _T[0][0], codes[1:]
+
+        def take(name, i, t, dtypes, shape, count):
+            """t's address, checked, of `count` elements; its span is kept."""
+            dt = t.dtype
+            if not (dt in dtypes and t.shape == shape and t.get_device() == dev and
+                    t.is_contiguous()):
+                _take(fn, dev, f"{name}[{i}]", t, dtypes, shape)  # raises
+            at = t.data_ptr()
+            if count:
+                spans.append((at, at + count * dt.itemsize, name != "grads", i))
+            return at
+
         for i, (p, w, g, a, b, sa, sb) in enumerate(zip(*lists)):
             for name, t in (("params", p), ("grads", g), ("m", a), ("v", b)):
                 if t is None:
                     raise ValueError(f"{fn}: {name}[{i}] is missing")
             if (sa is None) != (sb is None):
                 raise ValueError(f"{fn}: only one of m_scales[{i}] and v_scales[{i}] is given")
-            if w is not None and p.dtype != (_T or _types())[0][0]:
-                raise TypeError(f"{fn}: masters[{i}] stands beside a parameter of {p.dtype}")
-            s = self.array[i]
-            take = lambda name, t, dt, size: _take(fn, self.device, f"{name}[{i}]", t, dt,  # noqa: E731
-                                                   size)
-            s.n = p.numel()
-            blocks = (-(-s.n // 256),)
-            s.p, s.p_dt = take("params", p, floats, p.shape), _code(p.dtype)
-            s.master = take("masters", w, f32, p.shape)
-            s.g, s.g_dt = take("grads", g, floats, p.shape), _code(g.dtype)
-            s.m = take("m", a, f32 if sa is None else codes, p.shape)
-            s.v = take("v", b, f32 if sa is None else codes[1:], p.shape)
-            s.m_scales = take("m_scales", sa, f32, blocks)
-            s.v_scales = take("v_scales", sb, f32, blocks)
-            for t, written in ((p, 1), (w, 1), (g, 0), (a, 1), (b, 1), (sa, 1), (sb, 1)):
-                if t is not None and t.numel():
-                    spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), written, i))
+            shape, s = p.shape, self.array[i]
+            s.n = count = p.numel()
+            s.p, s.p_dt = take("params", i, p, floats, shape, count), _code(p.dtype)
+            s.g, s.g_dt = take("grads", i, g, floats, shape, count), _code(g.dtype)
+            if w is not None:
+                if p.dtype != bf16:
+                    raise TypeError(f"{fn}: masters[{i}] stands beside a parameter of {p.dtype}")
+                s.master = take("masters", i, w, f32, shape, count)
+            if sa is None:
+                s.m, s.v = take("m", i, a, f32, shape, count), take("v", i, b, f32, shape, count)
+            else:
+                blocks = (-(-count // 256),)
+                s.m, s.v = take("m", i, a, codes, shape, count), take("v", i, b, byte, shape, count)
+                s.m_scales = take("m_scales", i, sa, f32, blocks, blocks[0])
+                s.v_scales = take("v_scales", i, sb, f32, blocks, blocks[0])
         # two spans overlap only if one of them does with the one that reaches
         # furthest among those that begin before it: of the written and of all
         end = [(0, -1), (0, -1)]

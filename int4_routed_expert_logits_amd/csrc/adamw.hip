@@ -16,10 +16,14 @@
 // that is not zero never gets code 0: m, whose codes reach further down, would
 // then be divided by eps alone.
 //
-// Bound by memory: a wavefront takes blocks of 256 elements, 4 of each lane, and
-// reads several of them before it works on the first.  The tensors' addresses
-// are kernel arguments (a batch of them a launch): nothing is kept on the device,
-// and a captured launch holds them.
+// Bound by memory: 402M elements of bf16 with masters take 2.25 ms (30 bytes each,
+// 5.4 TB/s), with 8-bit moments 1.37 (18 bytes, 5.3); few elements by the launch
+// (16 vectors of 6144: 3.5 us).  A wavefront takes one block of 256 elements, 4 of
+// each lane: with so many wavefronts in flight, four blocks each before the
+// first is worked on gain nothing (2.26 and 1.41 ms), and starve where there are
+// few (90 odd tensors, 2.9M elements: 28 us, so 17).  The tensors' addresses are
+// kernel arguments, up to 64 tensors a launch: nothing is kept on the device, and
+// a captured launch holds them.
 #include "common.h"
 #include "launch.h"
 
@@ -37,11 +41,52 @@ constexpr uint32_t kMaxGrid = 1u << 22;
 
 enum Store { kF32, kBf16, kMaster };  // the parameter: float32, bf16, bf16 with a float32 master
 
+// The tensors of a launch, by what their kind has of addresses: as many as the
+// 4 KB of a launch's arguments hold, and a wavefront's lanes.
+template <bool B8, int P>
 struct Batch {
-  AdamWTensor t[kAdamWBatch];
-  uint32_t first[kAdamWBatch + 1];  // each tensor's first chunk; the last: how many there are
+  static constexpr int kPtrs = 4 + (P == kMaster) + 2 * B8;
+  static constexpr int kFit = (4096 - 128) / (8 * (kPtrs + 1) + 4);
+  static constexpr int kMost = kFit < kWave ? kFit : kWave;
+  struct Slot {
+    uint64_t size;  // elements, and whether all its arrays are aligned for four at once
+    void* at[kPtrs];
+  };
+  Slot t[kMost];
+  uint32_t first[kMost + 1];  // each tensor's first chunk; the last: how many there are
   int n;
   AdamWStep s;
+  void add(const AdamWTensor& q, uint32_t chunks) {
+    Slot& x = t[n];
+    x.size = static_cast<uint64_t>(q.n) << 1 | q.wide;
+    x.at[0] = q.p;
+    x.at[1] = const_cast<void*>(q.g);
+    x.at[2] = q.m;
+    x.at[3] = q.v;
+    if constexpr (P == kMaster) x.at[4] = q.master;
+    if constexpr (B8) {
+      x.at[kPtrs - 2] = q.m_scales;
+      x.at[kPtrs - 1] = q.v_scales;
+    }
+    first[n + 1] = first[n] + chunks;
+    ++n;
+  }
+  __device__ __forceinline__ AdamWTensor get(int i) const {
+    const Slot& x = t[i];
+    AdamWTensor q{};
+    q.n = static_cast<int64_t>(x.size >> 1);
+    q.wide = x.size & 1;
+    q.p = x.at[0];
+    q.g = x.at[1];
+    q.m = x.at[2];
+    q.v = x.at[3];
+    if constexpr (P == kMaster) q.master = x.at[4];
+    if constexpr (B8) {
+      q.m_scales = static_cast<float*>(x.at[kPtrs - 2]);
+      q.v_scales = static_cast<float*>(x.at[kPtrs - 1]);
+    }
+    return q;
+  }
 };
 
 __device__ __forceinline__ float two_to(int n) {
@@ -51,13 +96,14 @@ __device__ __forceinline__ bool finite(float v) {
   return (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
 }
 
-// Elements i .. i + 3 of an array of n; `wide`: it is aligned for one access.
-template <class T>
-__device__ __forceinline__ void load4(const T* p, int64_t i, int64_t n, bool wide, T (&v)[kV]) {
+// Elements i .. i + 3 of an array of n.  WHOLE: all of them are there, and the
+// address is aligned for one access.
+template <bool WHOLE, class T>
+__device__ __forceinline__ void load4(const T* p, int64_t i, int64_t n, T (&v)[kV]) {
   struct alignas(sizeof(T) * kV) Pack {
     T v[kV];
   };
-  if (wide && i + kV <= n) {
+  if constexpr (WHOLE) {
     const Pack q = *reinterpret_cast<const Pack*>(p + i);
 #pragma unroll
     for (int j = 0; j < kV; ++j) v[j] = q.v[j];
@@ -66,12 +112,12 @@ __device__ __forceinline__ void load4(const T* p, int64_t i, int64_t n, bool wid
     for (int j = 0; j < kV; ++j) v[j] = i + j < n ? p[i + j] : T(0);
   }
 }
-template <class T>
-__device__ __forceinline__ void store4(T* p, int64_t i, int64_t n, bool wide, const T (&v)[kV]) {
+template <bool WHOLE, class T>
+__device__ __forceinline__ void store4(T* p, int64_t i, int64_t n, const T (&v)[kV]) {
   struct alignas(sizeof(T) * kV) Pack {
     T v[kV];
   };
-  if (wide && i + kV <= n) {
+  if constexpr (WHOLE) {
     Pack q;
 #pragma unroll
     for (int j = 0; j < kV; ++j) q.v[j] = v[j];
@@ -81,12 +127,6 @@ __device__ __forceinline__ void store4(T* p, int64_t i, int64_t n, bool wide, co
     for (int j = 0; j < kV; ++j)
       if (i + j < n) p[i + j] = v[j];
   }
-}
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  for (int off = kWave / 2; off > 0; off >>= 1)
-    v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), off, kWave)));
-  return v;
 }
 
 // Exponent n of the smallest scale 2^n >= 2^-126 with top <= limit * 2^n, limit =
@@ -107,8 +147,112 @@ struct Loaded {
   float ms, vs;
 };
 
-template <bool B8, int P, bool GBF16, int U>
-__global__ __launch_bounds__(kThreads) void adamw_step(const Batch b) {
+// The block from element `from` on.
+template <bool B8, int P, bool GBF16, bool WHOLE>
+__device__ __forceinline__ void update(const AdamWTensor& q, const AdamWStep& h, float size,
+                                       float root, float gs, int64_t from, int lane) {
+  const int64_t n = q.n;
+  const int64_t i = from + lane * kV, blk = from / kBlock;
+  Loaded<B8, P, GBF16> x;
+  if (P == kF32) load4<WHOLE>(static_cast<const float*>(q.p), i, n, x.p32);
+  if (P == kBf16) load4<WHOLE>(static_cast<const uint16_t*>(q.p), i, n, x.p16);
+  if (P == kMaster) load4<WHOLE>(static_cast<const float*>(q.master), i, n, x.p32);
+  if (GBF16)
+    load4<WHOLE>(static_cast<const uint16_t*>(q.g), i, n, x.g16);
+  else
+    load4<WHOLE>(static_cast<const float*>(q.g), i, n, x.g32);
+  if (B8) {
+    load4<WHOLE>(static_cast<const uint8_t*>(q.m), i, n, x.mc);
+    load4<WHOLE>(static_cast<const uint8_t*>(q.v), i, n, x.vc);
+    x.ms = q.m_scales[blk];
+    x.vs = q.v_scales[blk];
+  } else {
+    load4<WHOLE>(static_cast<const float*>(q.m), i, n, x.m32);
+    load4<WHOLE>(static_cast<const float*>(q.v), i, n, x.v32);
+  }
+  float m[kV], v[kV], r[kV], p[kV];
+  if (B8) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) w |= static_cast<uint32_t>(x.mc[j]) << (8 * j);
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
+    m[0] = lo[0] * x.ms; m[1] = lo[1] * x.ms;
+    m[2] = hi[0] * x.ms; m[3] = hi[1] * x.ms;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      const int code = x.vc[j], e = max((code >> 5) - 1, 0);
+      const float s = static_cast<float>((code - 32 * e) << e) * x.vs;
+      v[j] = s * s;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      m[j] = x.m32[j];
+      v[j] = x.v32[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    float g = GBF16 ? bf16_to_f32(x.g16[j]) : x.g32[j];
+    g = g * gs;
+    m[j] = m[j] * h.beta1 + g * h.rest1;
+    v[j] = v[j] * h.beta2 + g * g * h.rest2;
+    r[j] = sqrtf(v[j]);
+    p[j] = P == kBf16 ? bf16_to_f32(x.p16[j]) : x.p32[j];
+    p[j] = p[j] * h.keep - m[j] / (r[j] * root + h.eps) * size;
+  }
+  if (P != kF32) {
+    uint16_t half[kV];
+#pragma unroll
+    for (int j = 0; j < kV; ++j) half[j] = f32_to_bf16(p[j]);
+    store4<WHOLE>(static_cast<uint16_t*>(q.p), i, n, half);
+  }
+  if (P != kBf16) store4<WHOLE>(static_cast<float*>(P == kMaster ? q.master : q.p), i, n, p);
+  if (B8) {
+    uint32_t top_m = 0, top_r = 0;
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+      if (WHOLE || i + j < n) {
+        if (finite(m[j])) top_m = max(top_m, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+        top_r = max(top_r, __float_as_uint(r[j]) & 0x7FFFFFFFu);
+      }
+    top_m = wave_max_u32(top_m);
+    top_r = wave_max_u32(top_r);
+    const int em = scale_exponent(top_m, 0x600000u, 8);   // 448 = 1.75 * 2^8
+    const int er = scale_exponent(top_r, 0x7C0000u, 11);  // 4032 = 1.96875 * 2^11
+    const bool ok = top_r < 0x7F800000u;
+    const float im = two_to(-em), ir = ok ? two_to(-er) : 0.0f;
+    uint8_t mc[kV], vc[kV];
+    float a[kV];
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      a[j] = finite(m[j]) ? m[j] * im : __uint_as_float(0x7FC00000u);
+      const float s = ok ? r[j] * ir : 0.0f;
+      const int e = max(static_cast<int>(__float_as_uint(s) >> 23) - 126 - 6, 0);
+      const int code = 32 * e + static_cast<int>(rintf(s * two_to(-e)));
+      vc[j] = static_cast<uint8_t>(r[j] > 0.0f ? max(code, 1) : code);
+    }
+    int w = 0;
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(a[0], a[1], w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(a[2], a[3], w, true);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) mc[j] = static_cast<uint8_t>(w >> (8 * j));
+    store4<WHOLE>(static_cast<uint8_t*>(q.m), i, n, mc);
+    store4<WHOLE>(static_cast<uint8_t*>(q.v), i, n, vc);
+    if (lane == 0) {
+      q.m_scales[blk] = two_to(em);
+      q.v_scales[blk] = ok ? two_to(er) : __uint_as_float(0x7FC00000u);
+    }
+  } else {
+    store4<WHOLE>(static_cast<float*>(q.m), i, n, m);
+    store4<WHOLE>(static_cast<float*>(q.v), i, n, v);
+  }
+}
+
+template <bool B8, int P, bool GBF16>
+__global__ __launch_bounds__(kThreads) void adamw_step(const Batch<B8, P> b) {
+  static_assert(sizeof(b) <= 4096, "a launch's arguments");
   const int lane = threadIdx.x & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t my_first = b.first[min(lane, b.n)];
@@ -120,179 +264,60 @@ __global__ __launch_bounds__(kThreads) void adamw_step(const Batch b) {
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     // the last tensor whose first chunk is not behind c
     const int at = __popcll(__ballot(lane < b.n && my_first <= c)) - 1;
-    const AdamWTensor q = b.t[at];
-    const int64_t n = q.n;
-    const bool wide = q.wide;
-    const int64_t from =
-        (static_cast<int64_t>(c - b.first[at]) * (kWaves * U) + wv * U) * kBlock + lane * kV;
-    Loaded<B8, P, GBF16> x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = from + u * kBlock;
-      if (P == kF32) load4(static_cast<const float*>(q.p), i, n, wide, x[u].p32);
-      if (P == kBf16) load4(static_cast<const uint16_t*>(q.p), i, n, wide, x[u].p16);
-      if (P == kMaster) load4(static_cast<const float*>(q.master), i, n, wide, x[u].p32);
-      if (GBF16)
-        load4(static_cast<const uint16_t*>(q.g), i, n, wide, x[u].g16);
-      else
-        load4(static_cast<const float*>(q.g), i, n, wide, x[u].g32);
-      if (B8) {
-        load4(static_cast<const uint8_t*>(q.m), i, n, wide, x[u].mc);
-        load4(static_cast<const uint8_t*>(q.v), i, n, wide, x[u].vc);
-        const int64_t blk = (from - lane * kV) / kBlock + u;
-        const bool in = blk * kBlock < n;
-        x[u].ms = in ? q.m_scales[blk] : 0.0f;
-        x[u].vs = in ? q.v_scales[blk] : 0.0f;
-      } else {
-        load4(static_cast<const float*>(q.m), i, n, wide, x[u].m32);
-        load4(static_cast<const float*>(q.v), i, n, wide, x[u].v32);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = from + u * kBlock;
-      float m[kV], v[kV], r[kV], p[kV];
-      if (B8) {
-        uint32_t w = 0;
-#pragma unroll
-        for (int j = 0; j < kV; ++j) w |= static_cast<uint32_t>(x[u].mc[j]) << (8 * j);
-        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
-        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
-        m[0] = lo[0] * x[u].ms; m[1] = lo[1] * x[u].ms;
-        m[2] = hi[0] * x[u].ms; m[3] = hi[1] * x[u].ms;
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          const int code = x[u].vc[j], e = max((code >> 5) - 1, 0);
-          const float s = static_cast<float>((code - 32 * e) << e) * x[u].vs;
-          v[j] = s * s;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          m[j] = x[u].m32[j];
-          v[j] = x[u].v32[j];
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        float g = GBF16 ? bf16_to_f32(x[u].g16[j]) : x[u].g32[j];
-        g = g * gs;
-        m[j] = m[j] * b.s.beta1 + g * b.s.rest1;
-        v[j] = v[j] * b.s.beta2 + g * g * b.s.rest2;
-        r[j] = sqrtf(v[j]);
-        p[j] = P == kBf16 ? bf16_to_f32(x[u].p16[j]) : x[u].p32[j];
-        p[j] = p[j] * b.s.keep - m[j] / (r[j] * root + b.s.eps) * size;
-      }
-      if (P != kF32) {
-        uint16_t h[kV];
-#pragma unroll
-        for (int j = 0; j < kV; ++j) h[j] = f32_to_bf16(p[j]);
-        store4(static_cast<uint16_t*>(q.p), i, n, wide, h);
-      }
-      if (P != kBf16) store4(static_cast<float*>(P == kMaster ? q.master : q.p), i, n, wide, p);
-      if (B8) {
-        uint32_t top_m = 0, top_r = 0;
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-          if (i + j < n) {
-            if (finite(m[j])) top_m = max(top_m, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-            top_r = max(top_r, __float_as_uint(r[j]) & 0x7FFFFFFFu);
-          }
-        top_m = wave_max(top_m);
-        top_r = wave_max(top_r);
-        const int em = scale_exponent(top_m, 0x600000u, 8);   // 448 = 1.75 * 2^8
-        const int er = scale_exponent(top_r, 0x7C0000u, 11);  // 4032 = 1.96875 * 2^11
-        const bool ok = top_r < 0x7F800000u;
-        const float im = two_to(-em), ir = ok ? two_to(-er) : 0.0f;
-        uint8_t mc[kV], vc[kV];
-        float a[kV];
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          a[j] = finite(m[j]) ? m[j] * im : __uint_as_float(0x7FC00000u);
-          const float s = ok ? r[j] * ir : 0.0f;
-          const int e = max(static_cast<int>(__float_as_uint(s) >> 23) - 126 - 6, 0);
-          const int code = 32 * e + static_cast<int>(rintf(s * two_to(-e)));
-          vc[j] = static_cast<uint8_t>(r[j] > 0.0f ? max(code, 1) : code);
-        }
-        int w = 0;
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(a[0], a[1], w, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(a[2], a[3], w, true);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) mc[j] = static_cast<uint8_t>(w >> (8 * j));
-        store4(static_cast<uint8_t*>(q.m), i, n, wide, mc);
-        store4(static_cast<uint8_t*>(q.v), i, n, wide, vc);
-        const int64_t blk = (from - lane * kV) / kBlock + u;
-        if (lane == 0 && blk * kBlock < n) {
-          q.m_scales[blk] = two_to(em);
-          q.v_scales[blk] = ok ? two_to(er) : __uint_as_float(0x7FC00000u);
-        }
-      } else {
-        store4(static_cast<float*>(q.m), i, n, wide, m);
-        store4(static_cast<float*>(q.v), i, n, wide, v);
-      }
-    }
+    const AdamWTensor q = b.get(at);
+    const int64_t from = (static_cast<int64_t>(c - b.first[at]) * kWaves + wv) * kBlock;
+    if (q.wide && from + kBlock <= q.n)
+      update<B8, P, GBF16, true>(q, b.s, size, root, gs, from, lane);
+    else if (from < q.n)
+      update<B8, P, GBF16, false>(q, b.s, size, root, gs, from, lane);
   }
 }
 
-// Four blocks a wavefront, one where they would not fill the CUs twice.
-constexpr int64_t kFewElements = 2 * 256 * kWaves * 4 * kBlock;
-
+// The tensors of one kind, a batch of them a launch.
 template <bool B8, int P, bool GBF16>
-hipError_t go(const Batch& b, bool few, hipStream_t stream) {
-  const uint32_t chunks = b.first[b.n];
-  const dim3 grid(chunks < kMaxGrid ? chunks : kMaxGrid), block(kThreads);
-  return few ? launch(adamw_step<B8, P, GBF16, 1>, grid, block, 0, stream, b)
-             : launch(adamw_step<B8, P, GBF16, 4>, grid, block, 0, stream, b);
-}
-
-template <bool B8>
-hipError_t go(const Batch& b, int store, bool gbf16, bool few, hipStream_t stream) {
-  switch (store) {
-    case kF32: return gbf16 ? go<B8, kF32, true>(b, few, stream) : go<B8, kF32, false>(b, few, stream);
-    case kBf16:
-      return gbf16 ? go<B8, kBf16, true>(b, few, stream) : go<B8, kBf16, false>(b, few, stream);
-    default:
-      return gbf16 ? go<B8, kMaster, true>(b, few, stream) : go<B8, kMaster, false>(b, few, stream);
+hipError_t go(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t stream) {
+  constexpr int64_t per = kWaves * kBlock;
+  Batch<B8, P> b;
+  b.n = 0;
+  b.first[0] = 0;
+  b.s = s;
+  auto flush = [&]() -> hipError_t {
+    if (b.n == 0) return hipSuccess;
+    const uint32_t chunks = b.first[b.n];
+    const dim3 grid(chunks < kMaxGrid ? chunks : kMaxGrid), block(kThreads);
+    const hipError_t e = launch(adamw_step<B8, P, GBF16>, grid, block, 0, stream, b);
+    b.n = 0;
+    return e;
+  };
+  for (int i = 0; i < n; ++i) {
+    const AdamWTensor t = src.get(src.tensors, i);
+    const int store = t.master ? kMaster : t.p_bf16 ? kBf16 : kF32;
+    if (t.n == 0 || store != P || t.g_bf16 != GBF16 || (t.m_scales != nullptr) != B8) continue;
+    const int64_t chunks = (t.n + per - 1) / per;
+    if (b.n == b.kMost || (b.n > 0 && b.first[b.n] + chunks > INT32_MAX)) {
+      const hipError_t e = flush();
+      if (e != hipSuccess) return e;
+    }
+    b.add(t, static_cast<uint32_t>(chunks));
   }
+  return flush();
+}
+template <bool B8, int P>
+hipError_t go(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t stream) {
+  const hipError_t e = go<B8, P, false>(src, n, s, stream);
+  return e != hipSuccess ? e : go<B8, P, true>(src, n, s, stream);
 }
 
 }  // namespace
 
 // Tensors of one kind (how the parameter, its gradient and its moments are held)
-// share launches, up to kAdamWBatch at a time.
+// share launches.
 hipError_t launch_adamw(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t stream) {
-  int64_t total = 0;
-  for (int i = 0; i < n; ++i) total += src.get(src.tensors, i).n;
-  const bool few = total < kFewElements;
-  const int64_t per = static_cast<int64_t>(kWaves) * (few ? 1 : 4) * kBlock;
-  for (int kind = 0; kind < 12; ++kind) {
-    Batch b;
-    b.n = 0;
-    b.first[0] = 0;
-    b.s = s;
-    auto flush = [&]() -> hipError_t {
-      if (b.n == 0) return hipSuccess;
-      const int store = kind >> 2;
-      const bool b8 = kind & 1, gbf16 = kind & 2;
-      const hipError_t e = b8 ? go<true>(b, store, gbf16, few, stream)
-                              : go<false>(b, store, gbf16, few, stream);
-      b.n = 0;
-      return e;
-    };
-    for (int i = 0; i < n; ++i) {
-      const AdamWTensor t = src.get(src.tensors, i);
-      const int store = t.master ? kMaster : t.p_bf16 ? kBf16 : kF32;
-      if (t.n == 0 || (store << 2 | t.g_bf16 << 1 | (t.m_scales != nullptr)) != kind) continue;
-      const int64_t chunks = (t.n + per - 1) / per;
-      if (b.n == kAdamWBatch || (b.n > 0 && b.first[b.n] + chunks > INT32_MAX)) {
-        const hipError_t e = flush();
-        if (e != hipSuccess) return e;
-      }
-      b.t[b.n] = t;
-      b.first[b.n + 1] = b.first[b.n] + static_cast<uint32_t>(chunks);
-      ++b.n;
-    }
-    const hipError_t e = flush();
+  hipError_t (*const kinds[])(const AdamWSource&, int, const AdamWStep&, hipStream_t) = {
+      go<false, kF32>, go<false, kBf16>, go<false, kMaster>,
+      go<true, kF32>, go<true, kBf16>, go<true, kMaster>};
+  for (auto kind : kinds) {
+    const hipError_t e = kind(src, n, s, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

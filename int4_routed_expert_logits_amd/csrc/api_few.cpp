@@ -33,6 +33,10 @@ moe_status check_weights(const moe_expert_weights& w, moe_weights kind) {
   return MOE_OK;
 }
 
+moe::FewScratch scratch_of(const moe_shape* s, int32_t T) {
+  return moe::few_scratch(T, s->top_k, s->d, s->f, s->n_experts, s->f_shared != 0);
+}
+
 }  // namespace
 
 extern "C" {
@@ -40,7 +44,7 @@ extern "C" {
 size_t moe_layer_few_workspace_bytes(const moe_shape* shape, int32_t T) {
   if (check_sizes(shape, T) != MOE_OK || T == 0) return 0;
   return moe_route_workspace_bytes(shape, T) +
-         moe::round_up(moe::few_workspace(T, shape->top_k, shape->f, shape->f_shared != 0));
+         moe::round_up(scratch_of(shape, T).bytes);
 }
 
 moe_status moe_layer_few(const moe_shape* shape, int32_t T, const void* x, const float* w_router,
@@ -86,7 +90,8 @@ moe_status moe_layer_few(const moe_shape* shape, int32_t T, const void* x, const
   }
   uint8_t* scratch = static_cast<uint8_t*>(workspace) + moe_route_workspace_bytes(shape, T);
   g.table = scratch;
-  g.h = reinterpret_cast<uint16_t*>(scratch + moe::kFewTableBytes);
+  g.h = reinterpret_cast<uint16_t*>(scratch + scratch_of(shape, T).h);
+  g.parts = reinterpret_cast<float*>(scratch + scratch_of(shape, T).parts);
   g.h_apart = static_cast<int64_t>(T) * (g.k + g.shared) * g.f;
   g.out = out;
   g.out_f32 = out_dt == MOE_F32;

@@ -170,14 +170,17 @@ struct FewLayer {
   void* table;      // kFewTableBytes, 16-byte aligned
   uint16_t* h;      // h as a sum of two or three bf16 parts, each [T * k (+ T)][f]
   int64_t h_apart;  // from one part to the next
+  float* parts;     // sums of a narrow out's splits
   void* out;
   bool out_f32;
 };
-size_t few_workspace(int T, int k, int f, bool shared);
+struct FewScratch {
+  size_t h, parts, bytes;  // where they begin (the table does at 0), and all of it
+};
+FewScratch few_scratch(int T, int k, int d, int f, int E, bool shared);
 hipError_t launch_layer_few(const FewLayer& g, FewKind kind, hipStream_t stream);
 
 // adamw.hip: one optimiser step over many tensors.
-constexpr int kAdamWBatch = 40;   // tensors a launch
 constexpr int kAdamWBlock = 256;  // elements per scale of 8-bit moments
 struct AdamWTensor {
   int64_t n;

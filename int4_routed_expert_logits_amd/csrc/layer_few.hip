@@ -34,6 +34,9 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
+#ifndef SS
+#define SS 4
+#endif
 constexpr int kCols = 8;      // weight rows (output columns) of a fragment
 constexpr int kBlock = 128;   // rows and columns per scale of e4m3 codes
 constexpr int kMaxPairs = 256, kMaxIds = 1024, kCus = 256;
@@ -463,11 +466,11 @@ constexpr int kEdgeRows = 32;  // rows of an expert that wavefronts may share
 
 // Wavefront w's first step of `total`: a multiple of `grain`.
 __device__ __forceinline__ int first_step(int w, int waves, int total, int grain) {
-  return w * (total / grain) / waves * grain;
+  return static_cast<int>(static_cast<int64_t>(w) * (total / grain) / waves) * grain;
 }
 
 template <int KIND, int PARTS, bool MANY, int FR>
-__global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g) {
+__global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g, int splits) {
   using F = Fmt<KIND>;
   constexpr int kDnCols = FR * kCols, kDnPitch = kDnCols + 4;
   constexpr int kPassRows = MANY ? 16 : 8;
@@ -486,8 +489,12 @@ __global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g) {
   const int all = (g.f + F::kStep - 1) / F::kStep, total = groups * all;
   // an expert with more rows than `edge` holds is one wavefront's
   const int grain = __builtin_amdgcn_readfirstlane(table->most) > kEdgeRows ? all : 1;
-  const int begin = first_step(wv, kDnWaves, total, grain);
-  const int end = first_step(wv + 1, kDnWaves, total, grain);
+  const int split = blockIdx.y, waves = splits * kDnWaves;
+  const int begin = first_step(split * kDnWaves + wv, waves, total, grain);
+  const int end = first_step(split * kDnWaves + wv + 1, waves, total, grain);
+  // this workgroup's steps: it holds the sums of the experts that begin here
+  const int wg_begin = first_step(split * kDnWaves, waves, total, grain);
+  const int wg_end = first_step((split + 1) * kDnWaves, waves, total, grain);
 
   const int i8 = lane & 7, half = (lane >> 3) & 1, q = lane >> 4;
   const uint32_t off = static_cast<uint32_t>(i8 * g.f * F::kElem + half * 64 + q * 16);
@@ -589,9 +596,9 @@ __global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g) {
     if (row < pairs && !tb.valid[row]) continue;
     const int grp = row < pairs ? tb.group[row] + g.shared : 0;
     const int rank = row < pairs ? tb.rank[row] : row - pairs;
-    float y = sums[row][c];
+    float y = grp * all >= wg_begin && grp * all < wg_end ? sums[row][c] : 0.0f;
 #pragma unroll
-    for (int w = 1; w < kDnWaves; ++w)
+    for (int w = 0; w < kDnWaves; ++w)
       if (inside[w] == grp) y += edge[w][rank][c];
     sums[row][c] = y;
   }
@@ -607,16 +614,45 @@ __global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g) {
     }
     if (g.shared) v += sums[pairs + tok][c];
     const int64_t at = static_cast<int64_t>(tok) * g.d + n0 + c;
-    if (g.out_f32)
+    if (splits > 1)
+      g.parts[split * g.T * g.d + at] = v;
+    else if (g.out_f32)
       static_cast<float*>(g.out)[at] = v;
     else
       static_cast<uint16_t*>(g.out)[at] = f32_to_bf16(v);
   }
 }
-static_assert(kMaxPairs <= 8 * kWave, "a thread per pair");
+static_assert(kMaxPairs <= kDnThreads, "a thread per pair");
+
+// out = the splits' sum, in their order.
+__global__ __launch_bounds__(256) void few_join(FewLayer g, int splits) {
+  const int n = g.T * g.d, i = static_cast<int>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n) return;
+  float v = g.parts[i];
+#pragma unroll 4
+  for (int z = 1; z < splits; ++z) v += g.parts[z * n + i];
+  if (g.out_f32)
+    static_cast<float*>(g.out)[i] = v;
+  else
+    static_cast<uint16_t*>(g.out)[i] = f32_to_bf16(v);
+}
 
 // Fragments of a wavefront of few_down: as many workgroups as there are CUs.
 int down_frags(int d) { return (d / kCols + kCus - 1) / kCus; }
+
+// Where out is too narrow for that, the steps are split over workgroups too, and
+// a third kernel joins their sums: as many as fill the CUs and leave a wavefront
+// kSplitSteps steps if every pair has an expert of its own.
+constexpr int kMaxSplits = 16, kSplitSteps = SS;
+int down_splits(int T, int k, int d, int f, int E, bool shared, int step) {
+  const int tiles = d / kCols, pairs = T * k;
+  const int64_t steps = static_cast<int64_t>((pairs < E ? pairs : E) + shared) * ((f + step - 1) / step);
+  const int64_t most = steps / (kDnWaves * kSplitSteps);
+  int s = kCus / tiles;
+  if (s > most) s = static_cast<int>(most);
+  if (s > kMaxSplits) s = kMaxSplits;
+  return s > 1 ? s : 1;
+}
 
 template <int KIND, int PARTS, bool MANY>
 hipError_t go(const FewLayer& g, hipStream_t stream) {
@@ -625,12 +661,19 @@ hipError_t go(const FewLayer& g, hipStream_t stream) {
   const hipError_t e = launch(few_gate_up<KIND, PARTS, MANY>, dim3(static_cast<uint32_t>(slots * tiles + 1)),
                               dim3(kGuThreads), 0, stream, g, tiles);
   if (e != hipSuccess) return e;
+  const int splits = down_splits(g.T, g.k, g.d, g.f, g.E, g.shared, Fmt<KIND>::kStep);
   auto down = [&](auto fr) {
     constexpr int FR = decltype(fr)::value;
     return launch(few_down<KIND, PARTS, MANY, FR>,
-                  dim3(static_cast<uint32_t>((g.d / kCols + FR - 1) / FR)), dim3(kDnThreads), 0,
-                  stream, g);
+                  dim3(static_cast<uint32_t>((g.d / kCols + FR - 1) / FR), splits),
+                  dim3(kDnThreads), 0, stream, g, splits);
   };
+  if (splits > 1) {
+    const hipError_t err = down(std::integral_constant<int, 1>{});
+    if (err != hipSuccess) return err;
+    return launch(few_join, dim3(static_cast<uint32_t>((g.T * g.d + 255) / 256)), dim3(256), 0,
+                  stream, g, splits);
+  }
   switch (down_frags(g.d)) {
     case 1: return down(std::integral_constant<int, 1>{});
     case 2: return down(std::integral_constant<int, 2>{});
@@ -646,8 +689,15 @@ hipError_t go(const FewLayer& g, hipStream_t stream) {
 
 }  // namespace
 
-size_t few_workspace(int T, int k, int f, bool shared) {
-  return kFewTableBytes + static_cast<size_t>(T) * (k + shared) * f * 3 * sizeof(uint16_t);
+// The grouping, h, and the splits' sums (by the smaller step of the two: more splits).
+FewScratch few_scratch(int T, int k, int d, int f, int E, bool shared) {
+  FewScratch s;
+  s.h = kFewTableBytes;
+  const size_t h = static_cast<size_t>(T) * (k + shared) * f * 3 * sizeof(uint16_t);
+  s.parts = (s.h + h + 15) / 16 * 16;
+  const int splits = down_splits(T, k, d, f, E, shared, Fmt<kFewBf16>::kStep);
+  s.bytes = s.parts + (splits > 1 ? static_cast<size_t>(splits) * T * d * sizeof(float) : 0);
+  return s;
 }
 
 hipError_t launch_layer_few(const FewLayer& g, FewKind kind, hipStream_t stream) {

@@ -11,6 +11,8 @@
 // 64-token x 128-expert tiles.  Every product x*w is exact in float64 (bf16 or fp32
 // times fp32), so only the summation order can differ from any other
 // float64 evaluation, and that order is fixed for a given batch-size class.
+#include <type_traits>
+
 #include "common.h"
 #include "launch.h"
 #include "topk_wave.h"
@@ -37,19 +39,20 @@ __device__ __forceinline__ void load_x4(const void* x, size_t idx, float (&v)[4]
 // Small batches: one wavefront per (expert, part of d).  Spreading each
 // router row over P parts puts E*P wavefronts in flight, enough to stream the
 // router matrix at HBM rate; every wavefront keeps up to 8 tokens' float64
-// sums and writes part[t][e][p] (tree-summed over its lanes).
+// sums and writes part[t][e][p] (tree-summed over its lanes); more tokens are
+// other wavefronts'.
 constexpr int kTokGroup = 8;
 constexpr int kSplitMaxT = 32;  // larger batches use the matrix-core kernel
 
-// Partial float64 sums of tokens t0 .. t0+kTokGroup-1 against router row e
+// Partial float64 sums of tokens t0 .. t0+TG-1 against router row e
 // over columns [i0, i1), each lane its strided share.
-template <bool XBF16>
+template <bool XBF16, int TG>
 __device__ __forceinline__ void logits_part(const void* __restrict__ x, const float* __restrict__ w,
                                             int T, int d, int e, int i0, int i1, int t0, int lane,
-                                            double (&acc)[kTokGroup]) {
+                                            double (&acc)[TG]) {
   const float* wr = w + static_cast<size_t>(e) * d;
 #pragma unroll
-  for (int tt = 0; tt < kTokGroup; ++tt) acc[tt] = 0.0;
+  for (int tt = 0; tt < TG; ++tt) acc[tt] = 0.0;
   // four 256-column steps per pass, their router loads issued together
   for (int ib = i0 + lane * 4; ib < i1; ib += 4 * 256) {
     float4 wv[4];
@@ -58,26 +61,28 @@ __device__ __forceinline__ void logits_part(const void* __restrict__ x, const fl
       const int i = ib + u * 256;
       wv[u] = i < i1 ? *reinterpret_cast<const float4*>(wr + i) : make_float4(0, 0, 0, 0);
     }
+    // every token's columns of a step are loaded before any is multiplied (a
+    // token's place past the batch takes the last one's), so a step waits once
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = ib + u * 256;
       if (i >= i1) break;
+      float xv[TG][4];
 #pragma unroll
-      for (int tt = 0; tt < kTokGroup; ++tt) {
-        if (t0 + tt < T) {
-          float xv[4];
-          load_x4<XBF16>(x, static_cast<size_t>(t0 + tt) * d + i, xv);
-          acc[tt] = fma(static_cast<double>(xv[0]), static_cast<double>(wv[u].x), acc[tt]);
-          acc[tt] = fma(static_cast<double>(xv[1]), static_cast<double>(wv[u].y), acc[tt]);
-          acc[tt] = fma(static_cast<double>(xv[2]), static_cast<double>(wv[u].z), acc[tt]);
-          acc[tt] = fma(static_cast<double>(xv[3]), static_cast<double>(wv[u].w), acc[tt]);
-        }
+      for (int tt = 0; tt < TG; ++tt)
+        load_x4<XBF16>(x, static_cast<size_t>(min(t0 + tt, T - 1)) * d + i, xv[tt]);
+#pragma unroll
+      for (int tt = 0; tt < TG; ++tt) {
+        acc[tt] = fma(static_cast<double>(xv[tt][0]), static_cast<double>(wv[u].x), acc[tt]);
+        acc[tt] = fma(static_cast<double>(xv[tt][1]), static_cast<double>(wv[u].y), acc[tt]);
+        acc[tt] = fma(static_cast<double>(xv[tt][2]), static_cast<double>(wv[u].z), acc[tt]);
+        acc[tt] = fma(static_cast<double>(xv[tt][3]), static_cast<double>(wv[u].w), acc[tt]);
       }
     }
   }
 }
 
-template <bool XBF16>
+template <bool XBF16, int TG>
 __global__ __launch_bounds__(256) void logits_split(const void* __restrict__ x,
                                                      const float* __restrict__ w,
                                                      double* __restrict__ part, int T, int d,
@@ -87,15 +92,14 @@ __global__ __launch_bounds__(256) void logits_split(const void* __restrict__ x,
   if (item >= E * P) return;
   const int e = item / P, p = item - e * P;
   const int i0 = p * L, i1 = min(d, i0 + L);
-  for (int t0 = 0; t0 < T; t0 += kTokGroup) {
-    double acc[kTokGroup];
-    logits_part<XBF16>(x, w, T, d, e, i0, i1, t0, lane, acc);
+  const int t0 = blockIdx.y * TG;
+  double acc[TG];
+  logits_part<XBF16, TG>(x, w, T, d, e, i0, i1, t0, lane, acc);
 #pragma unroll
-    for (int tt = 0; tt < kTokGroup; ++tt) {
-      if (t0 + tt < T) {
-        const double s = wave_sum_f64_tree(acc[tt]);
-        if (lane == 0) part[(static_cast<size_t>(t0 + tt) * E + e) * P + p] = s;
-      }
+  for (int tt = 0; tt < TG; ++tt) {
+    if (t0 + tt < T) {
+      const double s = wave_sum_f64_tree(acc[tt]);
+      if (lane == 0) part[(static_cast<size_t>(t0 + tt) * E + e) * P + p] = s;
     }
   }
 }
@@ -319,11 +323,18 @@ hipError_t launch_logits(int T, int d, int E, int P, const void* x, bool x_bf16,
                          const float* w_router, double* logits, hipStream_t stream) {
   if (T <= kSplitMaxT) {
     const int L = ((d + P - 1) / P + 3) / 4 * 4;
-    const dim3 grid((E * P + 3) / 4);
-    return x_bf16 ? launch(logits_split<true>, grid, dim3(256), 0, stream, x, w_router, logits, T,
-                          d, E, P, L)
-                  : launch(logits_split<false>, grid, dim3(256), 0, stream, x, w_router, logits,
-                           T, d, E, P, L);
+    auto go = [&](auto tg) {
+      constexpr int TG = decltype(tg)::value;
+      const dim3 grid((E * P + 3) / 4, (T + TG - 1) / TG);
+      return x_bf16 ? launch(logits_split<true, TG>, grid, dim3(256), 0, stream, x, w_router,
+                             logits, T, d, E, P, L)
+                    : launch(logits_split<false, TG>, grid, dim3(256), 0, stream, x, w_router,
+                             logits, T, d, E, P, L);
+    };
+    if (T <= 1) return go(std::integral_constant<int, 1>{});
+    if (T <= 2) return go(std::integral_constant<int, 2>{});
+    if (T <= 4) return go(std::integral_constant<int, 4>{});
+    return go(std::integral_constant<int, kTokGroup>{});
   }
   const int L = ((d + P - 1) / P + kMK - 1) / kMK * kMK;
   const dim3 grid((E + kME - 1) / kME, (T + kMT - 1) / kMT, P);

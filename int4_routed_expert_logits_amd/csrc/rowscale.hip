@@ -79,27 +79,32 @@ __device__ __forceinline__ float row_scale(uint32_t top) {
   return fmaxf(__uint_as_float(top) * (1.0f / 127.0f), 0x1p-126f);
 }
 
-// Eight codes; zeros where the scale is NaN.
+// Eight codes; zeros where the scale is NaN.  Quotients this near to a half-way
+// point (about one wavefront's codes in twenty hold one) are decided by r.
 __device__ __forceinline__ uint2 codes8(const float (&v)[kV], float scale) {
-  const bool ok = scale == scale;
-  const float inv = 1.0f / scale, half = 0.5f * scale;
-  uint32_t w[2] = {0u, 0u};
+  if (!(scale == scale)) return make_uint2(0u, 0u);
+  const float inv = 1.0f / scale, half = 0.5f * scale, near = 0.9999f * half;
+  float q[kV];
+  bool close = false;
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
-    const float q = rintf(v[j] * inv);
-    const float r = fmaf(-q, scale, v[j]);
-    int c = static_cast<int>(q);
-    const bool odd = c & 1;
-    c += (r > half || (r == half && odd)) - (r < -half || (r == -half && odd));
-    w[j / 4] |= (ok ? static_cast<uint32_t>(c) & 0xFFu : 0u) << (8 * (j % 4));
+    q[j] = rintf(v[j] * inv);
+    close = close || fabsf(fmaf(-q[j], scale, v[j])) > near;
   }
+  if (close) {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      const float r = fmaf(-q[j], scale, v[j]);
+      const bool odd = static_cast<int>(q[j]) & 1;
+      if (r > half || (r == half && odd)) q[j] += 1.0f;
+      if (r < -half || (r == -half && odd)) q[j] -= 1.0f;
+    }
+  }
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < kV; ++j)
+    w[j / 4] |= (static_cast<uint32_t>(static_cast<int>(q[j])) & 0xFFu) << (8 * (j % 4));
   return make_uint2(w[0], w[1]);
-}
-
-__device__ __forceinline__ uint32_t wave_top(uint32_t m) {
-  for (int off = kWave / 2; off > 0; off >>= 1)
-    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), off, kWave)));
-  return m;
 }
 
 // WIDE: a workgroup per row, else a wavefront.
@@ -132,7 +137,7 @@ __global__ __launch_bounds__(kThreads) void row_codes(int64_t rows, int K,
       src.load(c, u);
       m = top8(u, m);
     }
-    m = wave_top(m);
+    m = wave_max_u32(m);
     if constexpr (WIDE) {  // two turns' maxima in turn, so one meeting each is enough
       if (threadIdx.x % kWave == 0) sh[turn][threadIdx.x / kWave] = m;
       __syncthreads();
