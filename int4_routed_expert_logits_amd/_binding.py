@@ -451,7 +451,7 @@ def _types():
         # the stream's handle and the device's index themselves: building a torch
         # Stream takes as long as a launch
         _raw_stream = torch._C._cuda_getCurrentRawStream
-        _current_device = torch._C._cuda_getDevice
+        _current_device = _current_device or torch._C._cuda_getDevice
         _INT8 = (torch.int8,)
         _CODES.update({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
         _T = ((torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32), (torch.int32,),

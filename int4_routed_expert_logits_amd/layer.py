@@ -6,15 +6,17 @@ moe_combine on one stream with no host synchronisation in between;
 ``run_layer_decode`` makes the single moe_layer_decode call instead (decode
 batches of at most 8 tokens).
 
-``run_layer_float`` is the layer on bfloat16 expert weights, or on e4m3 codes
-with block scales, ``run_layer_float_grad`` its gradient (the routing taken as
-given), and ``run_block`` any of them between its norms and residual.
+``run_layer_float`` is the layer on bfloat16 expert weights, on e4m3 codes with
+block scales or on 8-bit integers with row scales, ``run_layer_few`` the same for a
+few tokens in one call, ``run_layer_float_grad`` its gradient (the routing taken as
+given), ``AdamW`` the step that applies such gradients, and ``run_block`` any of the
+layers between its norms and residual.
 """
 from __future__ import annotations
 
 import contextlib
 import dataclasses
-from typing import Optional
+from typing import Optional, Sequence
 
 import torch
 
@@ -99,8 +101,9 @@ def run_layer_decode(x, w_router, bias, experts, shared, buf: LayerBuffers, stre
 class FloatExperts:
     """Expert weights of a layer: gate and up stacked [E, 2 f, d] (gate first),
     down [E, d, f], and the shared expert's as one-group tensors or None.  bf16,
-    or e4m3 codes with their scales per 128 x 128 ([E, 2 f / 128, d / 128] and
-    [E, d / 128, f / 128], rounded up)."""
+    e4m3 codes with their scales per 128 x 128 ([E, 2 f / 128, d / 128] and
+    [E, d / 128, f / 128], rounded up), or int8 codes with a scale per output
+    channel ([E, 2 f] and [E, d])."""
     gate_up: torch.Tensor
     down: torch.Tensor
     shared_gate_up: Optional[torch.Tensor] = None
@@ -109,19 +112,25 @@ class FloatExperts:
     shared_scales: Optional[tuple] = None
 
     @classmethod
-    def quantize(cls, e: "FloatExperts", stream=None) -> "FloatExperts":
-        """e's bf16 weights as codes and scales (moe_blockscale_quantize), ready
-        on `stream`.  Their memory is the current stream's: another one waits for
-        what is queued there first, and holds on to all it touches."""
+    def quantize(cls, e: "FloatExperts", stream=None, ints: bool = False) -> "FloatExperts":
+        """e's bf16 weights as e4m3 codes and scales (moe_blockscale_quantize), or
+        with `ints` as int8 ones (moe_rowscale_quantize), ready on `stream`.  Their
+        memory is the current stream's: another one waits for what is queued
+        there first, and holds on to all it touches."""
         side = _torch_stream(stream, e.gate_up.device)
 
         def q(w):
             if w is None:
                 return None, None
             n, r, k = w.shape
-            codes = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
-            scales = torch.empty((n, -(-r // 128), -(-k // 128)), device=w.device)
-            B.moe_blockscale_quantize(w, 128, codes, scales, stream)
+            if ints:
+                codes = torch.empty(w.shape, dtype=torch.int8, device=w.device)
+                scales = torch.empty((n, r), device=w.device)
+                B.moe_rowscale_quantize(w, codes, scales, stream)
+            else:
+                codes = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
+                scales = torch.empty((n, -(-r // 128), -(-k // 128)), device=w.device)
+                B.moe_blockscale_quantize(w, 128, codes, scales, stream)
             if side is not None:
                 for t in (w, codes, scales):
                     t.record_stream(side)
@@ -166,16 +175,21 @@ class FloatLayerBuffers:
     codes: Optional[dict]         # (codes, scales) of x, h, h_shared (8-bit experts)
     out: torch.Tensor
     workspace: torch.Tensor
+    ints: bool = False            # the codes are int8 with a scale per row
 
     @classmethod
     def allocate(cls, shape, T: int, codes: bool = False, device="cuda",
-                 y_dtype=torch.bfloat16, out_dtype=torch.bfloat16):
+                 y_dtype=torch.bfloat16, out_dtype=torch.bfloat16, ints: bool = False):
+        """codes: for 8-bit experts, e4m3 ones, or int8 ones with `ints`."""
+        codes = codes or ints
         sh = B._shape(shape)
         k, E, d, f, P = sh.top_k, sh.n_experts, sh.d, sh.f, T * sh.top_k
         new = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=device)  # noqa: E731
         i32 = torch.int32
 
         def pair(rows, cols):
+            if ints:
+                return new(rows, cols, dtype=torch.int8), new(rows, dtype=torch.float32)
             return (new(rows, cols, dtype=torch.float8_e4m3fn),
                     new(rows, -(-cols // 128), dtype=torch.float32))
 
@@ -193,7 +207,8 @@ class FloatLayerBuffers:
             codes=dict(x=pair(T, d), h=pair(P, f), h_shared=pair(T, f) if shared else None)
             if codes else None,
             out=new(T, d, dtype=out_dtype),
-            workspace=new(max(B.moe_route_workspace_bytes(sh, T), 256), dtype=torch.uint8))
+            workspace=new(max(B.moe_route_workspace_bytes(sh, T), 256), dtype=torch.uint8),
+            ints=ints)
 
 
 def _check_float(fn: str, x, experts: FloatExperts, buf: FloatLayerBuffers):
@@ -204,6 +219,9 @@ def _check_float(fn: str, x, experts: FloatExperts, buf: FloatLayerBuffers):
         raise ValueError(f"{fn}: the shape and the weights disagree about a shared expert")
     if (experts.scales is None) != (buf.codes is None):
         raise ValueError(f"{fn}: 8-bit experts take buffers allocated with codes=True, bf16 ones "
+                         "without")
+    if buf.codes is not None and (experts.gate_up.dtype == torch.int8) != buf.ints:
+        raise ValueError(f"{fn}: int8 experts take buffers allocated with ints=True, e4m3 ones "
                          "without")
     _check_tensor(fn, "x", x, torch.bfloat16, x.shape, buf.gu.device)
 
@@ -235,7 +253,8 @@ def _check_tensor(fn: str, name: str, t, dtype, shape, device):
 def run_layer_float(x, w_router, bias, experts: FloatExperts, buf: FloatLayerBuffers, stream=None):
     """The layer for x [T, d] bf16 on float or 8-bit experts: route and union
     (w_router [E, d] and bias [E] or None, float32), gate and up products over
-    the gathered tokens, SwiGLU, down products, combine."""
+    the gathered tokens, SwiGLU, down products, combine.  Products with 8-bit
+    experts take x and h quantised the same way."""
     fn, sh, b, k = "run_layer_float", buf.shape, buf, buf.shape.top_k
     _check_float(fn, x, experts, buf)
     _check_tensor(fn, "w_router", w_router, torch.float32, (sh.n_experts, sh.d), b.gu.device)
@@ -253,22 +272,59 @@ def run_layer_float(x, w_router, bias, experts: FloatExperts, buf: FloatLayerBuf
             B.moe_swiglu(b.gu_shared, b.h_shared, stream=stream)
             B.moe_grouped_mm(b.h_shared, experts.shared_down, b.all_rows, b.y_shared, stream=stream)
     else:
+        if buf.ints:
+            quantize, mm, swiglu = (B.moe_rowscale_quantize, B.moe_rowscale_mm,
+                                    B.moe_swiglu_rowscale)
+        else:
+            quantize, mm, swiglu = (lambda x, q, s, stream: B.moe_blockscale_quantize(  # noqa: E731
+                x, 1, q, s, stream), B.moe_blockscale_mm, B.moe_swiglu_quantize)
         (xq, xs), (hq, hs) = b.codes["x"], b.codes["h"]
         gus, dns = experts.scales
-        B.moe_blockscale_quantize(x, 1, xq, xs, stream)
-        B.moe_blockscale_mm(xq, xs, experts.gate_up, gus, b.offsets, b.gu, b.perm, k, stream)
-        B.moe_swiglu_quantize(b.gu, hq, hs, b.n_rows, stream)
-        B.moe_blockscale_mm(hq, hs, experts.down, dns, b.offsets, b.y, stream=stream)
+        quantize(x, xq, xs, stream)
+        mm(xq, xs, experts.gate_up, gus, b.offsets, b.gu, b.perm, k, stream)
+        swiglu(b.gu, hq, hs, b.n_rows, stream)
+        mm(hq, hs, experts.down, dns, b.offsets, b.y, stream=stream)
         if b.y_shared is not None:
             (hq, hs), (gus, dns) = b.codes["h_shared"], experts.shared_scales
-            B.moe_blockscale_mm(xq, xs, experts.shared_gate_up, gus, b.all_rows, b.gu_shared,
-                                stream=stream)
-            B.moe_swiglu_quantize(b.gu_shared, hq, hs, stream=stream)
-            B.moe_blockscale_mm(hq, hs, experts.shared_down, dns, b.all_rows, b.y_shared,
-                                stream=stream)
+            mm(xq, xs, experts.shared_gate_up, gus, b.all_rows, b.gu_shared, stream=stream)
+            swiglu(b.gu_shared, hq, hs, stream=stream)
+            mm(hq, hs, experts.shared_down, dns, b.all_rows, b.y_shared, stream=stream)
     with _gpu_of(b.gu):
         B.moe_combine(sh, b.y, b.y_shared, b.inv_perm, b.topk_w, b.out, stream)
     return b.out
+
+
+@dataclasses.dataclass
+class FewLayerBuffers:
+    """Routing outputs, result and scratch of one run_layer_few call."""
+    shape: B.Shape
+    T: int
+    topk_idx: torch.Tensor
+    topk_w: torch.Tensor
+    out: torch.Tensor
+    workspace: torch.Tensor
+
+    @classmethod
+    def allocate(cls, shape, T: int, device="cuda", out_dtype=torch.bfloat16):
+        sh = B._shape(shape)
+        new = lambda *s, dtype: torch.empty(s, dtype=dtype, device=device)  # noqa: E731
+        return cls(sh, T, new(T, sh.top_k, dtype=torch.int32), new(T, sh.top_k, dtype=torch.float32),
+                   new(T, sh.d, dtype=out_dtype),
+                   new(max(B.moe_layer_few_workspace_bytes(sh, T), 256), dtype=torch.uint8))
+
+
+def run_layer_few(x, w_router, bias, experts: FloatExperts, buf: FewLayerBuffers, stream=None):
+    """The layer for a few tokens x [T, d] bf16 (T <= 32, T * top_k <= 256) on any
+    of FloatExperts' weights in one call, moe_layer_few: the products read each
+    expert hit once, and x and h are not quantised.  w_router None: buf.topk_idx
+    and buf.topk_w are given."""
+    sc, ssc = experts.scales or (None, None), experts.shared_scales or (None, None)
+    shared = None
+    if experts.shared_gate_up is not None:
+        shared = (experts.shared_gate_up, experts.shared_down, *ssc)
+    B.moe_layer_few(buf.shape, x, w_router, bias, (experts.gate_up, experts.down, *sc), shared,
+                    buf.topk_idx, buf.topk_w, buf.out, buf.workspace, stream)
+    return buf.out
 
 
 @dataclasses.dataclass
@@ -336,6 +392,55 @@ def run_layer_float_grad(dout, x, experts: FloatExperts, buf: FloatLayerBuffers,
     with _gpu_of(b.gu):
         B.moe_combine(sh, g.dx_slots, g.dx_shared, b.inv_perm, g.ones, g.dx, stream)
     return g
+
+
+class AdamW:
+    """AdamW over a list of tensors and their gradients (buffers that later
+    backward passes fill again): moments in float32 or, with bits=8, in codes, a
+    float32 master of each bf16 parameter (masters=False: none), and the step's
+    number on the device, so that a captured step counts on."""
+
+    def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
+                 bits: int = 32, masters: bool = True):
+        if bits not in (8, 32):
+            raise ValueError(f"AdamW: moments of {bits} bits; 8 or 32")
+        if not params:
+            raise ValueError("AdamW: no parameters")
+        self.params, self.grads = list(params), list(grads)
+        dev = self.params[0].device
+        new = lambda p, dt: torch.zeros(p.shape, dtype=dt, device=p.device)  # noqa: E731
+        self.masters = [p.float() if masters and p.dtype == torch.bfloat16 else None
+                        for p in self.params]
+        if bits == 32:
+            self.m, self.v = ([new(p, torch.float32) for p in self.params] for _ in range(2))
+            self.m_scales = self.v_scales = None
+        else:
+            self.m = [new(p, torch.float8_e4m3fn) for p in self.params]
+            self.v = [new(p, torch.uint8) for p in self.params]
+            ones = lambda p: torch.ones(-(-p.numel() // 256), device=p.device)  # noqa: E731
+            self.m_scales, self.v_scales = ([ones(p) for p in self.params] for _ in range(2))
+        self.count = torch.zeros(1, dtype=torch.int64, device=dev)
+        self.tensors = B.AdamWTensors(self.params, self.grads, self.m, self.v, self.masters,
+                                      self.m_scales, self.v_scales)
+
+    @classmethod
+    def of_experts(cls, experts: FloatExperts, grads: "FloatLayerGrads", bits: int = 32,
+                   masters: bool = True) -> "AdamW":
+        """The bf16 weights of a layer with run_layer_float_grad's gradients."""
+        pairs = [(experts.gate_up, grads.dgate_up), (experts.down, grads.ddown),
+                 (experts.shared_gate_up, grads.dshared_gate_up),
+                 (experts.shared_down, grads.dshared_down)]
+        pairs = [(p, g) for p, g in pairs if p is not None]
+        return cls([p for p, _ in pairs], [g for _, g in pairs], bits, masters)
+
+    def step(self, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+             weight_decay: float = 0.0, grad_scale=None, stream=None):
+        """One step on `stream`, or the current one (moe_adamw)."""
+        side = _torch_stream(stream, self.count.device)
+        with contextlib.nullcontext() if side is None else torch.cuda.stream(side):
+            self.count += 1
+        B.moe_adamw(self.tensors, self.count, lr, beta1, beta2, eps, weight_decay, grad_scale,
+                    stream)
 
 
 @dataclasses.dataclass
