@@ -368,6 +368,15 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
       }
     }
   }
+  // integers: a row's and a column's scale a thread, on their way during the loop
+  float row_scale = 0.0f, col_scale = 0.0f;
+  if constexpr (C::I8) {
+    static_assert(C::BM <= C::Threads && C::BN <= C::Threads, "a thread per row and column");
+    const int64_t src = t < C::BM && m0 + t < mend ? source_row(g, m0 + t) : -1;
+    if (src >= 0) row_scale = g.r_scale[src];
+    if (t < C::BN && n0 + t < g.N)
+      col_scale = g.f_scale[static_cast<int64_t>(e) * g.N + n0 + t];
+  }
   // gathered F: the next stage's entries of rows, this wavefront's consecutive
   // ones
   constexpr int kWaveRows = C::K == kWeightsBy ? C::FBytes / (C::BN * 2) / C::Waves : 1;
@@ -580,24 +589,20 @@ __device__ void tile(const GroupedMm& g, uint8_t* smem, int e, int m0, int mend,
   // row again (stores of 8 bytes per lane, 32 in a row, took twice the time).
   const int cols = C::FT ? g.K : g.N;
   const int q = lane >> 4;
-  f32x4_t wsc[C::FF];  // integers: the columns' scales
+  f32x4_t wsc[C::FF];
+  float* scales = reinterpret_cast<float*>(smem);  // the rows', the columns'
   if constexpr (C::I8) {
+    if (t < C::BM) scales[t] = row_scale;
+    if (t < C::BN) scales[C::BM + t] = col_scale;
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < C::FF; ++j) {
-      const int n = n0 + nw + j * 16 + q * 4;
-      wsc[j] = n < cols ? *reinterpret_cast<const f32x4_t*>(g.f_scale +
-                                                            static_cast<int64_t>(e) * g.N + n)
-                        : f32x4_t{0, 0, 0, 0};
-    }
+    for (int j = 0; j < C::FF; ++j)
+      wsc[j] = *reinterpret_cast<const f32x4_t*>(scales + C::BM + nw + j * 16 + q * 4);
   }
 #pragma unroll
   for (int i = 0; i < C::RF; ++i) {
     const int m = m0 + mw + i * 16 + (lane & 15);
-    float xsc = 0.0f;
-    if constexpr (C::I8) {
-      const int64_t src = m < mend ? source_row(g, m) : -1;
-      if (src >= 0) xsc = g.r_scale[src];
-    }
+    const float xsc = C::I8 ? scales[mw + i * 16 + (lane & 15)] : 1.0f;
     auto value = [&](int j) -> f32x4_t {
       if constexpr (C::I8)
         return __builtin_convertvector(acc[i][j], f32x4_t) * xsc * wsc[j];
