@@ -907,6 +907,22 @@ int64_t most_row_tiles(const GroupedMm& g, int bm) {
 // (256 of 4096 x 6144, 2048 skewed rows of codes 1525 / 993).
 bool few_rows(const GroupedMm& g) { return g.P <= 64 + 3 * g.E; }
 
+// Integers, whose tiles read the weights about as fast wherever there are enough
+// of them: few rows in few tiles, and a few rows in groups of their own, but not
+// where the weight rows lie 4096 bytes apart (16 of them at once, as here, then
+// meet in the same channels) nor where a row is hardly one turn long.  us, this
+// kernel / the tiles: one expert of N = 4096, K = 6144 (16 tiles) 16 rows 7.7 / 23.0,
+// 48 rows 19.6 / 23.1, 64 rows 25.7 / 23.2; 8 rows over 64 of 1024 x 4096 (32 tiles)
+// 7.3 / 16.9, over 256 of 1024 x 2048 (32) 7.0 / 10.5; 64 over 256 of 4096 x 6144 (1024
+// tiles) 263 / 267, as a layer routes 8 tokens 225 / 232, skewed 141 / 135, 256 over
+// them 1051 / 1032, skewed 396 / 329; 40 over 15 of 1784 x 3568 22.5 / 25.1, 64 over 4 of
+// 6144 x 2048 13.8 / 11.2; 8 over 16 of 4096 x 4096 (128 tiles) 29.4 / 22.2; 64 over 256 of
+// 1024 x 512 10.9 / 7.0.
+bool few_integer_rows(const GroupedMm& g) {
+  if ((g.E < g.P ? g.E : g.P) * ((g.N + kBN - 1) / kBN) <= 64) return g.P <= 48;
+  return g.P <= 64 && g.P <= 3 * g.E && g.K % 4096 != 0 && g.K >= 1024;
+}
+
 constexpr int kSkinnyThreads = 256;
 constexpr int kSkinnyWaves = kSkinnyThreads / kWave;
 
@@ -1070,7 +1086,7 @@ hipError_t launch_grouped_mm(const GroupedMm& args, GroupedKind kind, hipStream_
     return launch(join_parts, dim3(static_cast<uint32_t>((n / 4 + 255) / 256)), dim3(256), 0, stream,
                   g);
   }
-  if (kind != kGroupedInput && few_rows(g)) {
+  if (kind == kGroupedInts ? few_integer_rows(g) : kind != kGroupedInput && few_rows(g)) {
     auto skinny = [&](auto kernel, int cols) {
       const int nb = (g.N + cols - 1) / cols;
       return launch(kernel, dim3(static_cast<uint32_t>(nb * (g.E < g.P ? g.E : g.P))),
