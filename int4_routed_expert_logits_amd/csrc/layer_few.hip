@@ -4,21 +4,31 @@
 //   few_gate_up   h[s] = silu(G_e x[t]) * (U_e x[t])
 //   few_down      out[t] = sum_j w[t][j] D_e h[t k + j]  (+ D h of the shared expert)
 //
-// Bound by reading the hit experts' weights once.  Neither kernel needs the
+// Bound by reading the hit experts' weights once.  few_gate_up does not need the
 // tokens grouped beforehand: a workgroup sets a bit per chosen expert in LDS,
 // takes its expert from the set bits and finds the expert's pairs by ballots
-// over the (at most 256) ids.  A second kernel is needed since every element of
-// out wants all of h; combining there spares y's way through memory and a launch.
+// over the (at most 256) ids; one more workgroup writes that grouping down for
+// few_down.  A second kernel is needed since every element of out wants all of h;
+// combining there spares y's way through memory and a launch.
 //
-// The weights go from memory straight into the matrix instruction's A side, 16
-// of its rows x 64 bytes a load: there is nothing to share through LDS, so the
-// loads need no barrier.  The tokens are the B side, up to 16 a fragment and two
-// fragments at once; lanes without a token multiply zeros, which no one reads.
-// Codes are widened to bf16, which holds each of them exactly.  x is not
-// quantised; h is kept as two bf16 values (16 significant bits, off by 2^-17 at
-// most, the second one's product costing little beside the weights' bytes).
-// All sums are float32, in an order that depends on the sizes and the number of
-// experts hit alone.
+// The weights go from memory straight into the matrix instruction's A side, 8 of
+// its rows x 128 bytes a load: there is nothing to share through LDS, so the loads
+// need no barrier.  The tokens are the B side, up to 8 a fragment and two
+// fragments at once.  Codes are widened to bf16, which holds each of them exactly.
+// x is not quantised; h is kept as a sum of bf16 values: three hold all of its 24
+// bits, and two (17 bits) do for an out of bf16, whose own rounding is 2^-9.
+// All sums are float32, in an order that depends on the sizes and the routing
+// alone.
+//
+// Measured: one token over 8 of 256 bf16 experts of 6144 x 2048 and a shared one
+// 137 us with its routing: 79 (453 MB, 5.7 TB/s) and 43 us (226 MB, 5.3 TB/s); 8 tokens
+// on integers 401: 240 (1.47 GB, 6.1 TB/s) and 130 us (0.74 GB, 5.7 TB/s).  Steps that
+// got there, for the two: 16 weight rows x 64 bytes a load and tokens by masked
+// loads 188 / 633, 8 rows x 128 bytes without masks 145 / 726, gate and up (or two
+// column tiles) sharing their tokens, one step at a time with the next weights
+// under way 157 / 467, few_down's steps shared evenly and the grouping handed on 145 /
+// 455, its columns by the CUs 136 / 405.  Two or more steps at a time, or the
+// tokens a step ahead as well, gain nothing and need the registers.
 #include <type_traits>
 
 #include "common.h"
@@ -34,9 +44,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-#ifndef SS
-#define SS 4
-#endif
 constexpr int kCols = 8;      // weight rows (output columns) of a fragment
 constexpr int kBlock = 128;   // rows and columns per scale of e4m3 codes
 constexpr int kMaxPairs = 256, kMaxIds = 1024, kCus = 256;
@@ -637,21 +644,47 @@ __global__ __launch_bounds__(256) void few_join(FewLayer g, int splits) {
     static_cast<uint16_t*>(g.out)[i] = f32_to_bf16(v);
 }
 
-// Fragments of a wavefront of few_down: as many workgroups as there are CUs.
-int down_frags(int d) { return (d / kCols + kCus - 1) / kCus; }
+// How few_down is laid out: the fragments of a wavefront (8 columns of out each)
+// and the workgroups that share the steps of one tile of out.
+struct DownPlan {
+  int frags, splits;
+};
 
-// Where out is too narrow for that, the steps are split over workgroups too, and
-// a third kernel joins their sums: as many as fill the CUs and leave a wavefront
-// kSplitSteps steps if every pair has an expert of its own.
-constexpr int kMaxSplits = 16, kSplitSteps = SS;
-int down_splits(int T, int k, int d, int f, int E, bool shared, int step) {
-  const int tiles = d / kCols, pairs = T * k;
-  const int64_t steps = static_cast<int64_t>((pairs < E ? pairs : E) + shared) * ((f + step - 1) / step);
-  const int64_t most = steps / (kDnWaves * kSplitSteps);
-  int s = kCus / tiles;
-  if (s > most) s = static_cast<int>(most);
-  if (s > kMaxSplits) s = kMaxSplits;
-  return s > 1 ? s : 1;
+// A workgroup for each CU, or as many of them as go: us of the layer with 1, 2, 3, 4
+// fragments, one token on bf16 over 64 experts of f = 1024 and 8 on integers:
+//   d = 2048  26.9  28.1  30.1  31.8 and  73  69  75  69
+//   d = 2560  39.0  33.5  33.6  35.4     107  91  85  83
+//   d = 4096  49.9  44.5  47.9  47.3     127 114 122 114
+//   d = 6144  71.4  69.2  62.4  64.1     184 176 155 162
+// Short calls (fewer than kLongSteps steps of all experts) take the fewest
+// fragments that suffice.  In longer ones what is read of h counts beside the
+// weights, two fragments share it, and a third kernel that joins the sums of
+// workgroups that split the steps (3 us and a launch) costs less than CUs without
+// work: of the layouts that use most CUs, the one with two fragments or the
+// fewest more.  Steps are split where that leaves a wavefront kSplitSteps steps
+// if every pair has an expert of its own, in short calls too (28 tokens over 5
+// experts of 128 x 3584: 104 us without, 48 so).
+constexpr int kMaxSplits = 16, kSplitSteps = 4, kLongSteps = 256, kMaxFrags = 4;
+DownPlan down_plan(int T, int k, int d, int f, int E, bool shared, int step) {
+  const int pairs = T * k, cols = d / kCols;
+  const int64_t steps =
+      static_cast<int64_t>((pairs < E ? pairs : E) + shared) * ((f + step - 1) / step);
+  auto splits_of = [&](int frags) {
+    int64_t s = kCus / ((cols + frags - 1) / frags);
+    const int64_t most = steps / (kDnWaves * kSplitSteps);
+    if (s > most) s = most;
+    if (s > kMaxSplits) s = kMaxSplits;
+    return s > 1 ? static_cast<int>(s) : 1;
+  };
+  const int least = (cols + kCus - 1) / kCus;
+  DownPlan best{least, splits_of(least)};
+  if (steps < kLongSteps) return best;
+  auto used = [&](const DownPlan& p) { return (cols + p.frags - 1) / p.frags * p.splits; };
+  for (int frags = least + 1; frags <= kMaxFrags; ++frags) {
+    const DownPlan p{frags, splits_of(frags)};
+    if (used(p) > used(best) || (used(p) == used(best) && best.frags == 1)) best = p;
+  }
+  return best;
 }
 
 template <int KIND, int PARTS, bool MANY>
@@ -661,25 +694,23 @@ hipError_t go(const FewLayer& g, hipStream_t stream) {
   const hipError_t e = launch(few_gate_up<KIND, PARTS, MANY>, dim3(static_cast<uint32_t>(slots * tiles + 1)),
                               dim3(kGuThreads), 0, stream, g, tiles);
   if (e != hipSuccess) return e;
-  const int splits = down_splits(g.T, g.k, g.d, g.f, g.E, g.shared, Fmt<KIND>::kStep);
+  const DownPlan plan = down_plan(g.T, g.k, g.d, g.f, g.E, g.shared, Fmt<KIND>::kStep);
   auto down = [&](auto fr) {
     constexpr int FR = decltype(fr)::value;
     return launch(few_down<KIND, PARTS, MANY, FR>,
-                  dim3(static_cast<uint32_t>((g.d / kCols + FR - 1) / FR), splits),
-                  dim3(kDnThreads), 0, stream, g, splits);
+                  dim3(static_cast<uint32_t>((g.d / kCols + FR - 1) / FR), plan.splits),
+                  dim3(kDnThreads), 0, stream, g, plan.splits);
   };
-  if (splits > 1) {
-    const hipError_t err = down(std::integral_constant<int, 1>{});
-    if (err != hipSuccess) return err;
-    return launch(few_join, dim3(static_cast<uint32_t>((g.T * g.d + 255) / 256)), dim3(256), 0,
-                  stream, g, splits);
+  hipError_t err;
+  switch (plan.frags) {
+    case 1: err = down(std::integral_constant<int, 1>{}); break;
+    case 2: err = down(std::integral_constant<int, 2>{}); break;
+    case 3: err = down(std::integral_constant<int, 3>{}); break;
+    default: err = down(std::integral_constant<int, 4>{});
   }
-  switch (down_frags(g.d)) {
-    case 1: return down(std::integral_constant<int, 1>{});
-    case 2: return down(std::integral_constant<int, 2>{});
-    case 3: return down(std::integral_constant<int, 3>{});
-    default: return down(std::integral_constant<int, 4>{});
-  }
+  if (plan.splits == 1 || err != hipSuccess) return err;
+  return launch(few_join, dim3(static_cast<uint32_t>((g.T * g.d + 255) / 256)), dim3(256), 0, stream,
+                g, plan.splits);
 }
 template <int KIND>
 hipError_t go(const FewLayer& g, hipStream_t stream) {
@@ -689,13 +720,17 @@ hipError_t go(const FewLayer& g, hipStream_t stream) {
 
 }  // namespace
 
-// The grouping, h, and the splits' sums (by the smaller step of the two: more splits).
+// The grouping, h, and the splits' sums, whatever the weights are held in.
 FewScratch few_scratch(int T, int k, int d, int f, int E, bool shared) {
   FewScratch s;
   s.h = kFewTableBytes;
   const size_t h = static_cast<size_t>(T) * (k + shared) * f * 3 * sizeof(uint16_t);
   s.parts = (s.h + h + 15) / 16 * 16;
-  const int splits = down_splits(T, k, d, f, E, shared, Fmt<kFewBf16>::kStep);
+  int splits = 1;
+  for (int step : {Fmt<kFewBf16>::kStep, Fmt<kFewE4m3>::kStep, Fmt<kFewInt8>::kStep}) {
+    const int n = down_plan(T, k, d, f, E, shared, step).splits;
+    if (n > splits) splits = n;
+  }
   s.bytes = s.parts + (splits > 1 ? static_cast<size_t>(splits) * T * d * sizeof(float) : 0);
   return s;
 }
