@@ -450,7 +450,9 @@ __global__ __launch_bounds__(kGuThreads) void few_gate_up(FewLayer g, int tiles)
       uint16_t* out = g.h + static_cast<int64_t>(row) * g.f + n0 + c;
 #pragma unroll
       for (int p = 0; p < PARTS; ++p) {
-        const uint16_t v = f32_to_bf16(h);
+        uint16_t v = f32_to_bf16(h);
+        // what is finite but rounds to an infinity takes bf16's largest
+        if ((v & 0x7FFFu) == 0x7F80u && fabsf(h) < __builtin_inff()) --v;
         out[p * g.h_apart] = v;
         h -= bf16_to_f32(v);
         if (h != h) h = 0.0f;  // what is not finite has no rest
@@ -561,7 +563,6 @@ __global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g, int splits) {
           const int r = min(m0 + b * 8 + i8, n - 1);
           row[b] = shared ? pairs + r : tb.pair[first + r];
           xo[b] = static_cast<uint32_t>(row[b] * g.f + half * F::kHalf + q * F::kChunk) * 2;
-          
 #pragma unroll
           for (int f = 0; f < FR; ++f) acc[f][b] = f32x4_t{0, 0, 0, 0};
         }
@@ -617,7 +618,9 @@ __global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g, int splits) {
 #pragma unroll 4
     for (int j = 0; j < g.k; ++j) {
       const int s = tok * g.k + j;
-      if (tb.valid[s]) v = fmaf(weight[s], sums[s][c], v);
+      // an expert without steps here has no part in this sum, whatever its weight
+      const int at = (tb.group[s] + g.shared) * all;
+      if (tb.valid[s] && at < wg_end && at + all > wg_begin) v = fmaf(weight[s], sums[s][c], v);
     }
     if (g.shared) v += sums[pairs + tok][c];
     const int64_t at = static_cast<int64_t>(tok) * g.d + n0 + c;

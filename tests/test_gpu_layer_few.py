@@ -165,6 +165,81 @@ def test_infinite_h_is_no_nan(gpu_lib):
     assert (run(c) == float("inf")).all()
 
 
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_h_past_bfloat16s_largest(gpu_lib, out):
+    """h = 2^64 (2^63 255/128 + 2^55 3/2) = (2 - 2^-9) 2^127, which float32 holds and
+    bf16 would round to infinity.  out = 64 h 2^-20: h's parts hold it exactly in
+    float32, and within 2^-17 for an out of bf16, whose own rounding is 2^-9."""
+    c = make("bf16", 1, 64, 64, 1, 1, False, 1, idx=torch.zeros((1, 1)))
+    c["w"].fill_(1.0)
+    c["x"].zero_()
+    c["x"][0, :2] = 1.0
+    gu = c["experts"][0]
+    gu.zero_()
+    gu[0, :64, 0] = 2.0 ** 64
+    gu[0, 64:, 0] = 2.0 ** 63 * 255 / 128
+    gu[0, 64:, 1] = 2.0 ** 55 * 1.5
+    c["experts"][1].fill_(2.0 ** -20)
+    h = 2.0 ** 64 * (2.0 ** 63 * 255 / 128 + 2.0 ** 55 * 1.5)
+    got = d64(run(c, out))
+    allow = 0.0 if out == F32 else 2.0 ** -17 + 2.0 ** -9
+    assert ((got - 64 * h * 2.0 ** -20).abs() <= allow * 64 * h * 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "int8"])
+def test_an_infinite_weight_where_workgroups_share_the_steps(gpu_lib, kind):
+    """Two experts of 64 columns over a long f: several workgroups share a tile's
+    steps, and the ones without any of the second expert leave its weight alone."""
+    c = make(kind, 1, 64, 8192, 2, 2, False, 3, idx=torch.tensor([[0, 1]]))
+    c["x"].abs_()
+    for w in c["experts"][:2]:
+        w.copy_(w.float().abs().clamp(max=100).to(w.dtype))
+    for weights in ((1.0, float("inf")), (float("inf"), 1.0)):
+        c["w"].copy_(torch.tensor([weights]))
+        assert (run(c) == float("inf")).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("T,d,f,E,k,shared", [
+    (1, 64, 8192, 2, 2, True), (28, 128, 3584, 5, 3, False), (8, 2176, 1088, 16, 8, True),
+    (32, 4160, 64, 100, 8, False), (32, 4608, 192, 40, 8, True), (16, 8128, 320, 4, 2, False)])
+def test_layouts_of_the_down_product(gpu_lib, T, d, f, E, k, shared, kind):
+    """Split steps, one to four fragments a wavefront, and columns that fill the last
+    workgroup's in part."""
+    c = make(kind, T, d, f, E, k, shared, T + d)
+    for out in (F32, BF16):
+        check(c, run(c, out), out, f"{kind} {out}")
+    assert torch.equal(run(c), run(c))
+
+
+def test_256_experts_of_one_pair_each(gpu_lib):
+    """As many experts hit as the grouping holds."""
+    idx = torch.randperm(1024, generator=gen(9))[:256].view(32, 8)
+    for kind in ("bf16", "e4m3", "int8"):
+        c = make(kind, 32, 128, 64, 1024, 8, True, 10, idx=idx)
+        check(c, run(c), F32, kind)
+
+
+def test_one_workspace_in_two_graphs(gpu_lib):
+    """Graphs that are replayed one after the other may share a workspace."""
+    cases = [make(kind, T, 320, 192, 8, 3, True, T) for kind, T in (("bf16", 5), ("int8", 20))]
+    ws = torch.empty(max(moe.moe_layer_few_workspace_bytes(c["shape"], c["T"]) for c in cases),
+                     dtype=torch.uint8, device="cuda")
+    want = [run(c) for c in cases]
+    graphs, outs = [], [torch.empty_like(w) for w in want]
+    for c, o in zip(cases, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_layer_few(c["shape"], c["x"], None, None, c["experts"], c["shared"], c["idx"],
+                              c["w"], o, ws)
+        graphs.append(graph)
+    for i in (0, 1, 1, 0, 1, 0):
+        outs[i].fill_(3)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], want[i])
+
+
 def test_batch_does_not_change_a_token_much(gpu_lib):
     """A token alone and among others: both within their allowances of each other's
     reference."""
