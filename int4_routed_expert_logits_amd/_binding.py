@@ -829,7 +829,9 @@ class AdamWTensors:
     the moments: float32 of the same shape, or with m_scales and v_scales 8-bit
     codes (m float8_e4m3fn or uint8, v uint8) and a float32 scale per 256 elements.
     masters: a float32 copy of each bf16 parameter, or None for all or for one.
-    All on one GPU, without gaps, none overlapping one that the step writes."""
+    All on one GPU, without gaps, none overlapping one that the step writes.  A step
+    goes by the addresses taken here; it refuses a list of which a parameter or a
+    gradient has been given other memory since (`p.data = ...`)."""
 
     def __init__(self, params, grads, m, v, masters=None, m_scales=None, v_scales=None):
         fn = "AdamWTensors"
@@ -848,6 +850,8 @@ class AdamWTensors:
         self.device = params[0].get_device() if n else -1
         self.array = (AdamWTensor * n)()
         self.n = n
+        # their memory, also of one that is given another later
+        self.held = [t.untyped_storage() for q in lists for t in q if t is not None]
         spans, dev = [], self.device
         bf16, byte = _T[0][0], codes[1:]
 
@@ -883,6 +887,7 @@ class AdamWTensors:
                 s.m, s.v = take("m", i, a, codes, shape, count), take("v", i, b, byte, shape, count)
                 s.m_scales = take("m_scales", i, sa, f32, blocks, blocks[0])
                 s.v_scales = take("v_scales", i, sb, f32, blocks, blocks[0])
+        self.at = self.where()
         # two spans overlap only if one of them does with the one that reaches
         # furthest among those that begin before it: of the written and of all
         end = [(0, -1), (0, -1)]
@@ -894,6 +899,13 @@ class AdamWTensors:
                 end[0] = max(end[0], (hi, i))
             end[1] = max(end[1], (hi, i))
 
+    def where(self):
+        """The addresses of what a training loop may replace (all of them take 80 ns
+        each, a third of a step over small tensors)."""
+        import torch
+        at = torch.Tensor.data_ptr
+        return [*map(at, self.tensors[0]), *map(at, self.tensors[2])]
+
 
 def moe_adamw(tensors: AdamWTensors, step, lr: float, beta1: float = 0.9, beta2: float = 0.999,
               eps: float = 1e-8, weight_decay: float = 0.0, grad_scale=None, stream=None):
@@ -901,6 +913,8 @@ def moe_adamw(tensors: AdamWTensors, step, lr: float, beta1: float = 0.9, beta2:
     advances it); grad_scale: device f32 [1] that gradients are multiplied by."""
     fn = "moe_adamw"
     import torch
+    if tensors.where() != tensors.at:
+        raise ValueError(f"{fn}: a tensor lies elsewhere than when the list was made")
     dev = tensors.device if tensors.n else step.get_device()
     _, f32, _, _, _ = _T or _types()
     _run(fn, dev, stream, tensors.array, tensors.n,

@@ -398,7 +398,8 @@ class AdamW:
     """AdamW over a list of tensors and their gradients (buffers that later
     backward passes fill again): moments in float32 or, with bits=8, in codes, a
     float32 master of each bf16 parameter (masters=False: none), and the step's
-    number on the device, so that a captured step counts on."""
+    number on the device, so that a captured step counts on.  A saved state (count,
+    masters, m, v and the scales) is copied into these tensors."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                  bits: int = 32, masters: bool = True):
@@ -409,7 +410,7 @@ class AdamW:
         self.params, self.grads = list(params), list(grads)
         dev = self.params[0].device
         new = lambda p, dt: torch.zeros(p.shape, dtype=dt, device=p.device)  # noqa: E731
-        self.masters = [p.float() if masters and p.dtype == torch.bfloat16 else None
+        self.masters = [p.detach().float() if masters and p.dtype == torch.bfloat16 else None
                         for p in self.params]
         if bits == 32:
             self.m, self.v = ([new(p, torch.float32) for p in self.params] for _ in range(2))
@@ -437,10 +438,16 @@ class AdamW:
              weight_decay: float = 0.0, grad_scale=None, stream=None):
         """One step on `stream`, or the current one (moe_adamw)."""
         side = _torch_stream(stream, self.count.device)
-        with contextlib.nullcontext() if side is None else torch.cuda.stream(side):
+        turn = lambda: contextlib.nullcontext() if side is None else torch.cuda.stream(side)  # noqa: E731
+        with turn():
             self.count += 1
-        B.moe_adamw(self.tensors, self.count, lr, beta1, beta2, eps, weight_decay, grad_scale,
-                    stream)
+        try:
+            B.moe_adamw(self.tensors, self.count, lr, beta1, beta2, eps, weight_decay, grad_scale,
+                        stream)
+        except Exception:
+            with turn():
+                self.count -= 1  # a step that was refused is none
+            raise
 
 
 @dataclasses.dataclass

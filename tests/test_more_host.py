@@ -345,6 +345,28 @@ def test_adamw_tensors_are_checked():
         moe.moe_adamw(q, torch.ones(1), 1e-3)
 
 
+def test_adamw_refuses_a_list_whose_memory_was_replaced():
+    for name in ("params", "grads"):
+        a = {q: [z(8), z(300)] for q in ("params", "grads", "m", "v")}
+        q = moe.AdamWTensors(**a)
+        a[name][1].data = z(300)
+        with pytest.raises(ValueError, match="lies elsewhere"):
+            moe.moe_adamw(q, torch.ones(1, dtype=torch.int64), 1e-3)
+
+
+def test_a_refused_step_does_not_count():
+    opt = L.AdamW([z(4)], [z(4)])
+    for _ in range(2):
+        with pytest.raises(ValueError, match="not on the GPU"):
+            opt.step(1e-3)
+    assert int(opt.count) == 0
+
+
+def test_masters_are_no_part_of_a_graph():
+    p = torch.nn.Parameter(z(4, dt=BF16))
+    assert not L.AdamW([p], [z(4)]).masters[0].requires_grad
+
+
 def test_optimiser_state_of_a_layer():
     bf = lambda *s: z(*s, dt=BF16)  # noqa: E731
     sh = moe.Shape(128, 64, 4, 2, 64, 64)
