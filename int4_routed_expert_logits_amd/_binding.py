@@ -439,20 +439,20 @@ def moe_cache_layer_decode(cache: int, x, w_router, bias, shared, topk_idx, topk
 # ----------------------------------------------------------------------------
 
 # set by _types(), which every call below makes first (once: `_T or _types()`)
-_T = _raw_stream = _current_device = _INT8 = None
+_T = _raw_stream = _current_device = _INT8 = _INT64 = _data_ptr = None
 _CODES = {}  # torch type -> moe_dtype
 
 
 def _types():
     """(bf16, f32, either, int32, e4m3 code) as tuples of torch types."""
-    global _T, _raw_stream, _current_device, _INT8
+    global _T, _raw_stream, _current_device, _INT8, _INT64, _data_ptr
     if _T is None:
         import torch
         # the stream's handle and the device's index themselves: building a torch
         # Stream takes as long as a launch
         _raw_stream = torch._C._cuda_getCurrentRawStream
         _current_device = _current_device or torch._C._cuda_getDevice
-        _INT8 = (torch.int8,)
+        _INT8, _INT64, _data_ptr = (torch.int8,), (torch.int64,), torch.Tensor.data_ptr
         _CODES.update({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
         _T = ((torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32), (torch.int32,),
               (torch.float8_e4m3fn, torch.uint8))
@@ -887,7 +887,10 @@ class AdamWTensors:
                 s.m, s.v = take("m", i, a, codes, shape, count), take("v", i, b, byte, shape, count)
                 s.m_scales = take("m_scales", i, sa, f32, blocks, blocks[0])
                 s.v_scales = take("v_scales", i, sb, f32, blocks, blocks[0])
-        self.at = self.where()
+        # what a training loop may give other memory (looking at all of them takes a
+        # third of a step over small tensors: 80 ns each)
+        self.live = [*lists[0], *lists[2]]
+        self.at = list(map(_data_ptr, self.live))
         # two spans overlap only if one of them does with the one that reaches
         # furthest among those that begin before it: of the written and of all
         end = [(0, -1), (0, -1)]
@@ -899,24 +902,15 @@ class AdamWTensors:
                 end[0] = max(end[0], (hi, i))
             end[1] = max(end[1], (hi, i))
 
-    def where(self):
-        """The addresses of what a training loop may replace (all of them take 80 ns
-        each, a third of a step over small tensors)."""
-        import torch
-        at = torch.Tensor.data_ptr
-        return [*map(at, self.tensors[0]), *map(at, self.tensors[2])]
-
 
 def moe_adamw(tensors: AdamWTensors, step, lr: float, beta1: float = 0.9, beta2: float = 0.999,
               eps: float = 1e-8, weight_decay: float = 0.0, grad_scale=None, stream=None):
     """One step, in place.  step: device int64 [1], 1 for the first (the caller
     advances it); grad_scale: device f32 [1] that gradients are multiplied by."""
     fn = "moe_adamw"
-    import torch
-    if tensors.where() != tensors.at:
+    if list(map(_data_ptr, tensors.live)) != tensors.at:
         raise ValueError(f"{fn}: a tensor lies elsewhere than when the list was made")
     dev = tensors.device if tensors.n else step.get_device()
-    _, f32, _, _, _ = _T or _types()
     _run(fn, dev, stream, tensors.array, tensors.n,
-         _take(fn, dev, "step", step, (torch.int64,), (1,)), lr, beta1, beta2, eps, weight_decay,
-         _take(fn, dev, "grad_scale", grad_scale, f32, (1,)))
+         _take(fn, dev, "step", step, _INT64, (1,)), lr, beta1, beta2, eps, weight_decay,
+         _take(fn, dev, "grad_scale", grad_scale, _T[1], (1,)))

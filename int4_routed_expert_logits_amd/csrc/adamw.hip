@@ -24,6 +24,8 @@
 // few (90 odd tensors, 2.9M elements: 28 us, so 17).  The tensors' addresses are
 // kernel arguments, up to 64 tensors a launch: nothing is kept on the device, and
 // a captured launch holds them.
+#include <utility>
+
 #include "common.h"
 #include "launch.h"
 
@@ -273,9 +275,19 @@ __global__ __launch_bounds__(kThreads) void adamw_step(const Batch<B8, P> b) {
   }
 }
 
+// How a tensor is held, as a number: its parameter, gradient and moments.
+constexpr int kKinds = 12;
+constexpr int kind_of(bool b8, int store, bool gbf16) { return (b8 * 3 + store) * 2 + gbf16; }
+int kind_of(const AdamWTensor& t) {
+  return kind_of(t.m_scales != nullptr, t.master ? kMaster : t.p_bf16 ? kBf16 : kF32, t.g_bf16);
+}
+
 // The tensors of one kind, a batch of them a launch.
-template <bool B8, int P, bool GBF16>
+template <int KIND>
 hipError_t go(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t stream) {
+  constexpr bool B8 = KIND / 6, GBF16 = KIND % 2;
+  constexpr int P = KIND / 2 % 3;
+  static_assert(KIND == kind_of(B8, P, GBF16));
   constexpr int64_t per = kWaves * kBlock;
   Batch<B8, P> b;
   b.n = 0;
@@ -291,8 +303,7 @@ hipError_t go(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t str
   };
   for (int i = 0; i < n; ++i) {
     const AdamWTensor t = src.get(src.tensors, i);
-    const int store = t.master ? kMaster : t.p_bf16 ? kBf16 : kF32;
-    if (t.n == 0 || store != P || t.g_bf16 != GBF16 || (t.m_scales != nullptr) != B8) continue;
+    if (t.n == 0 || kind_of(t) != KIND) continue;
     const int64_t chunks = (t.n + per - 1) / per;
     if (b.n == b.kMost || (b.n > 0 && b.first[b.n] + chunks > INT32_MAX)) {
       const hipError_t e = flush();
@@ -302,25 +313,24 @@ hipError_t go(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t str
   }
   return flush();
 }
-template <bool B8, int P>
-hipError_t go(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t stream) {
-  const hipError_t e = go<B8, P, false>(src, n, s, stream);
-  return e != hipSuccess ? e : go<B8, P, true>(src, n, s, stream);
+template <int... KIND>
+hipError_t go_each(uint32_t present, const AdamWSource& src, int n, const AdamWStep& s,
+                   hipStream_t stream, std::integer_sequence<int, KIND...>) {
+  hipError_t e = hipSuccess;
+  ((present >> KIND & 1 && e == hipSuccess ? void(e = go<KIND>(src, n, s, stream)) : void()), ...);
+  return e;
 }
 
 }  // namespace
 
-// Tensors of one kind (how the parameter, its gradient and its moments are held)
-// share launches.
+// Tensors of one kind share launches.
 hipError_t launch_adamw(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t stream) {
-  hipError_t (*const kinds[])(const AdamWSource&, int, const AdamWStep&, hipStream_t) = {
-      go<false, kF32>, go<false, kBf16>, go<false, kMaster>,
-      go<true, kF32>, go<true, kBf16>, go<true, kMaster>};
-  for (auto kind : kinds) {
-    const hipError_t e = kind(src, n, s, stream);
-    if (e != hipSuccess) return e;
+  uint32_t present = 0;
+  for (int i = 0; i < n; ++i) {
+    const AdamWTensor t = src.get(src.tensors, i);
+    if (t.n != 0) present |= 1u << kind_of(t);
   }
-  return hipSuccess;
+  return go_each(present, src, n, s, stream, std::make_integer_sequence<int, kKinds>{});
 }
 
 }  // namespace moe
