@@ -65,7 +65,8 @@ typedef struct {
  *              count as 1); the caller advances it, in a captured graph too
  *  grad_scale  device float32, or NULL for 1 (a clipping factor, or 1 / loss scale)
  *  lr, weight_decay  finite, >= 0; eps finite, > 0 in float32; beta1, beta2 in
- *              [0, 1) (else MOE_ERR_SHAPE) */
+ *              [0, 1) (else MOE_ERR_SHAPE); a captured step repeats these values and
+ *              the tensors' addresses */
 moe_status moe_adamw(const moe_adamw_tensor* tensors, int32_t n_tensors, const int64_t* step,
                      double lr, double beta1, double beta2, double eps, double weight_decay,
                      const float* grad_scale, void* stream);

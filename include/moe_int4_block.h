@@ -27,7 +27,8 @@
  * same bits (a product's last bits may differ between calls of other sizes, which
  * other kernels add up in another order).  Tensors are row-major without gaps;
  * bf16 and f32 arrays are 16-byte aligned, codes, the norms' weights and the
- * scales of a matrix's output channels too, int32 arrays, other scales and the weights' gradients of the norms 4-byte.
+ * scales of a matrix's output channels too, int32 arrays, other scales and the
+ * weights' gradients of the norms 4-byte.
  *
  * Rows grouped by expert: position p belongs to expert e when
  *   offsets[e] <= p < offsets[e + 1],

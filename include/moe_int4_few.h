@@ -3,8 +3,9 @@
  *
  * moe_layer_few computes what the calls of moe_int4_block.h compute in turn
  * (route, gate and up products, SwiGLU, down product, combine, shared expert)
- * for at most 32 tokens, in two kernels behind the router's, which read each hit
- * expert's weights once.  Conventions as in moe_int4_block.h: caller-owned
+ * for at most 32 tokens, in two kernels behind the router's (and a third that
+ * joins partial sums where out is narrow), which read each hit expert's weights
+ * once, or once per 16 of its tokens.  Conventions as in moe_int4_block.h: caller-owned
  * device memory, work enqueued on `stream`, nothing allocated, no state,
  * arguments checked before anything is enqueued, no atomics in memory: a call
  * repeated on the same inputs gives the same bits.
@@ -55,8 +56,8 @@ size_t moe_layer_few_workspace_bytes(const moe_shape* shape, int32_t T);
  *  T         0..32 with T * top_k <= 256, else MOE_ERR_UNSUPPORTED; 0 enqueues nothing
  *  w_router  [E][d] float32: the routing is moe_route's (bias [E] or NULL) and is
  *            written to topk_idx and topk_w [T][top_k].  NULL: both are inputs (and
- *            bias is NULL); an id outside [0, E) contributes nothing, and the same
- *            one twice counts twice.
+ *            bias is NULL); an id outside [0, E) contributes nothing, the same one
+ *            twice counts twice, and an infinite weight gives an infinity or NaN.
  *  experts, shared  host structures of device addresses, read during the call;
  *            shared NULL exactly where the shape has no shared expert
  *  out       [T][d] bf16 or f32; must not overlap an input
@@ -64,9 +65,9 @@ size_t moe_layer_few_workspace_bytes(const moe_shape* shape, int32_t T);
  *            initial contents required; never shared between calls that may run
  *            at the same time
  * x is not rounded (unlike the calls on codes, which quantise it); the products
- * are summed in float32, and h = silu(G x) * (U x) is held with 16 significant
- * bits between the two kernels (each off by 2^-17 of itself at most, where both
- * parts are normal bf16 numbers). */
+ * are summed in float32, and h = silu(G x) * (U x) is held between the kernels as a
+ * sum of bf16 values: three for an out of f32 (all 24 bits), two for one of bf16
+ * (17 bits, each off by 2^-17 of itself at most, where both are normal numbers). */
 moe_status moe_layer_few(const moe_shape* shape, int32_t T, const void* x, const float* w_router,
                          const float* bias, moe_weights kind, const moe_expert_weights* experts,
                          const moe_expert_weights* shared, int32_t* topk_idx, float* topk_w,

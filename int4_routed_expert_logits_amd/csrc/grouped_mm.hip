@@ -28,6 +28,11 @@
 // against the other's products; 8192 rows over one 4096 x 4096 matrix run at
 // 1150-1190 TFLOP/s in all, over 8192 x 8192 at 1310.  Codes run their products
 // at the same rate with the widening beside them: 930 TFLOP/s (297 us) there.
+// Integers have half the bytes and twice the rate, so the same balance: 8192
+// rows over 4096 x 4096 118 us, over 8192 x 8192 427 us (2.33 and 2.58 POP/s), 64
+// groups of 512 rows over 2048 x 2048 166 us (1.66), where each tile's 32 stages
+// hardly hide its start and its stores; 64 rows over 57 of 256 experts of 4096 x 6144
+// 225 us (6.4 TB/s), the skewed 2048-token prompt 1.24 ms (5.3 TB/s).
 #include <type_traits>
 
 #include "common.h"

@@ -1,4 +1,5 @@
-// The whole layer for a few tokens in two kernels, on bf16 experts, e4m3 codes
+// The whole layer for a few tokens in two kernels (and one that joins the sums of
+// workgroups that share a narrow out's steps), on bf16 experts, e4m3 codes
 // with a float32 scale per 128 x 128, or 8-bit integers with one per output
 // channel.  With s a (token, expert) pair of the routing and e its expert:
 //   few_gate_up   h[s] = silu(G_e x[t]) * (U_e x[t])
@@ -21,14 +22,18 @@
 // alone.
 //
 // Measured: one token over 8 of 256 bf16 experts of 6144 x 2048 and a shared one
-// 137 us with its routing: 79 (453 MB, 5.7 TB/s) and 43 us (226 MB, 5.3 TB/s); 8 tokens
-// on integers 401: 240 (1.47 GB, 6.1 TB/s) and 130 us (0.74 GB, 5.7 TB/s).  Steps that
-// got there, for the two: 16 weight rows x 64 bytes a load and tokens by masked
-// loads 188 / 633, 8 rows x 128 bytes without masks 145 / 726, gate and up (or two
-// column tiles) sharing their tokens, one step at a time with the next weights
-// under way 157 / 467, few_down's steps shared evenly and the grouping handed on 145 /
-// 455, its columns by the CUs 136 / 405.  Two or more steps at a time, or the
-// tokens a step ahead as well, gain nothing and need the registers.
+// 136 us with its routing: 79 (453 MB, 5.7 TB/s) and 43 us (226 MB, 5.3 TB/s); 8 tokens
+// on integers 403: 240 (1.47 GB, 6.1 TB/s) and 130 us (0.74 GB, 5.7 TB/s); 32 tokens
+// over 64 bf16 experts of 2048 x 1024 174-177: 95 (537 MB, 5.7 TB/s) and 66 us (268 MB,
+// 4.1 TB/s beside what is read of h); 3 tokens routed to 23 e4m3 experts of 2048 x 512
+// 28: 12.4 (50 MB) and 13.2 us (25 MB), each a workgroup's few steps and their latency.
+// Steps that got there, for the first two: 16 weight rows x 64 bytes a load and
+// tokens by masked loads 188 / 633, 8 rows x 128 bytes without masks 145 / 726, gate
+// and up (or two column tiles) sharing their tokens, one step at a time with the
+// next weights under way 157 / 467, few_down's steps shared evenly and the
+// grouping handed on 145 / 455, its columns by the CUs 136 / 405.  Two or more steps
+// at a time, or the tokens a step ahead as well, gain nothing and need the
+// registers.
 #include <type_traits>
 
 #include "common.h"
