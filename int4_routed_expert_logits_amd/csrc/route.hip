@@ -38,10 +38,12 @@ __device__ __forceinline__ void load_x4(const void* x, size_t idx, float (&v)[4]
 
 // Small batches: one wavefront per (expert, part of d).  Spreading each
 // router row over P parts puts E*P wavefronts in flight, enough to stream the
-// router matrix at HBM rate; every wavefront keeps up to 8 tokens' float64
+// router matrix at HBM rate; every wavefront keeps up to 4 tokens' float64
 // sums and writes part[t][e][p] (tree-summed over its lanes); more tokens are
-// other wavefronts'.
-constexpr int kTokGroup = 8;
+// other wavefronts', which find the router row in a cache.  us of moe_route with
+// 8, 4, 2 tokens a wavefront: 8 tokens over 256 experts of d = 6144 13.8 11.6 11.6, 32
+// tokens 22.9 20.3 21.9, over 64 of 2048 8.1 7.8 8.2, over 256 of 2048 14.8 15.1 16.8.
+constexpr int kTokGroup = 4;
 constexpr int kSplitMaxT = 32;  // larger batches use the matrix-core kernel
 
 // Partial float64 sums of tokens t0 .. t0+TG-1 against router row e
@@ -333,7 +335,6 @@ hipError_t launch_logits(int T, int d, int E, int P, const void* x, bool x_bf16,
     };
     if (T <= 1) return go(std::integral_constant<int, 1>{});
     if (T <= 2) return go(std::integral_constant<int, 2>{});
-    if (T <= 4) return go(std::integral_constant<int, 4>{});
     return go(std::integral_constant<int, kTokGroup>{});
   }
   const int L = ((d + P - 1) / P + kMK - 1) / kMK * kMK;
