@@ -55,9 +55,17 @@ constexpr int kMaxPairs = 256, kMaxIds = 1024, kCus = 256;
 constexpr int kIds = kMaxPairs / kWave;  // ids a lane holds
 
 // A load of a wavefront: 8 weight rows x 128 bytes.  The matrix instruction's 16
-// rows are those 8 with the first 64 bytes and again with the other 64, its 16
-// columns 8 tokens with the one and with the other half of x, so that of its
-// result the two 8 x 8 blocks on the diagonal are the two halves' sums.
+// rows are those 8 with the even 16-byte chunks and again with the odd ones, its
+// 16 columns 8 tokens with the one and with the other chunks of x, so that on its
+// result's diagonal lie 8 x 8 times both parts' sums.  Neighbouring lanes hold the
+// two parts, so that they read 32 bytes together.
+struct Lane {
+  int row, part, q;  // of 8 rows or tokens, of 2 chunks, of 4 pairs of chunks
+  int tail;          // 1: in the second 64 bytes of a load
+  __device__ __forceinline__ explicit Lane(int lane)
+      : row((lane >> 1) & 7), part(lane & 1), q(lane >> 4), tail(lane >> 5) {}
+  __device__ __forceinline__ int chunk() const { return q * 2 + part; }
+};
 template <int KIND>
 struct Fmt {
   static constexpr int kElem = KIND == kFewBf16 ? 2 : 1;
@@ -253,9 +261,9 @@ template <int KIND, int FR>
 struct Loaded {
   u32x4_t w[FR];
   // `last`: the step whose second half lies past the contraction's end; there the
-  // lanes of that half read the first
-  __device__ __forceinline__ void load(const Weights<FR>& at, uint32_t off, int s, int last, int half) {
-    if (KIND != kFewBf16 && s == last) off -= half * 64;
+  // lanes of that half (`tail`) read the first
+  __device__ __forceinline__ void load(const Weights<FR>& at, uint32_t off, int s, int last, int tail) {
+    if (KIND != kFewBf16 && s == last) off -= tail * 64;
 #pragma unroll
     for (int f = 0; f < FR; ++f) w[f] = load16(at.p[f] + static_cast<int64_t>(s) * 128, off);
   }
@@ -273,7 +281,7 @@ template <int KIND, int FR, int NB, int PARTS>
 __device__ __forceinline__ void steps(const Weights<FR>& at, uint32_t off, Loaded<KIND, FR>& first,
                                       int from, int to, int K, const Weights<FR>& next, int next_from,
                                       const uint8_t* x, const uint32_t (&xo)[NB], int64_t apart,
-                                      int half, f32x4_t (&acc)[FR][NB]) {
+                                      int tail, f32x4_t (&acc)[FR][NB]) {
   using F = Fmt<KIND>;
   constexpr int kPer = KIND == kFewBf16 ? 1 : 2;  // matrix instructions per load and token
   const int last = K % F::kStep ? K / F::kStep : -1;
@@ -286,7 +294,7 @@ __device__ __forceinline__ void steps(const Weights<FR>& at, uint32_t off, Loade
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
           uint32_t o = xo[b] + i * 16;
-          if (KIND != kFewBf16 && s == last) o -= half * (F::kHalf * 2);
+          if (KIND != kFewBf16 && s == last) o -= tail * (F::kHalf * 2);
           v[i][b][p] = load16(x + p * apart + static_cast<int64_t>(s) * (F::kStep * 2), o);
         }
   };
@@ -298,7 +306,7 @@ __device__ __forceinline__ void steps(const Weights<FR>& at, uint32_t off, Loade
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int p = 0; p < PARTS; ++p)
-            if (half) v[i][b][p] = u32x4_t{0, 0, 0, 0};
+            if (tail) v[i][b][p] = u32x4_t{0, 0, 0, 0};
     }
 #pragma unroll
     for (int f = 0; f < FR; ++f) {
@@ -330,25 +338,24 @@ __device__ __forceinline__ void steps(const Weights<FR>& at, uint32_t off, Loade
   for (int s = from; s < to; s += 2) {
     const bool two = s + 1 < to, more = s + 2 < to;
     tokens(s);
-    second.load(at, off, min(s + 1, to - 1), last, half);
+    second.load(at, off, min(s + 1, to - 1), last, tail);
     __builtin_amdgcn_sched_barrier(0);
     work(first, s);
     __builtin_amdgcn_sched_barrier(0);
     if (two) tokens(s + 1);
-    first.load(more ? at : next, off, more ? s + 2 : next_from, last, half);
+    first.load(more ? at : next, off, more ? s + 2 : next_from, last, tail);
     __builtin_amdgcn_sched_barrier(0);
     if (two) work(second, s + 1);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// The sums of a fragment's two halves: column 4 (lane / 16) + j of token lane % 16
-// in lanes of the first 32 with a token below 8.
-__device__ __forceinline__ bool owns_sums(int lane) { return lane < 32 && !(lane & 8); }
-__device__ __forceinline__ f32x4_t both_halves(f32x4_t v) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] += __shfl_down(v[j], 40, kWave);
-  return v;
+// The sum of a fragment's two parts for column ln.chunk() of token ln.row: a lane's
+// results are columns 2 q and 2 q + 1 of its own part, then of none; its neighbour
+// has the other part of both.
+__device__ __forceinline__ float both_parts(f32x4_t v, const Lane& ln) {
+  const float keep = ln.part ? v[3] : v[0], give = ln.part ? v[1] : v[2];
+  return keep + __uint_as_float(dpp_u32<0xB1>(__float_as_uint(give)));  // the neighbour's
 }
 
 // ---------------------------------------------------------------------------
@@ -386,7 +393,7 @@ __global__ __launch_bounds__(kGuThreads) void few_gate_up(FewLayer g, int tiles)
     if (e < 0) return;
     n = pairs_of(ids, e, lane, lists[wv]);
   }
-  const int i8 = lane & 7, half = (lane >> 3) & 1, q = lane >> 4;
+  const Lane ln(lane);
   const uint8_t* wbase = static_cast<const uint8_t*>(shared ? g.shared_gate_up : g.gate_up);
   const float* sbase = shared ? g.shared_gate_up_scales : g.gate_up_scales;
   Weights<kGuFrags> at;
@@ -398,12 +405,12 @@ __global__ __launch_bounds__(kGuThreads) void few_gate_up(FewLayer g, int tiles)
                                     : sbase + (static_cast<int64_t>(e) * ((2 * g.f + kBlock - 1) / kBlock) +
                                                row / kBlock) * ((g.d + kBlock - 1) / kBlock);
   }
-  const uint32_t off = static_cast<uint32_t>(i8 * g.d * F::kElem + half * 64 + q * 16);
+  const uint32_t off = static_cast<uint32_t>(ln.row * g.d * F::kElem + ln.chunk() * 16);
   const int all = (g.d + F::kStep - 1) / F::kStep;
   const int from = all * wv / kGuWaves, to = all * (wv + 1) / kGuWaves;
   const int last = g.d % F::kStep ? g.d / F::kStep : -1;
   Loaded<KIND, kGuFrags> w;
-  w.load(at, off, min(from, all - 1), last, half);
+  w.load(at, off, min(from, all - 1), last, ln.tail);
   for (int m0 = 0; m0 < n; m0 += kPassRows) {
     auto pass = [&](auto nb) {
       constexpr int NB = decltype(nb)::value;
@@ -411,22 +418,18 @@ __global__ __launch_bounds__(kGuThreads) void few_gate_up(FewLayer g, int tiles)
       uint32_t xo[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int r = min(m0 + b * 8 + i8, n - 1);
+        const int r = min(m0 + b * 8 + ln.row, n - 1);
         const int token = shared ? r : list[r] / g.k;
-        xo[b] = static_cast<uint32_t>(token * g.d + half * F::kHalf + q * F::kChunk) * 2;
+        xo[b] = static_cast<uint32_t>(token * g.d + ln.chunk() * F::kChunk) * 2;
         acc[0][b] = acc[1][b] = f32x4_t{0, 0, 0, 0};
       }
       steps<KIND, kGuFrags, NB, 1>(at, off, w, from, to, g.d, at, min(from, all - 1),
-                         static_cast<const uint8_t*>(g.x), xo, 0, half, acc);
+                         static_cast<const uint8_t*>(g.x), xo, 0, ln.tail, acc);
 #pragma unroll
       for (int f = 0; f < kGuFrags; ++f)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const f32x4_t v = both_halves(acc[f][b]);
-          if (owns_sums(lane))
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[wv][f][b * 8 + i8][q * 4 + j] = v[j];
-        }
+        for (int b = 0; b < NB; ++b)
+          part[wv][f][b * 8 + ln.row][ln.chunk()] = both_parts(acc[f][b], ln);
     };
     if constexpr (MANY) {
       if (n - m0 > 8)
@@ -510,8 +513,8 @@ __global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g, int splits) {
   const int wg_begin = first_step(split * kDnWaves, waves, total, grain);
   const int wg_end = first_step((split + 1) * kDnWaves, waves, total, grain);
 
-  const int i8 = lane & 7, half = (lane >> 3) & 1, q = lane >> 4;
-  const uint32_t off = static_cast<uint32_t>(i8 * g.f * F::kElem + half * 64 + q * 16);
+  const Lane ln(lane);
+  const uint32_t off = static_cast<uint32_t>(ln.row * g.f * F::kElem + ln.chunk() * 16);
   const int last = g.f % F::kStep ? g.f / F::kStep : -1;
   auto weights_of = [&](int grp, int e) {
     const bool shared = grp < g.shared;
@@ -535,7 +538,7 @@ __global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g, int splits) {
   if (begin < end) {  // the first weights, ahead of the rest of the table
     if (grp >= g.shared) e = __builtin_amdgcn_readfirstlane(table->active[grp - g.shared]);
     at = weights_of(grp, e);
-    w.load(at, off, begin - grp * all, last, half);
+    w.load(at, off, begin - grp * all, last, ln.tail);
   }
   for (int i = t; i < static_cast<int>(sizeof(FewTable) / 16); i += kDnThreads)
     reinterpret_cast<u32x4_t*>(&tb)[i] = reinterpret_cast<const u32x4_t*>(table)[i];
@@ -565,28 +568,25 @@ __global__ __launch_bounds__(kDnThreads) void few_down(FewLayer g, int splits) {
         uint32_t xo[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const int r = min(m0 + b * 8 + i8, n - 1);
+          const int r = min(m0 + b * 8 + ln.row, n - 1);
           row[b] = shared ? pairs + r : tb.pair[first + r];
-          xo[b] = static_cast<uint32_t>(row[b] * g.f + half * F::kHalf + q * F::kChunk) * 2;
+          xo[b] = static_cast<uint32_t>(row[b] * g.f + ln.chunk() * F::kChunk) * 2;
 #pragma unroll
           for (int f = 0; f < FR; ++f) acc[f][b] = f32x4_t{0, 0, 0, 0};
         }
         steps<KIND, FR, NB, PARTS>(at, off, w, from, to, g.f, again ? at : next,
                                again ? from : s < end ? 0 : from,
-                               reinterpret_cast<const uint8_t*>(g.h), xo, g.h_apart * 2, half, acc);
+                               reinterpret_cast<const uint8_t*>(g.h), xo, g.h_apart * 2, ln.tail, acc);
 #pragma unroll
         for (int f = 0; f < FR; ++f) {
-          f32x4_t sc{1, 1, 1, 1};
+          float sc = 1.0f;
           if constexpr (KIND == kFewInt8)
-            sc = *reinterpret_cast<const f32x4_t*>(sbase + static_cast<int64_t>(e) * g.d +
-                                                   min(n0 + f * kCols, g.d - kCols) + (q & 1) * 4);
+            sc = sbase[static_cast<int64_t>(e) * g.d + min(n0 + f * kCols, g.d - kCols) + ln.chunk()];
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const f32x4_t v = both_halves(acc[f][b]) * sc;
-            const int r = m0 + b * 8 + i8;
-            if (owns_sums(lane) && r < n)
-              *reinterpret_cast<f32x4_t*>((from == 0 ? sums[row[b]] : edge[wv][r]) + f * kCols +
-                                          q * 4) = v;
+            const float v = both_parts(acc[f][b], ln) * sc;
+            const int r = m0 + b * 8 + ln.row;
+            if (r < n) (from == 0 ? sums[row[b]] : edge[wv][r])[f * kCols + ln.chunk()] = v;
           }
         }
       };
@@ -670,9 +670,10 @@ struct DownPlan {
 // workgroups that split the steps (3 us and a launch) costs less than CUs without
 // work: of the layouts that use most CUs, the one with two fragments or the
 // fewest more.  Steps are split where that leaves a wavefront kSplitSteps steps
-// if every pair has an expert of its own, in short calls too (28 tokens over 5
-// experts of 128 x 3584: 104 us without, 48 so).
-constexpr int kMaxSplits = 16, kSplitSteps = 4, kLongSteps = 256, kMaxFrags = 4;
+// if every pair has an expert of its own, in short calls too.  us without, with 4
+// and with 2: 28 tokens over 5 experts of 128 x 3584 104, 48, 38; 26 over 31 of 256 x
+// 640 34 (4 does not split them), 29; 2 over 59 of 320 x 704 16 (likewise), 18.
+constexpr int kMaxSplits = 16, kSplitSteps = 2, kLongSteps = 256, kMaxFrags = 4;
 DownPlan down_plan(int T, int k, int d, int f, int E, bool shared, int step) {
   const int pairs = T * k, cols = d / kCols;
   const int64_t steps =
