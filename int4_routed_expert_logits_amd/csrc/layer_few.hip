@@ -659,20 +659,25 @@ struct DownPlan {
 };
 
 // A workgroup for each CU, or as many of them as go: us of the layer with 1, 2, 3, 4
-// fragments, one token on bf16 over 64 experts of f = 1024 and 8 on integers:
-//   d = 2048  26.9  28.1  30.1  31.8 and  73  69  75  69
-//   d = 2560  39.0  33.5  33.6  35.4     107  91  85  83
-//   d = 4096  49.9  44.5  47.9  47.3     127 114 122 114
-//   d = 6144  71.4  69.2  62.4  64.1     184 176 155 162
+// fragments, 1 token on bf16, 8 on integers and 32 on bf16 over 64 experts of f = 1024
+// (2048 where d = 6144):
+//   d = 2048  25.7  26.8  27.7  27.8 and  70  67  70  68 and 168 160 170 155
+//   d = 2560  37.5  31.8  32.2  32.8      98  82  77  77     248 218 197 190
+//   d = 4096  48.3  43.6  45.0  46.2     122 107 114 110     321 291 310 284
+//   d = 6144   119   117   110   111     320 304 276 284     930 929 845 857
 // Short calls (fewer than kLongSteps steps of all experts) take the fewest
 // fragments that suffice.  In longer ones what is read of h counts beside the
 // weights, two fragments share it, and a third kernel that joins the sums of
 // workgroups that split the steps (3 us and a launch) costs less than CUs without
 // work: of the layouts that use most CUs, the one with two fragments or the
-// fewest more.  Steps are split where that leaves a wavefront kSplitSteps steps
-// if every pair has an expert of its own, in short calls too.  us without, with 4
-// and with 2: 28 tokens over 5 experts of 128 x 3584 104, 48, 38; 26 over 31 of 256 x
-// 640 34 (4 does not split them), 29; 2 over 59 of 320 x 704 16 (likewise), 18.
+// fewest more, or the most for many tokens on bf16 with 16 steps an expert (8 steps,
+// 32 tokens over 128 of 1024 x 512 76.8 us with two, 80.0 with four; 12 tokens over 64
+// of 2048 x 1024 121 and 123, 20 over 16 of 4096 x 4096 353 and 323; codes, which need more
+// registers, 32 over 64 of 2048 x 1024 110 and 123).  Steps are split where that
+// leaves a wavefront kSplitSteps steps if every pair has an expert of its own, in
+// short calls too.  us without, with 4 and with 2: 28 tokens over 5 experts of
+// 128 x 3584 104, 48, 38; 26 over 31 of 256 x 640 34 (4 does not split them), 29; 2
+// over 59 of 320 x 704 16 (likewise), 18.
 constexpr int kMaxSplits = 16, kSplitSteps = 2, kLongSteps = 256, kMaxFrags = 4;
 DownPlan down_plan(int T, int k, int d, int f, int E, bool shared, int step) {
   const int pairs = T * k, cols = d / kCols;
@@ -688,10 +693,11 @@ DownPlan down_plan(int T, int k, int d, int f, int E, bool shared, int step) {
   const int least = (cols + kCus - 1) / kCus;
   DownPlan best{least, splits_of(least)};
   if (steps < kLongSteps) return best;
+  const bool most = step == Fmt<kFewBf16>::kStep && T > 16 && f / step >= 16;
   auto used = [&](const DownPlan& p) { return (cols + p.frags - 1) / p.frags * p.splits; };
   for (int frags = least + 1; frags <= kMaxFrags; ++frags) {
     const DownPlan p{frags, splits_of(frags)};
-    if (used(p) > used(best) || (used(p) == used(best) && best.frags == 1)) best = p;
+    if (used(p) > used(best) || (used(p) == used(best) && (most || best.frags == 1))) best = p;
   }
   return best;
 }
