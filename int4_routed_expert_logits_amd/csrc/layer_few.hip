@@ -21,19 +21,23 @@
 // All sums are float32, in an order that depends on the sizes and the routing
 // alone.
 //
-// Measured: one token over 8 of 256 bf16 experts of 6144 x 2048 and a shared one
-// 136 us with its routing: 79 (453 MB, 5.7 TB/s) and 43 us (226 MB, 5.3 TB/s); 8 tokens
-// on integers 403: 240 (1.47 GB, 6.1 TB/s) and 130 us (0.74 GB, 5.7 TB/s); 32 tokens
-// over 64 bf16 experts of 2048 x 1024 174-177: 95 (537 MB, 5.7 TB/s) and 66 us (268 MB,
-// 4.1 TB/s beside what is read of h); 3 tokens routed to 23 e4m3 experts of 2048 x 512
-// 28: 12.4 (50 MB) and 13.2 us (25 MB), each a workgroup's few steps and their latency.
+// Measured (the kernels' own times under the profiler, which runs some per cent
+// slower): one token over 8 of 256 bf16 experts of 6144 x 2048 and a shared one 134 us
+// with its routing, 80 (453 MB, 5.7 TB/s) and 43 us (226 MB, 5.3 TB/s); 8 tokens on
+// integers 373-388, 253 (1.47 GB, 5.8 TB/s) and 134 us (0.74 GB, 5.5 TB/s); 32 tokens
+// over 64 bf16 experts of 2048 x 1024 159-162, 96 (537 MB, 5.6 TB/s) and 54 us (268 MB,
+// 4.9 TB/s beside what is read of h); 3 tokens routed to 23 e4m3 experts of 2048 x 512
+// 25, 12.5 (50 MB) and 12.7 us (25 MB), each a workgroup's few steps and their latency.
 // Steps that got there, for the first two: 16 weight rows x 64 bytes a load and
 // tokens by masked loads 188 / 633, 8 rows x 128 bytes without masks 145 / 726, gate
 // and up (or two column tiles) sharing their tokens, one step at a time with the
 // next weights under way 157 / 467, few_down's steps shared evenly and the
-// grouping handed on 145 / 455, its columns by the CUs 136 / 405.  Two or more steps
-// at a time, or the tokens a step ahead as well, gain nothing and need the
-// registers.
+// grouping handed on 145 / 455, its columns by the CUs 136 / 405, neighbouring lanes reading 32 bytes
+// together, where each had read 16 of another row and the cache took an access for
+// every lane, 134 / 385.  Two or more steps at a time, or the tokens a step ahead as
+// well, gain nothing and need the registers; several tiles of h a workgroup cost
+// 2 to 4% in short calls and gain 4% on e4m3 in long ones; a second workgroup per CU
+// of few_down costs 2 to 7%.
 #include <type_traits>
 
 #include "common.h"
