@@ -5,8 +5,8 @@
  * (or a model) in one call, with float32 or 8-bit moments.  Conventions as in
  * moe_int4.h: caller-owned device memory, work enqueued on `stream`, nothing
  * allocated, no state but the caller's, arguments checked before anything is
- * enqueued.  A step repeated on the same state gives the same bits, however the
- * tensors are listed.
+ * enqueued.  A step repeated on the same state with the same number gives the same
+ * bits, however the tensors are listed.
  */
 #ifndef MOE_INT4_ADAMW_H
 #define MOE_INT4_ADAMW_H
@@ -34,11 +34,22 @@ extern "C" {
  * t * 2^e with e = max(c / 32 - 1, 0) and t = c - 32 e (0..63 in steps of 1, then 6
  * significant bits, up to 4032).  Scales are the smallest powers of two, 2^-126 at
  * least, that keep a block's largest |m| within 448 and largest sqrt(v) within 4032
- * (1 for a block of zeros); codes are the nearest, ties to even, but not 0 for a v
- * that is not 0.  Codes and scales of zero are moments of zero.  A step that would
- * move sqrt(v) by less than half of its last place (0.8 to 1.6% of it; for beta2 =
- * 0.999 a g^2 within about 17 times v) leaves it where it is; m, with beta1 = 0.9,
- * likewise up to 3 to 6%.  Where a moment is not finite, m's code is NaN and the
+ * (1 for a block of zeros); no code is 0 for a v that is not 0.  Codes and scales of
+ * zero are moments of zero.
+ *  beta1 > 0.9 or beta2 > 0.95 (0.999 among them): a code is one of the two next to
+ *    its value, drawn by a hash of the step's number and the element's index in its
+ *    tensor, so that the expected m and v are the values themselves.  Over 3000
+ *    steps of normal, constant and 20 times shrinking gradients with beta2 from
+ *    0.95 to 0.9999 the updates' norm stays within 6% of the one with float32
+ *    moments.  A single root strays by 6 to 8% of itself down to a thirtieth of its
+ *    block's largest, by 32% at a thousandth; one below 1 / 4032 of it is held as
+ *    that much or more.
+ *  else: the nearest code, ties to even.  A moment that a step would move by less
+ *    than half a place (m 3 to 6%, sqrt(v) 0.8 to 1.6%) stays where it is, so at beta1 =
+ *    0.9 and beta2 = 0.95 updates come out 1% too large for normal gradients, and up to
+ *    13% too small for ones that hardly change; a beta2 a little above 0.95 takes
+ *    the other rounding.
+ * Where a moment is not finite, m's code is NaN and the
  * whole block's v_scale. */
 typedef struct {
   int64_t n;

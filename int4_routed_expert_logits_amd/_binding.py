@@ -906,7 +906,8 @@ class AdamWTensors:
 def moe_adamw(tensors: AdamWTensors, step, lr: float, beta1: float = 0.9, beta2: float = 0.999,
               eps: float = 1e-8, weight_decay: float = 0.0, grad_scale=None, stream=None):
     """One step, in place.  step: device int64 [1], 1 for the first (the caller
-    advances it); grad_scale: device f32 [1] that gradients are multiplied by."""
+    advances it; the codes of 8-bit moments are drawn by it where beta1 > 0.9 or
+    beta2 > 0.95); grad_scale: device f32 [1] that gradients are multiplied by."""
     fn = "moe_adamw"
     if list(map(_data_ptr, tensors.live)) != tensors.at:
         raise ValueError(f"{fn}: a tensor lies elsewhere than when the list was made")

@@ -16,10 +16,28 @@
 // that is not zero never gets code 0: m, whose codes reach further down, would
 // then be divided by eps alone.
 //
+// How codes are rounded.  A step moves v by (1 - b2)(g'^2 - v) at most and m by
+// (1 - b1)(g' - m); rounded to nearest, a code stays where it is if that is less
+// than half a place, in the next step too, and a moment that should fall or grow
+// slowly never does.  So the codes of slow moments are rounded up or down with the
+// probability that makes the expected m and the expected v (not its root) the ones
+// rounded, the draw a hash of the step's number and the element's place: the same
+// state gives the same bits, and over steps the errors cancel.  A root's own spread
+// from it is 6 to 8% down to a thirtieth of its block's largest, 10% at a
+// hundredth, 32% at a thousandth.  Norm of the
+// update over the one with float32 moments after 2000 steps (nearest / by the hash,
+// b1 = 0.9; normal gradients, constant ones of mixed sizes, and normal ones 20
+// times smaller after a third):
+//   b2 = 0.95   1.01 / 1.00   0.88 / 1.00   1.01 / 1.00
+//   b2 = 0.99   0.61 / 1.01   1.34 / 1.00   0.03 / 1.01
+//   b2 = 0.999  1.49 / 1.01   3.39 / 1.00   0.69 / 1.05
+// Up to b1 = 0.9 and b2 = 0.95 codes go to the nearest, which needs fewer
+// instructions (1371 against 1474 us for 402M elements with masters).
+//
 // Bound by memory: 402M elements of bf16 with masters take 2.25 ms (30 bytes each,
-// 5.4 TB/s), with 8-bit moments 1.37 (18 bytes, 5.3); few elements by the launch
-// (16 vectors of 6144: 3.5 us).  A wavefront takes one block of 256 elements, 4 of
-// each lane: with so many wavefronts in flight, four blocks each before the
+// 5.4 TB/s), with 8-bit moments 1.37 (18 bytes, 5.3; hashed 1.47); few elements by
+// the launch (16 vectors of 6144: 3.5 us).  A wavefront takes one block of 256
+// elements, 4 of each lane: with so many wavefronts in flight, four blocks each before the
 // first is worked on gain nothing (2.26 and 1.41 ms), and starve where there are
 // few (90 odd tensors, 2.9M elements: 28 us, so 17).  The tensors' addresses are
 // kernel arguments, up to 64 tensors a launch: nothing is kept on the device, and
@@ -42,6 +60,7 @@ static_assert(kBlock == kAdamWBlock, "a wavefront holds a block");
 constexpr uint32_t kMaxGrid = 1u << 22;
 
 enum Store { kF32, kBf16, kMaster };  // the parameter: float32, bf16, bf16 with a float32 master
+enum Moments { kFloats, kNearest, kHashed };  // float32; codes, and how they are rounded
 
 // The tensors of a launch, by what their kind has of addresses: as many as the
 // 4 KB of a launch's arguments hold, and a wavefront's lanes.
@@ -131,6 +150,28 @@ __device__ __forceinline__ void store4(T* p, int64_t i, int64_t n, const T (&v)[
   }
 }
 
+// Bits of h spread over all 32: two products with odd numbers, shifts between.
+__host__ __device__ constexpr uint32_t mix(uint32_t h) {
+  h = (h ^ (h >> 16)) * 0x6A09E667u;
+  h = (h ^ (h >> 15)) * 0x9E3779B9u;
+  return h ^ (h >> 16);
+}
+// Two numbers in (0, 1), 16 bits and a half each: of m's code, of v's.
+struct Draw {
+  float m, v;
+};
+__device__ __forceinline__ Draw draw(uint32_t h) {
+  return {(static_cast<float>(h & 0xFFFFu) + 0.5f) * 0x1p-16f,
+          (static_cast<float>(h >> 16) + 0.5f) * 0x1p-16f};
+}
+
+// The e4m3 value next to a (|a| <= 448) below it or above, so that a is the mean
+// over u: |a| in places of its binade, at least 2^-9 each.
+__device__ __forceinline__ float e4m3_mean(float a, float u) {
+  const int e = max(static_cast<int>(__float_as_uint(a) >> 23 & 0xFFu) - 127, -6) - 3;
+  return copysignf(floorf(fabsf(a) * two_to(-e) + u) * two_to(e), a);
+}
+
 // Exponent n of the smallest scale 2^n >= 2^-126 with top <= limit * 2^n, limit =
 // 1.mant * 2^log: 0 for a top of zero.
 __device__ __forceinline__ int scale_exponent(uint32_t top, uint32_t mant, int log) {
@@ -140,7 +181,6 @@ __device__ __forceinline__ int scale_exponent(uint32_t top, uint32_t mant, int l
 }
 
 // What a lane holds of a block before its update.
-template <bool B8, int P, bool GBF16>
 struct Loaded {
   float p32[kV];
   uint16_t p16[kV], g16[kV];
@@ -149,13 +189,14 @@ struct Loaded {
   float ms, vs;
 };
 
-// The block from element `from` on.
-template <bool B8, int P, bool GBF16, bool WHOLE>
+// The block from element `from` on.  key: the step's, for the hash.
+template <int M, int P, bool GBF16, bool WHOLE>
 __device__ __forceinline__ void update(const AdamWTensor& q, const AdamWStep& h, float size,
-                                       float root, float gs, int64_t from, int lane) {
+                                       float root, float gs, uint32_t key, int64_t from, int lane) {
+  constexpr bool B8 = M != kFloats;
   const int64_t n = q.n;
   const int64_t i = from + lane * kV, blk = from / kBlock;
-  Loaded<B8, P, GBF16> x;
+  Loaded x;
   if (P == kF32) load4<WHOLE>(static_cast<const float*>(q.p), i, n, x.p32);
   if (P == kBf16) load4<WHOLE>(static_cast<const uint16_t*>(q.p), i, n, x.p16);
   if (P == kMaster) load4<WHOLE>(static_cast<const float*>(q.master), i, n, x.p32);
@@ -227,12 +268,25 @@ __device__ __forceinline__ void update(const AdamWTensor& q, const AdamWStep& h,
     const float im = two_to(-em), ir = ok ? two_to(-er) : 0.0f;
     uint8_t mc[kV], vc[kV];
     float a[kV];
+    const uint32_t place = M == kHashed ? static_cast<uint32_t>(i) +
+                                              mix(key + static_cast<uint32_t>(from >> 32))
+                                        : 0u;
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       a[j] = finite(m[j]) ? m[j] * im : __uint_as_float(0x7FC00000u);
       const float s = ok ? r[j] * ir : 0.0f;
       const int e = max(static_cast<int>(__float_as_uint(s) >> 23) - 126 - 6, 0);
-      const int code = 32 * e + static_cast<int>(rintf(s * two_to(-e)));
+      const float t = s * two_to(-e);
+      int code = 32 * e;
+      if constexpr (M == kHashed) {
+        const Draw u = draw(mix(place + j));
+        if (finite(m[j])) a[j] = e4m3_mean(a[j], u.m);
+        // t^2 as the mean of low^2 and (low + 1)^2
+        const float low = floorf(t);
+        code += static_cast<int>(low) + ((t - low) * (t + low) > u.v * (2.0f * low + 1.0f));
+      } else {
+        code += static_cast<int>(rintf(t));
+      }
       vc[j] = static_cast<uint8_t>(r[j] > 0.0f ? max(code, 1) : code);
     }
     int w = 0;
@@ -252,14 +306,16 @@ __device__ __forceinline__ void update(const AdamWTensor& q, const AdamWStep& h,
   }
 }
 
-template <bool B8, int P, bool GBF16>
-__global__ __launch_bounds__(kThreads) void adamw_step(const Batch<B8, P> b) {
+template <int M, int P, bool GBF16>
+__global__ __launch_bounds__(kThreads) void adamw_step(const Batch<M != kFloats, P> b) {
   static_assert(sizeof(b) <= 4096, "a launch's arguments");
   const int lane = threadIdx.x & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t my_first = b.first[min(lane, b.n)];
   const uint32_t chunks = b.first[b.n];
-  const double t = static_cast<double>(max(*b.s.step, int64_t(1)));
+  const int64_t step = max(*b.s.step, int64_t(1));
+  const double t = static_cast<double>(step);
+  const uint32_t key = mix(static_cast<uint32_t>(step) + mix(static_cast<uint32_t>(step >> 32)));
   const float size = static_cast<float>(b.s.lr / (1.0 - exp(t * b.s.log_beta1)));
   const float root = static_cast<float>(1.0 / sqrt(1.0 - exp(t * b.s.log_beta2)));
   const float gs = b.s.grad_scale ? *b.s.grad_scale : 1.0f;
@@ -269,27 +325,28 @@ __global__ __launch_bounds__(kThreads) void adamw_step(const Batch<B8, P> b) {
     const AdamWTensor q = b.get(at);
     const int64_t from = (static_cast<int64_t>(c - b.first[at]) * kWaves + wv) * kBlock;
     if (q.wide && from + kBlock <= q.n)
-      update<B8, P, GBF16, true>(q, b.s, size, root, gs, from, lane);
+      update<M, P, GBF16, true>(q, b.s, size, root, gs, key, from, lane);
     else if (from < q.n)
-      update<B8, P, GBF16, false>(q, b.s, size, root, gs, from, lane);
+      update<M, P, GBF16, false>(q, b.s, size, root, gs, key, from, lane);
   }
 }
 
-// How a tensor is held, as a number: its parameter, gradient and moments.
-constexpr int kKinds = 12;
-constexpr int kind_of(bool b8, int store, bool gbf16) { return (b8 * 3 + store) * 2 + gbf16; }
-int kind_of(const AdamWTensor& t) {
-  return kind_of(t.m_scales != nullptr, t.master ? kMaster : t.p_bf16 ? kBf16 : kF32, t.g_bf16);
+// How a tensor is held and its codes are rounded, as a number.
+constexpr int kKinds = 18;
+constexpr int kind_of(int moments, int store, bool gbf16) { return (moments * 3 + store) * 2 + gbf16; }
+int kind_of(const AdamWTensor& t, bool nearest) {
+  return kind_of(!t.m_scales ? kFloats : nearest ? kNearest : kHashed,
+                 t.master ? kMaster : t.p_bf16 ? kBf16 : kF32, t.g_bf16);
 }
 
 // The tensors of one kind, a batch of them a launch.
 template <int KIND>
 hipError_t go(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t stream) {
-  constexpr bool B8 = KIND / 6, GBF16 = KIND % 2;
-  constexpr int P = KIND / 2 % 3;
-  static_assert(KIND == kind_of(B8, P, GBF16));
+  constexpr bool GBF16 = KIND % 2;
+  constexpr int M = KIND / 6, P = KIND / 2 % 3;
+  static_assert(KIND == kind_of(M, P, GBF16));
   constexpr int64_t per = kWaves * kBlock;
-  Batch<B8, P> b;
+  Batch<M != kFloats, P> b;
   b.n = 0;
   b.first[0] = 0;
   b.s = s;
@@ -297,13 +354,13 @@ hipError_t go(const AdamWSource& src, int n, const AdamWStep& s, hipStream_t str
     if (b.n == 0) return hipSuccess;
     const uint32_t chunks = b.first[b.n];
     const dim3 grid(chunks < kMaxGrid ? chunks : kMaxGrid), block(kThreads);
-    const hipError_t e = launch(adamw_step<B8, P, GBF16>, grid, block, 0, stream, b);
+    const hipError_t e = launch(adamw_step<M, P, GBF16>, grid, block, 0, stream, b);
     b.n = 0;
     return e;
   };
   for (int i = 0; i < n; ++i) {
     const AdamWTensor t = src.get(src.tensors, i);
-    if (t.n == 0 || kind_of(t) != KIND) continue;
+    if (t.n == 0 || kind_of(t, s.nearest) != KIND) continue;
     const int64_t chunks = (t.n + per - 1) / per;
     if (b.n == b.kMost || (b.n > 0 && b.first[b.n] + chunks > INT32_MAX)) {
       const hipError_t e = flush();
@@ -328,7 +385,7 @@ hipError_t launch_adamw(const AdamWSource& src, int n, const AdamWStep& s, hipSt
   uint32_t present = 0;
   for (int i = 0; i < n; ++i) {
     const AdamWTensor t = src.get(src.tensors, i);
-    if (t.n != 0) present |= 1u << kind_of(t);
+    if (t.n != 0) present |= 1u << kind_of(t, s.nearest);
   }
   return go_each(present, src, n, s, stream, std::make_integer_sequence<int, kKinds>{});
 }

@@ -15,6 +15,8 @@ using moe::aligned;
 
 constexpr int32_t kMaxTensors = 1 << 20;
 constexpr int64_t kMaxElements = int64_t(1) << 40;
+// the betas up to which codes of moments go to the nearest
+constexpr double kNearestBeta1 = 0.9, kNearestBeta2 = 0.95;
 
 moe_status check_tensor(const moe_adamw_tensor& t) {
   if (t.n < 0) return MOE_ERR_SHAPE;
@@ -90,6 +92,7 @@ moe_status moe_adamw(const moe_adamw_tensor* tensors, int32_t n_tensors, const i
   s.rest2 = static_cast<float>(1.0 - beta2);
   s.eps = static_cast<float>(eps);
   s.keep = static_cast<float>(1.0 - lr * weight_decay);
+  s.nearest = beta1 <= kNearestBeta1 && beta2 <= kNearestBeta2;
   return moe::hip_status(moe::launch_adamw(moe::AdamWSource{tensors, get_tensor}, n_tensors, s,
                                            static_cast<hipStream_t>(stream)));
 }

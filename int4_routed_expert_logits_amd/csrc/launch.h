@@ -196,6 +196,7 @@ struct AdamWStep {
   const float* grad_scale;
   double lr, log_beta1, log_beta2;
   float beta1, rest1, beta2, rest2, eps, keep;  // rest = 1 - beta, keep = 1 - lr * decay
+  bool nearest;  // codes of moments go to the nearest, else by the hash
 };
 struct AdamWSource {
   const void* tensors;
