@@ -49,8 +49,11 @@ extern "C" {
  *    0.9 and beta2 = 0.95 updates come out 1% too large for normal gradients, and up to
  *    13% too small for ones that hardly change; a beta2 a little above 0.95 takes
  *    the other rounding.
- * Where a moment is not finite, m's code is NaN and the
- * whole block's v_scale. */
+ * Where m is not finite its code is NaN.  Where v is not (g^2 past float32's largest
+ * is enough), its code is 255 and its block's v_scale a NaN whose last 8 bits are the
+ * biased exponent of the scale that the block's other codes, up to 254, have: such
+ * an element's parameter is what it is with float32 moments, and no other element
+ * changes (its m is held within 448 m_scale and does not count for that).  (A v_scale of any NaN whose last 8 bits are 0 makes the whole block NaN.) */
 typedef struct {
   int64_t n;
   void* p;

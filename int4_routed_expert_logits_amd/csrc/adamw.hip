@@ -14,7 +14,10 @@
 // t 2^e, e 0..6 and t up to 63 (from 32 on where e > 0): 6 significant bits over a
 // range of 2^12, the scale the smallest that keeps the block within 4032.  A root
 // that is not zero never gets code 0: m, whose codes reach further down, would
-// then be divided by eps alone.
+// then be divided by eps alone.  Where an element's root is not finite, its block's
+// scale is a NaN that carries the scale's exponent in its last 8 bits, and code
+// 255 stands for infinity (the other codes keep below it): that element stays so
+// (its m has no part in m's scale), the 255 beside it are as they would be without it.
 //
 // How codes are rounded.  A step moves v by (1 - b2)(g'^2 - v) at most and m by
 // (1 - b1)(g' - m); rounded to nearest, a code stays where it is if that is less
@@ -32,10 +35,10 @@
 //   b2 = 0.99   0.61 / 1.01   1.34 / 1.00   0.03 / 1.01
 //   b2 = 0.999  1.49 / 1.01   3.39 / 1.00   0.69 / 1.05
 // Up to b1 = 0.9 and b2 = 0.95 codes go to the nearest, which needs fewer
-// instructions (1371 against 1474 us for 402M elements with masters).
+// instructions (1375 against 1530 us for 402M elements with masters).
 //
 // Bound by memory: 402M elements of bf16 with masters take 2.25 ms (30 bytes each,
-// 5.4 TB/s), with 8-bit moments 1.37 (18 bytes, 5.3; hashed 1.47); few elements by
+// 5.4 TB/s), with 8-bit moments 1.37 (18 bytes, 5.3; hashed 1.53); few elements by
 // the launch (16 vectors of 6144: 3.5 us).  A wavefront takes one block of 256
 // elements, 4 of each lane: with so many wavefronts in flight, four blocks each before the
 // first is worked on gain nothing (2.26 and 1.41 ms), and starve where there are
@@ -197,6 +200,7 @@ __device__ __forceinline__ void update(const AdamWTensor& q, const AdamWStep& h,
   const int64_t n = q.n;
   const int64_t i = from + lane * kV, blk = from / kBlock;
   Loaded x;
+  bool marked = false;  // the block holds a root that is not finite
   if (P == kF32) load4<WHOLE>(static_cast<const float*>(q.p), i, n, x.p32);
   if (P == kBf16) load4<WHOLE>(static_cast<const uint16_t*>(q.p), i, n, x.p16);
   if (P == kMaster) load4<WHOLE>(static_cast<const float*>(q.master), i, n, x.p32);
@@ -209,6 +213,9 @@ __device__ __forceinline__ void update(const AdamWTensor& q, const AdamWStep& h,
     load4<WHOLE>(static_cast<const uint8_t*>(q.v), i, n, x.vc);
     x.ms = q.m_scales[blk];
     x.vs = q.v_scales[blk];
+    marked = !(x.vs == x.vs);
+    const uint32_t e = __float_as_uint(x.vs) & 0xFFu;
+    if (marked && e != 0u) x.vs = __uint_as_float(e << 23);
   } else {
     load4<WHOLE>(static_cast<const float*>(q.m), i, n, x.m32);
     load4<WHOLE>(static_cast<const float*>(q.v), i, n, x.v32);
@@ -226,7 +233,7 @@ __device__ __forceinline__ void update(const AdamWTensor& q, const AdamWStep& h,
     for (int j = 0; j < kV; ++j) {
       const int code = x.vc[j], e = max((code >> 5) - 1, 0);
       const float s = static_cast<float>((code - 32 * e) << e) * x.vs;
-      v[j] = s * s;
+      v[j] = marked && code == 255 ? __builtin_inff() : s * s;
     }
   } else {
 #pragma unroll
@@ -253,19 +260,25 @@ __device__ __forceinline__ void update(const AdamWTensor& q, const AdamWStep& h,
   }
   if (P != kBf16) store4<WHOLE>(static_cast<float*>(P == kMaster ? q.master : q.p), i, n, p);
   if (B8) {
-    uint32_t top_m = 0, top_r = 0;
+    uint32_t top_m, top_r;
+    auto tops = [&](auto counts) {
+      top_m = top_r = 0;
 #pragma unroll
-    for (int j = 0; j < kV; ++j)
-      if (WHOLE || i + j < n) {
-        if (finite(m[j])) top_m = max(top_m, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-        top_r = max(top_r, __float_as_uint(r[j]) & 0x7FFFFFFFu);
-      }
-    top_m = wave_max_u32(top_m);
-    top_r = wave_max_u32(top_r);
+      for (int j = 0; j < kV; ++j)
+        if ((WHOLE || i + j < n) && counts(j)) {
+          if (finite(m[j])) top_m = max(top_m, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+          top_r = max(top_r, __float_as_uint(r[j]) & 0x7FFFFFFFu);
+        }
+      top_m = wave_max_u32(top_m);
+      top_r = wave_max_u32(top_r);
+    };
+    tops([](int) { return true; });
+    const bool odd = top_r >= 0x7F800000u;
+    if (odd) tops([&](int j) { return finite(r[j]); });
     const int em = scale_exponent(top_m, 0x600000u, 8);   // 448 = 1.75 * 2^8
-    const int er = scale_exponent(top_r, 0x7C0000u, 11);  // 4032 = 1.96875 * 2^11
-    const bool ok = top_r < 0x7F800000u;
-    const float im = two_to(-em), ir = ok ? two_to(-er) : 0.0f;
+    // 4032 = 1.96875 * 2^11, or below code 255: 3968 = 1.9375 * 2^11
+    const int er = scale_exponent(top_r, odd ? 0x780000u : 0x7C0000u, 11);
+    const float im = two_to(-em), ir = two_to(-er);
     uint8_t mc[kV], vc[kV];
     float a[kV];
     const uint32_t place = M == kHashed ? static_cast<uint32_t>(i) +
@@ -274,7 +287,7 @@ __device__ __forceinline__ void update(const AdamWTensor& q, const AdamWStep& h,
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       a[j] = finite(m[j]) ? m[j] * im : __uint_as_float(0x7FC00000u);
-      const float s = ok ? r[j] * ir : 0.0f;
+      const float s = fminf(r[j] * ir, 4032.0f);  // a number where r is none, too
       const int e = max(static_cast<int>(__float_as_uint(s) >> 23) - 126 - 6, 0);
       const float t = s * two_to(-e);
       int code = 32 * e;
@@ -294,11 +307,21 @@ __device__ __forceinline__ void update(const AdamWTensor& q, const AdamWStep& h,
     w = __builtin_amdgcn_cvt_pk_fp8_f32(a[2], a[3], w, true);
 #pragma unroll
     for (int j = 0; j < kV; ++j) mc[j] = static_cast<uint8_t>(w >> (8 * j));
+    if (odd) {
+#pragma unroll
+      for (int j = 0; j < kV; ++j)
+        if (!finite(r[j])) {
+          vc[j] = 255;
+          // m moves nothing there; 0x7E is 448
+          if (finite(m[j]) && !(fabsf(m[j] * im) <= 448.0f)) mc[j] = m[j] < 0.0f ? 0xFE : 0x7E;
+        }
+    }
     store4<WHOLE>(static_cast<uint8_t*>(q.m), i, n, mc);
     store4<WHOLE>(static_cast<uint8_t*>(q.v), i, n, vc);
     if (lane == 0) {
       q.m_scales[blk] = two_to(em);
-      q.v_scales[blk] = ok ? two_to(er) : __uint_as_float(0x7FC00000u);
+      q.v_scales[blk] = odd ? __uint_as_float(0x7FC00000u | static_cast<uint32_t>(er + 127))
+                            : two_to(er);
     }
   } else {
     store4<WHOLE>(static_cast<float*>(q.m), i, n, m);

@@ -1,6 +1,7 @@
-"""Plain form, on the CPU, of the 8-bit moments of slow betas: codes rounded up or
-down by a hash of the step's number and the element's place, in the documented
-float32 operations; and what a run of AdamW steps does with them.
+"""Plain form, on the CPU, of 8-bit moments: codes rounded up or down by a hash of
+the step's number and the element's place (or, for step None, to the nearest), in
+the documented float32 operations; blocks with roots that are not finite; and what
+a run of AdamW steps does with them.
 
 The draws are two 16-bit numbers and a half each, so a code's probability is off by
 2^-17 at most."""
@@ -40,35 +41,54 @@ def scales(top, limit):
     return np.where(top == 0, 1.0, np.exp2(n)).astype(F)
 
 
-def m_codes(m, step, first=0):
-    """(e4m3 values, scales) of a float32 array whose first element is `first`."""
-    b = _blocks(m)
-    s = scales(np.abs(b).max(1), 448.0)
-    a = (np.abs(b) * (F(1) / s)[:, None]).reshape(-1)[:len(m)]  # a power of two: exact
+def m_codes(m, step, first=0, r=None):
+    """(e4m3 values, scales) of a float32 array whose first element is `first`; of
+    elements whose root r is not finite only the nearest within the others' scale."""
+    b = np.where(np.isfinite(m if r is None else m * F(0) + r), m, F(0))
+    s = scales(np.abs(_blocks(b)).max(1), 448.0)
+    # by a power of two: exact
+    a = np.abs(np.where(np.isfinite(m), m, F(0))) * np.repeat(F(1) / s, 256)[:len(m)]
+    a = np.minimum(a, F(448))
     place = np.exp2(np.maximum(exponent(a), -6) - 3).astype(F)
-    q = np.floor(a / place + draws(step, first, len(m))[0]) * place
-    return np.copysign(q, m).astype(F), s
+    t = a / place
+    q = (np.rint(t) if step is None else np.floor(t + draws(step, first, len(m))[0])) * place
+    return np.where(np.isfinite(m), np.copysign(q, m), F(np.nan)).astype(F), s
 
 
 def v_codes(r, step, first=0):
     """(codes, scales) of a float32 array of roots."""
-    b = _blocks(r)
-    s = scales(b.max(1), 4032.0)
-    a = (b * (F(1) / s)[:, None]).reshape(-1)[:len(r)]
+    b = np.where(np.isfinite(r), r, F(0))
+    odd = ~np.isfinite(_blocks(r)).all(1)
+    s = scales(_blocks(b).max(1), np.where(odd, 3968.0, 4032.0))
+    a = b * np.repeat(F(1) / s, 256)[:len(r)]
     e = np.maximum(exponent(a) - 5, 0)
     t = a * np.exp2(-e).astype(F)
     low = np.floor(t)
-    up = (t - low) * (t + low) > draws(step, first, len(r))[1] * (F(2) * low + F(1))
+    if step is None:
+        low, up = np.rint(t), False
+    else:
+        up = (t - low) * (t + low) > draws(step, first, len(r))[1] * (F(2) * low + F(1))
     c = 32 * e + low.astype(np.int32) + up
-    return np.where((r > 0) & (c == 0), 1, c).astype(np.uint8), s
+    c = np.where(np.isfinite(r), np.where((r > 0) & (c == 0), 1, c), 255)
+    marks = (U32(0x7FC00000) | (s.view(U32) >> U32(23))).view(F)
+    return c.astype(np.uint8), np.where(odd, marks, s)
+
+
+def m_of(q, s):
+    return q * np.repeat(s, 256)[:len(q)]
+
+
+def v_of(c, s):
+    """v of codes and their blocks' scales."""
+    odd, exp = np.isnan(s), s.view(U32) & U32(0xFF)
+    s = np.where(odd & (exp != 0), (exp << U32(23)).view(F), s)
+    r = root_values().astype(F)[c] * np.repeat(s, 256)[:len(c)]
+    return np.where(np.repeat(odd, 256)[:len(c)] & (c == 255), F(np.inf), r * r)
 
 
 def moments(m, r, step, first=0):
     """What the codes of m and of the root r stand for, as m and v."""
-    q, s = m_codes(m, step, first)
-    c, z = v_codes(r, step, first)
-    z = root_values().astype(F)[c] * np.repeat(z, 256)[:len(r)]
-    return q * np.repeat(s, 256)[:len(m)], z * z
+    return m_of(*m_codes(m, step, first, r)), v_of(*v_codes(r, step, first))
 
 
 KINDS = ("normal", "constant", "shrinking")

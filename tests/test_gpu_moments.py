@@ -114,6 +114,46 @@ def test_captured_steps_draw_by_their_number(gpu_lib):
             assert torch.equal(a[0].view(U8), b[0].view(U8)), i
 
 
+@pytest.mark.parametrize("beta2", [0.95, 0.999])
+@pytest.mark.parametrize("store", ["f32", "master"])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf"), 1e25])
+def test_elements_that_are_not_finite_spoil_no_other(gpu_lib, bad, store, beta2):
+    """One step with such gradients (the square of 1e25 is none of float32) and four
+    without: the moments by the form, the other parameters as in a clean run."""
+    n, at = 1000, [300, 999]
+    say(f"not finite {bad} {store} {beta2}")
+    same = torch.ones(n, dtype=torch.bool)
+    same[at] = False
+    runs = []
+    for spoilt in (True, False):
+        p, w, m, v, ms, vs = state(n, store)
+        g = torch.zeros(n, device="cuda")
+        q = moe.AdamWTensors([p], [g], [m], [v], [w] if store == "master" else None, [ms], [vs])
+        p32, m32, v32 = (np.zeros(n, F),) * 3
+        for t in range(1, 6):
+            g.normal_(generator=torch.Generator(device="cuda").manual_seed(t)).mul_(1e-2)
+            g[::256] = 1.0  # each block's largest
+            if spoilt and t == 1:
+                g[at] = bad
+            step = torch.tensor([t], dtype=torch.int64, device="cuda")
+            moe.moe_adamw(q, step, 1e-2, 0.9, beta2, 1e-8, 0.1)
+            with np.errstate(all="ignore"):
+                p32, m32, v32, r = ref.adamw32(p32, g.cpu().numpy(), m32, v32, t, 1e-2, 0.9, beta2, 1e-8, 0.1)
+                draw = None if beta2 == 0.95 else t
+                (mc, sm), (vc, sv) = mom.m_codes(m32, draw, 0, r), mom.v_codes(r, draw)
+                m32, v32 = mom.m_of(mc, sm), mom.v_of(vc, sv)
+            got = (w if store == "master" else p).cpu().numpy()
+            assert np.array_equal(got, p32, equal_nan=True), t
+            assert np.array_equal(m.float().cpu().numpy(), mc, equal_nan=True), t
+            assert np.array_equal(v.cpu().numpy(), vc), t
+            assert np.array_equal(vs.cpu().numpy().view(np.uint32), sv.view(np.uint32)), t
+        runs.append((p.cpu(), v.cpu(), vs.cpu()))
+    (p, v, vs), (p0, v0, _) = runs
+    assert torch.isnan(vs).tolist() == [False, True, False, True]
+    assert torch.equal(p[same], p0[same]) and torch.equal(v[same], v0[same])
+    assert torch.isfinite(p[~same]).all() == (bad == 1e25)
+
+
 def test_places_past_four_billion(gpu_lib):
     """The last blocks of 2^32 + 600 elements, by the form at their places."""
     n, tail = 2 ** 32 + 600, 600 + 512

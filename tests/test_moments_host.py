@@ -18,10 +18,7 @@ def hashed(m, r, step):
 
 
 def nearest(m, r, step):
-    q, s = ref.m_codes(m)
-    c, z = ref.v_codes(r)
-    z = ref.root_values().astype(F)[c] * np.repeat(z, 256)[:len(r)]
-    return q.astype(F) * np.repeat(s, 256)[:len(m)], z * z
+    return mom.moments(m, r, None)
 
 
 @pytest.mark.parametrize("sizes", list(SIZES))
@@ -68,6 +65,36 @@ def test_scales_are_those_of_the_nearest_codes():
                            np.nextafter(F(4032) * F(2) ** np.arange(-120, 100, 7), F(9e9)), [0, 3.3e38]]).astype(F)
     for limit in (448.0, 4032.0):
         assert np.array_equal(mom.scales(tops, limit), ref._scales(tops.astype(np.float64), limit).astype(F))
+
+
+def test_nearest_codes_are_those_found_by_search():
+    rng = np.random.default_rng(5)
+    m = (rng.standard_normal(1500) * np.exp(rng.uniform(-15, 0, 1500))).astype(F)
+    for got, want in zip(mom.m_codes(m, None) + mom.v_codes(np.abs(m), None),
+                         ref.m_codes(m) + ref.v_codes(np.abs(m))):
+        assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("step", [None, 3])
+def test_a_root_that_is_not_finite_keeps_to_itself(step):
+    """Its code is 255, its block's scale a NaN that holds the scale, and the others
+    mean what they mean without it, where it is not the largest."""
+    r = np.exp(np.random.default_rng(6).uniform(-6, 0, 700)).astype(F)
+    for bad in (np.nan, np.inf):
+        x = r.copy()
+        x[300] = bad
+        (c, s), (c0, s0) = mom.v_codes(x, step), mom.v_codes(r, step)
+        assert np.isnan(s).tolist() == [False, True, False] and c[300] == 255
+        same = np.arange(700) != 300
+        assert np.array_equal(c[same], c0[same]) and (c[256:512] == 255).sum() == 1
+        v = mom.v_of(c, s)
+        assert np.array_equal(v[same], mom.v_of(c0, s0)[same]) and v[300] == np.inf
+    # a root that would be code 255 takes the next scale beside a mark
+    x = np.array([4032, 5, np.inf], F)
+    c, s = mom.v_codes(x, step)
+    assert c[0] == 223 and mom.v_of(c, s)[0] == F(4032) ** 2 and mom.v_of(c, s)[2] == np.inf
+    # a NaN that holds no scale makes a block of NaN
+    assert np.isnan(mom.v_of(np.array([3, 0], np.uint8), np.array([np.nan], F))).all()
 
 
 def test_values_that_codes_hold_stay():
