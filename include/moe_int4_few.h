@@ -70,9 +70,9 @@ size_t moe_layer_few_workspace_bytes(const moe_shape* shape, int32_t T);
  * (17 bits, each off by 2^-17 of itself at most, where both are normal numbers).  A
  * bf16 out is thus off by 2^-17 sum |w D h| beside its own rounding, which is more
  * than half of its last place where that sum cancels by more than 2^8: an f32 out
- * does not have it.  Codes are summed before their scales are multiplied in, so
- * values within 2^9 sqrt(d) (gate and up) or sqrt(f) (down) of float32's largest give
- * infinities although the scaled result may be smaller. */
+ * does not have it.  Products with codes (up to 448 each) are summed before their
+ * scales are multiplied in: a sum that passes float32's largest is an infinity,
+ * also where the scaled result would not be. */
 moe_status moe_layer_few(const moe_shape* shape, int32_t T, const void* x, const float* w_router,
                          const float* bias, moe_weights kind, const moe_expert_weights* experts,
                          const moe_expert_weights* shared, int32_t* topk_idx, float* topk_w,

@@ -439,20 +439,21 @@ def moe_cache_layer_decode(cache: int, x, w_router, bias, shared, topk_idx, topk
 # ----------------------------------------------------------------------------
 
 # set by _types(), which every call below makes first (once: `_T or _types()`)
-_T = _raw_stream = _current_device = _INT8 = _INT64 = _data_ptr = None
+_T = _raw_stream = _current_device = _INT8 = _INT64 = _same_memory = None
 _CODES = {}  # torch type -> moe_dtype
 
 
 def _types():
     """(bf16, f32, either, int32, e4m3 code) as tuples of torch types."""
-    global _T, _raw_stream, _current_device, _INT8, _INT64, _data_ptr
+    global _T, _raw_stream, _current_device, _INT8, _INT64, _same_memory
     if _T is None:
         import torch
         # the stream's handle and the device's index themselves: building a torch
         # Stream takes as long as a launch
         _raw_stream = torch._C._cuda_getCurrentRawStream
         _current_device = _current_device or torch._C._cuda_getDevice
-        _INT8, _INT64, _data_ptr = (torch.int8,), (torch.int64,), torch.Tensor.data_ptr
+        _INT8, _INT64 = (torch.int8,), (torch.int64,)
+        _same_memory = torch._C._tensors_data_ptrs_at_indices_equal
         _CODES.update({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
         _T = ((torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32), (torch.int32,),
               (torch.float8_e4m3fn, torch.uint8))
@@ -830,8 +831,8 @@ class AdamWTensors:
     codes (m float8_e4m3fn or uint8, v uint8) and a float32 scale per 256 elements.
     masters: a float32 copy of each bf16 parameter, or None for all or for one.
     All on one GPU, without gaps, none overlapping one that the step writes.  A step
-    goes by the addresses taken here; it refuses a list of which a parameter or a
-    gradient has been given other memory since (`p.data = ...`)."""
+    goes by the addresses taken here; it refuses a list of which a tensor has been
+    given other memory since (`p.data = ...`, moments moved away and back)."""
 
     def __init__(self, params, grads, m, v, masters=None, m_scales=None, v_scales=None):
         fn = "AdamWTensors"
@@ -887,10 +888,8 @@ class AdamWTensors:
                 s.m, s.v = take("m", i, a, codes, shape, count), take("v", i, b, byte, shape, count)
                 s.m_scales = take("m_scales", i, sa, f32, blocks, blocks[0])
                 s.v_scales = take("v_scales", i, sb, f32, blocks, blocks[0])
-        # what a training loop may give other memory (looking at all of them takes a
-        # third of a step over small tensors: 80 ns each)
-        self.live = [*lists[0], *lists[2]]
-        self.at = list(map(_data_ptr, self.live))
+        live = [t for q in lists for t in q if t is not None]
+        self.live = (live, [t.data_ptr() for t in live], list(range(len(live))))
         # two spans overlap only if one of them does with the one that reaches
         # furthest among those that begin before it: of the written and of all
         end = [(0, -1), (0, -1)]
@@ -909,7 +908,7 @@ def moe_adamw(tensors: AdamWTensors, step, lr: float, beta1: float = 0.9, beta2:
     advances it; the codes of 8-bit moments are drawn by it where beta1 > 0.9 or
     beta2 > 0.95); grad_scale: device f32 [1] that gradients are multiplied by."""
     fn = "moe_adamw"
-    if list(map(_data_ptr, tensors.live)) != tensors.at:
+    if not _same_memory(*tensors.live):  # 60 ns each: a step over many small ones waits for it
         raise ValueError(f"{fn}: a tensor lies elsewhere than when the list was made")
     dev = tensors.device if tensors.n else step.get_device()
     _run(fn, dev, stream, tensors.array, tensors.n,

@@ -399,7 +399,8 @@ class AdamW:
     backward passes fill again): moments in float32 or, with bits=8, in codes, a
     float32 master of each bf16 parameter (masters=False: none), and the step's
     number on the device, so that a captured step counts on.  A saved state (count,
-    masters, m, v and the scales) is copied into these tensors."""
+    masters, m, v and the scales) is copied into these tensors: a step refuses ones
+    that were given other memory."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                  bits: int = 32, masters: bool = True):
@@ -407,19 +408,21 @@ class AdamW:
             raise ValueError(f"AdamW: moments of {bits} bits; 8 or 32")
         if not params:
             raise ValueError("AdamW: no parameters")
-        self.params, self.grads = list(params), list(grads)
+        self.params, self.grads = tuple(params), tuple(grads)
         dev = self.params[0].device
         new = lambda p, dt: torch.zeros(p.shape, dtype=dt, device=p.device)  # noqa: E731
-        self.masters = [p.detach().float() if masters and p.dtype == torch.bfloat16 else None
-                        for p in self.params]
+        # tuples: an entry put in later would not be the step's
+        self.masters = tuple(p.detach().float() if masters and p.dtype == torch.bfloat16 else None
+                             for p in self.params)
+        each = lambda make: tuple(make(p) for p in self.params)  # noqa: E731
         if bits == 32:
-            self.m, self.v = ([new(p, torch.float32) for p in self.params] for _ in range(2))
+            self.m, self.v = (each(lambda p: new(p, torch.float32)) for _ in range(2))
             self.m_scales = self.v_scales = None
         else:
-            self.m = [new(p, torch.float8_e4m3fn) for p in self.params]
-            self.v = [new(p, torch.uint8) for p in self.params]
+            self.m = each(lambda p: new(p, torch.float8_e4m3fn))
+            self.v = each(lambda p: new(p, torch.uint8))
             ones = lambda p: torch.ones(-(-p.numel() // 256), device=p.device)  # noqa: E731
-            self.m_scales, self.v_scales = ([ones(p) for p in self.params] for _ in range(2))
+            self.m_scales, self.v_scales = (each(ones) for _ in range(2))
         self.count = torch.zeros(1, dtype=torch.int64, device=dev)
         self.tensors = B.AdamWTensors(self.params, self.grads, self.m, self.v, self.masters,
                                       self.m_scales, self.v_scales)
