@@ -439,13 +439,13 @@ def moe_cache_layer_decode(cache: int, x, w_router, bias, shared, topk_idx, topk
 # ----------------------------------------------------------------------------
 
 # set by _types(), which every call below makes first (once: `_T or _types()`)
-_T = _raw_stream = _current_device = _INT8 = _INT64 = _same_memory = None
+_T = _raw_stream = _current_device = _INT8 = _INT64 = _same_memory = _written = None
 _CODES = {}  # torch type -> moe_dtype
 
 
 def _types():
     """(bf16, f32, either, int32, e4m3 code) as tuples of torch types."""
-    global _T, _raw_stream, _current_device, _INT8, _INT64, _same_memory
+    global _T, _raw_stream, _current_device, _INT8, _INT64, _same_memory, _written
     if _T is None:
         import torch
         # the stream's handle and the device's index themselves: building a torch
@@ -454,6 +454,7 @@ def _types():
         _current_device = _current_device or torch._C._cuda_getDevice
         _INT8, _INT64 = (torch.int8,), (torch.int64,)
         _same_memory = torch._C._tensors_data_ptrs_at_indices_equal
+        _written = torch.autograd.graph.increment_version
         _CODES.update({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
         _T = ((torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32), (torch.int32,),
               (torch.float8_e4m3fn, torch.uint8))
@@ -889,6 +890,8 @@ class AdamWTensors:
                 s.m_scales = take("m_scales", i, sa, f32, blocks, blocks[0])
                 s.v_scales = take("v_scales", i, sb, f32, blocks, blocks[0])
         live = [t for q in lists for t in q if t is not None]
+        # what a graph of autograd may have saved
+        self.kept = [t for q in lists[:2] for t in q if t is not None]
         self.live = (live, [t.data_ptr() for t in live], list(range(len(live))))
         # two spans overlap only if one of them does with the one that reaches
         # furthest among those that begin before it: of the written and of all
@@ -905,7 +908,8 @@ class AdamWTensors:
 def moe_adamw(tensors: AdamWTensors, step, lr: float, beta1: float = 0.9, beta2: float = 0.999,
               eps: float = 1e-8, weight_decay: float = 0.0, grad_scale=None, stream=None):
     """One step, in place.  step: device int64 [1], 1 for the first (the caller
-    advances it; the codes of 8-bit moments are drawn by it where beta1 > 0.9 or
+    advances it; the parameters and masters count as modified in place, but not by
+    a captured step's replays; the codes of 8-bit moments are drawn by it where beta1 > 0.9 or
     beta2 > 0.95); grad_scale: device f32 [1] that gradients are multiplied by."""
     fn = "moe_adamw"
     if not _same_memory(*tensors.live):  # 60 ns each: a step over many small ones waits for it
@@ -914,3 +918,4 @@ def moe_adamw(tensors: AdamWTensors, step, lr: float, beta1: float = 0.9, beta2:
     _run(fn, dev, stream, tensors.array, tensors.n,
          _take(fn, dev, "step", step, _INT64, (1,)), lr, beta1, beta2, eps, weight_decay,
          _take(fn, dev, "grad_scale", grad_scale, _T[1], (1,)))
+    _written(tensors.kept)  # a backward pass over values of before the step is refused
