@@ -36,7 +36,7 @@ extern "C" {
  * least, that keep a block's largest |m| within 448 and largest sqrt(v) within 4032
  * (1 for a block of zeros); no code is 0 for a v that is not 0.  Codes and scales of
  * zero are moments of zero.
- *  beta1 > 0.9 or beta2 > 0.95 (0.999 among them): a code is one of the two next to
+ *  Drawn codes, for beta2 = 0.999 among others: a code is one of the two next to
  *    its value, drawn by a hash of the step's number and the element's index in its
  *    tensor, so that the expected m and v are the values themselves.  Over 3000
  *    steps of normal, constant and 20 times shrinking gradients with beta2 from
@@ -44,11 +44,12 @@ extern "C" {
  *    moments.  A single root strays by 6 to 8% of itself down to a thirtieth of its
  *    block's largest, by 32% at a thousandth; one below 1 / 4032 of it is held as
  *    that much or more.
- *  else: the nearest code, ties to even.  A moment that a step would move by less
- *    than half a place (m 3 to 6%, sqrt(v) 0.8 to 1.6%) stays where it is, so at beta1 =
- *    0.9 and beta2 = 0.95 updates come out 1% too large for normal gradients, and up to
- *    13% too small for ones that hardly change; a beta2 a little above 0.95 takes
- *    the other rounding.
+ *  Nearest codes, ties to even, where beta2 <= 0.95 and 1 - beta2 is between a fifth
+ *    and a half of 1 - beta1 (0.9 and 0.95 among them).  A moment that a step would
+ *    move by less than half a place (m 3 to 6%, sqrt(v) 0.8 to 1.6%) stays where it is, so
+ *    that updates come out 1% too large for normal gradients, and for ones that
+ *    hardly change up to 12% too small (0.9 and 0.95) or too large; any beta2 just
+ *    above 0.95 has drawn codes.
  * Where m is not finite its code is NaN.  Where v is not (g^2 past float32's largest
  * is enough), its code is 255 and its block's v_scale a NaN whose last 8 bits are the
  * biased exponent of the scale that the block's other codes, up to 254, have: such

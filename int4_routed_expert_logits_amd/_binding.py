@@ -909,8 +909,8 @@ def moe_adamw(tensors: AdamWTensors, step, lr: float, beta1: float = 0.9, beta2:
               eps: float = 1e-8, weight_decay: float = 0.0, grad_scale=None, stream=None):
     """One step, in place.  step: device int64 [1], 1 for the first (the caller
     advances it; the parameters and masters count as modified in place, but not by
-    a captured step's replays; the codes of 8-bit moments are drawn by it where beta1 > 0.9 or
-    beta2 > 0.95); grad_scale: device f32 [1] that gradients are multiplied by."""
+    a captured step's replays; the codes of 8-bit moments are drawn by it
+    but for betas like 0.9 and 0.95); grad_scale: device f32 [1] that gradients are multiplied by."""
     fn = "moe_adamw"
     if not _same_memory(*tensors.live):  # 60 ns each: a step over many small ones waits for it
         raise ValueError(f"{fn}: a tensor lies elsewhere than when the list was made")

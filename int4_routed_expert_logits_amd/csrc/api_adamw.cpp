@@ -15,8 +15,6 @@ using moe::aligned;
 
 constexpr int32_t kMaxTensors = 1 << 20;
 constexpr int64_t kMaxElements = int64_t(1) << 40;
-// the betas up to which codes of moments go to the nearest
-constexpr double kNearestBeta1 = 0.9, kNearestBeta2 = 0.95;
 
 moe_status check_tensor(const moe_adamw_tensor& t) {
   if (t.n < 0) return MOE_ERR_SHAPE;
@@ -52,6 +50,14 @@ moe::AdamWTensor get_tensor(const void* tensors, int i) {
   r.wide = aligned(t.p, r.p_bf16 ? 8 : 16) && aligned(t.master, 16) &&
            aligned(t.g, r.g_bf16 ? 8 : 16) && aligned(t.m, state) && aligned(t.v, state);
   return r;
+}
+
+// Whether codes of moments go to the nearest (adamw.hip): v fast enough to fall by
+// such codes, and 2 to 5 times slower than m (0.9 and 0.95 are just that, hence the
+// room for their last places).
+bool nearest_codes(double beta1, double beta2) {
+  const double a = 1.0 - beta1, b = 1.0 - beta2, room = 1.0 + 1e-9;
+  return beta2 <= 0.95 && 2.0 * b <= a * room && a <= 5.0 * b * room;
 }
 
 bool at_least_zero(double v) { return isfinite(v) && v >= 0.0; }
@@ -92,7 +98,7 @@ moe_status moe_adamw(const moe_adamw_tensor* tensors, int32_t n_tensors, const i
   s.rest2 = static_cast<float>(1.0 - beta2);
   s.eps = static_cast<float>(eps);
   s.keep = static_cast<float>(1.0 - lr * weight_decay);
-  s.nearest = beta1 <= kNearestBeta1 && beta2 <= kNearestBeta2;
+  s.nearest = nearest_codes(beta1, beta2);
   return moe::hip_status(moe::launch_adamw(moe::AdamWSource{tensors, get_tensor}, n_tensors, s,
                                            static_cast<hipStream_t>(stream)));
 }

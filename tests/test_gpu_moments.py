@@ -28,12 +28,14 @@ def state(n, store, shift=0):
             new(U8), ones(), ones())
 
 
-@pytest.mark.parametrize("b1,b2", [(0.9, 0.999), (0.9, 0.99), (0.95, 0.95), (0.0, 0.9999)])
+@pytest.mark.parametrize("b1,b2", [(0.9, 0.999), (0.9, 0.99), (0.95, 0.95), (0.0, 0.9999), (0.9, 0.9),
+                                   (0.9, 0.951), (0.5, 0.95), (0.9, 0.95), (0.8, 0.9), (0.5, 0.9)])
 @pytest.mark.parametrize("store,gdt,shift", [("f32", F32, 0), ("master", BF16, 0), ("bf16", F32, 1),
                                             ("f32", BF16, 3)])
 def test_steps_are_the_forms(gpu_lib, store, gdt, shift, b1, b2):
     sizes = [1, 255, 256, 257, 3000]
     say(f"moments {store} {gdt} {shift} {b1} {b2}")
+    drawn = (b1, b2) not in ((0.9, 0.95), (0.8, 0.9), (0.5, 0.9))
     rng = np.random.default_rng(3)
     states = [state(n, store, shift) for n in sizes]
     grads = [torch.zeros(n + shift, dtype=gdt, device="cuda")[shift:] for n in sizes]
@@ -49,7 +51,8 @@ def test_steps_are_the_forms(gpu_lib, store, gdt, shift, b1, b2):
         moe.moe_adamw(q, step, 1e-2, b1, b2, 1e-8, 0.1)
         for i, (p, m, v) in enumerate(want):
             p, m, v, r = ref.adamw32(p, grads[i].float().cpu().numpy(), m, v, t, 1e-2, b1, b2, 1e-8, 0.1)
-            (mc, ms), (vc, vs) = mom.m_codes(m, t), mom.v_codes(r, t)
+            (mc, ms), (vc, vs) = (codes(a, t if drawn else None) for codes, a in
+                                  ((mom.m_codes, m), (mom.v_codes, r)))
             got = states[i]
             new = torch.from_numpy(p)
             if store == "master":
@@ -58,7 +61,7 @@ def test_steps_are_the_forms(gpu_lib, store, gdt, shift, b1, b2):
             assert np.array_equal(got[2].float().cpu().numpy(), mc), (t, i)
             assert np.array_equal(got[3].cpu().numpy(), vc), (t, i)
             assert np.array_equal(got[4].cpu().numpy(), ms) and np.array_equal(got[5].cpu().numpy(), vs)
-            m, v = mom.moments(m, r, t)
+            m, v = mom.m_of(mc, ms), mom.v_of(vc, vs)
             want[i] = (got[0].float().cpu().numpy() if store == "bf16" else p, m, v)
 
 

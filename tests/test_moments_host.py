@@ -38,6 +38,15 @@ def test_nearest_codes_do_not_at_slow_betas():
         assert low < mom.update_ratio(kind, 1500, 0.9, b2, few, nearest) < high, (kind, b2)
 
 
+@pytest.mark.parametrize("b1,b2", [(0.9, 0.95), (0.8, 0.9), (0.8, 0.95), (0.7, 0.94), (0.5, 0.75),
+                                   (0.5, 0.9), (0.0, 0.5), (0.0, 0.8)])
+def test_nearest_codes_where_they_are_kept(b1, b2):
+    """Within an eighth: v falls, and the lags of m and v nearly cancel."""
+    for kind in mom.KINDS:
+        for sizes in SIZES.values():
+            assert abs(mom.update_ratio(kind, 400, b1, b2, sizes, nearest) - 1) < 0.125, kind
+
+
 def test_the_mean_over_steps_is_the_value():
     """Means of N draws of a value between two codes: the standard deviation is half
     their distance over sqrt(N) at most, and six of them are allowed."""
