@@ -255,7 +255,7 @@ __device__ __forceinline__ f32x4_t mma(bf16x8_t w, u32x4_t x, f32x4_t acc) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8_t, x), acc, 0, 0, 0);
 }
 
-// One wavefront's loads of weights: step s of its two fragments.
+// One wavefront's loads of weights: step s of its fragments.
 template <int FR>
 struct Weights {
   const uint8_t* p[FR];  // the fragments' first rows
@@ -364,7 +364,7 @@ __device__ __forceinline__ float both_parts(f32x4_t v, const Lane& ln) {
 
 // ---------------------------------------------------------------------------
 // gate and up: a workgroup takes 8 columns of one expert's h: each wavefront the
-// gate's and the up's rows over an eighth of the contraction.
+// gate's and the up's rows over a quarter of the contraction.
 // ---------------------------------------------------------------------------
 constexpr int kGuFrags = 2;  // the gate's and the up's
 constexpr int kGuWaves = 4, kGuThreads = kGuWaves * kWave;
@@ -476,7 +476,8 @@ __global__ __launch_bounds__(kGuThreads) void few_gate_up(FewLayer g, int tiles)
 static_assert(kGuThreads >= 16 * kCols, "a thread per element of h");
 
 // ---------------------------------------------------------------------------
-// down and combine: a workgroup takes 16 columns of out.  Its wavefronts share the
+// down and combine: a workgroup takes 8 to 32 columns of out, FR fragments (down_plan).
+// Its wavefronts share the
 // steps of all the experts hit evenly, each a contiguous range of them; an
 // expert's sums are left in LDS by the wavefront that begins it, those of a
 // wavefront that begins inside one beside them, and one meeting later they are
@@ -682,6 +683,11 @@ struct DownPlan {
 // short calls too.  us without, with 4 and with 2: 28 tokens over 5 experts of
 // 128 x 3584 104, 48, 38; 26 over 31 of 256 x 640 34 (4 does not split them), 29; 2
 // over 59 of 320 x 704 16 (likewise), 18.
+//
+// On codes with more than 8 tokens the wider layouts do not fit a workgroup's 128
+// registers: bytes of scratch a lane with 3 and 4 fragments 56 and 132 (e4m3, out of
+// f32), 0 and 80 (e4m3, bf16), 12 and 88 (integers, f32), 0 and 12 (integers, bf16).  d
+// above 6144 takes 4, d = 6144 3, long calls on narrower layers 2 to 4.
 constexpr int kMaxSplits = 16, kSplitSteps = 2, kLongSteps = 256, kMaxFrags = 4;
 DownPlan down_plan(int T, int k, int d, int f, int E, bool shared, int step) {
   const int pairs = T * k, cols = d / kCols;

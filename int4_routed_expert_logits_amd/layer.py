@@ -315,9 +315,10 @@ class FewLayerBuffers:
 
 def run_layer_few(x, w_router, bias, experts: FloatExperts, buf: FewLayerBuffers, stream=None):
     """The layer for a few tokens x [T, d] bf16 (T <= 32, T * top_k <= 256) on any
-    of FloatExperts' weights in one call, moe_layer_few: the products read each
-    expert hit once, and x and h are not quantised.  w_router None: buf.topk_idx
-    and buf.topk_w are given."""
+    of FloatExperts' weights in one call, moe_layer_few, and x and h are not
+    quantised.  The faster one up to 8 tokens; beyond, run_layer_float is by up to a
+    tenth where an expert of e4m3 codes has three tokens or more, or d is 8192.
+    w_router None: buf.topk_idx and buf.topk_w are given."""
     sc, ssc = experts.scales or (None, None), experts.shared_scales or (None, None)
     shared = None
     if experts.shared_gate_up is not None:
