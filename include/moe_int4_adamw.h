@@ -54,7 +54,8 @@ extern "C" {
  * is enough), its code is 255 and its block's v_scale a NaN whose last 8 bits are the
  * biased exponent of the scale that the block's other codes, up to 254, have: such
  * an element's parameter is what it is with float32 moments, and no other element
- * changes (its m is held within 448 m_scale and does not count for that).  (A v_scale of any NaN whose last 8 bits are 0 makes the whole block NaN.) */
+ * changes (its m is held within 448 m_scale and does not count for that).  A v_scale
+ * of any NaN whose last 8 bits are 0 makes the whole block NaN. */
 typedef struct {
   int64_t n;
   void* p;

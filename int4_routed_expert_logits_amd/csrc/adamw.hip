@@ -22,35 +22,34 @@
 // How codes are rounded.  A step moves v by (1 - b2)(g'^2 - v) at most and m by
 // (1 - b1)(g' - m); rounded to nearest, a code stays where it is if that is less
 // than half a place, in the next step too, and a moment that should fall or grow
-// slowly never does.  So the codes are rounded up or down with the
-// probability that makes the expected m and the expected v (not its root) the ones
-// rounded, the draw a hash of the step's number and the element's place: the same
-// state gives the same bits, and over steps the errors cancel.  A root's own spread
-// from it is 6 to 8% down to a thirtieth of its block's largest, 10% at a
-// hundredth, 32% at a thousandth.  Norm of the
-// update over the one with float32 moments after 2000 steps (nearest / by the hash,
-// b1 = 0.9; normal gradients, constant ones of mixed sizes, and normal ones 20
-// times smaller after a third):
+// slowly never does.  So the codes are rounded up or down with the probability that
+// makes the expected m and the expected v (not its root) the ones rounded, the draw
+// a hash of the step's number and the element's place: the same state gives the same
+// bits, and over steps the errors cancel.  A root's own spread from it is 6 to 8%
+// down to a thirtieth of its block's largest, 10% at a hundredth, 32% at a
+// thousandth.  Norm of the update over the one with float32 moments after 3000 steps
+// (nearest / by the hash, b1 = 0.9; normal gradients, constant ones of mixed sizes,
+// and normal ones 20 times smaller after a third):
 //   b2 = 0.95   1.01 / 1.00   0.88 / 1.00   1.01 / 1.00
 //   b2 = 0.99   0.61 / 1.01   1.34 / 1.00   0.03 / 1.01
 //   b2 = 0.999  1.49 / 1.01   3.39 / 1.00   0.69 / 1.05
-// Codes go to the nearest, which needs fewer instructions (1375 against 1530 us for 402M
-// elements with masters), where that keeps the norm within 12%: with b2 <= 0.95, so
-// that v falls, and 1 - b2 between a half and a fifth of 1 - b1, where the two moments'
-// lags behind constant gradients nearly cancel (b1 / b2 0.9 / 0.95 0.88 to 0.98, 0.8 / 0.9
-// 0.90 to 0.99, 0.7 / 0.94 1.04 to 1.09, 0.5 / 0.9 1.06 to 1.09; but 0.9 / 0.9 0.79 to 0.88, 0.5 /
-// 0.95 1.13 to 1.21).
+// Codes go to the nearest, which needs fewer instructions (1375 against 1530 us for
+// 402M elements with masters), where that keeps the norm within 12%: with b2 <= 0.95,
+// so that v falls, and 1 - b2 between a half and a fifth of 1 - b1, where the two
+// moments' lags behind constant gradients nearly cancel (b1 / b2 of 0.9 / 0.95: 0.88
+// to 0.98, 0.8 / 0.9: 0.90 to 0.99, 0.7 / 0.94: 1.04 to 1.09, 0.5 / 0.9: 1.06 to 1.09;
+// but 0.9 / 0.9: 0.79 to 0.88, 0.5 / 0.95: 1.13 to 1.21).
 //
 // Bound by memory: 402M elements of bf16 with masters take 2.25 ms (30 bytes each,
 // 5.4 TB/s), with 8-bit moments 1.37 (18 bytes, 5.3 TB/s; 473 vector instructions a
 // wavefront fill the SIMDs beside it), hashed 1.53 (601, which bound it); few
 // elements by the launch and by the betas' powers, which each wavefront computes in
-// double ahead of its data (16 vectors of 6144: 3.6 us).  A wavefront takes one block of 256
-// elements, 4 of each lane: with so many wavefronts in flight, four blocks each before the
-// first is worked on gain nothing (2.26 and 1.41 ms), and starve where there are
-// few (90 odd tensors, 2.9M elements: 28 us, so 17).  The tensors' addresses are
-// kernel arguments, up to 64 tensors a launch: nothing is kept on the device, and
-// a captured launch holds them.
+// double ahead of its data (16 vectors of 6144: 3.6 us).  A wavefront takes one block
+// of 256 elements, 4 of each lane: with so many wavefronts in flight, four blocks
+// each before the first is worked on gain nothing (2.26 and 1.41 ms), and starve
+// where there are few (90 odd tensors, 2.9M elements: 28 us on the GPU, so 17).  The
+// tensors' addresses are kernel arguments, up to 64 tensors a launch: nothing is
+// kept on the device, and a captured launch holds them.
 #include <utility>
 
 #include "common.h"
